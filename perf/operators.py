@@ -1,0 +1,550 @@
+"""Measured cases of the operators around the FP8 linear layer: the norm in
+front of it, and the paged 8-bit key / value cache with the attention that
+reads it.
+
+Operators (formulas: include/fp8lin_block.h)
+  norm       h = x + residual; y = h * rstd * w, rstd = (mean(h^2) + eps)^-1/2;
+             y in E4M3 / E5M2 with one power-of-two scale, or in bf16
+  norm_grad  dx, dw of the norm, the residual's own gradient added
+  append     new keys and values (rotated by their position, with the queries)
+             into the cache, one power-of-two scale for each block and head
+  read       cached keys and values back as bf16
+  attention  queries over the cache, causal, optionally in a window
+
+Shapes are those of GPT-111M (d 768, 12 heads of 64), Llama-2-7B (4096, 32
+heads of 128), 13B (5120, 40 heads) and 70B (8192, 64 query and 8 key heads).
+With `own` false the operators are computed by elementary torch operations in
+fp32; with `own` true by the framework's kernels.
+"""
+import random
+
+import torch
+
+own = False
+
+E4M3, E5M2 = 0, 1
+FLOAT8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+FMT_MAX = (448.0, 57344.0)
+EMAX = (8, 15)          # FMT_MAX = 1.75 * 2^EMAX
+EPS = 1e-5
+NO_SCALE = 126          # cache bias of a block that holds only zeros, and the largest
+
+
+# ------------------------------------------------------------------ cases
+def _norm(name, rows, d, x="fp32", residual="bf16", out="quantize", fmt=E4M3):
+    return {"name": name, "op": "norm", "rows": rows, "d": d, "x": x, "residual": residual, "out": out, "fmt": fmt}
+
+
+def _grad(name, rows, d, dy="fp32", h="bf16", residual=True):
+    return {"name": name, "op": "norm_grad", "rows": rows, "d": d, "dy": dy, "h": h, "residual": residual}
+
+
+def _cache(name, op, batch, q_heads, kv_heads, head_dim, new_lo, new_hi, past_lo, past_hi, block=64, fmt=E4M3,
+           pattern=1, **more):
+    """new_lo..new_hi new tokens a sequence on top of past_lo..past_hi cached ones."""
+    return {"name": name, "op": op, "batch": batch, "q_heads": q_heads, "kv_heads": kv_heads, "head_dim": head_dim,
+            "new_lo": new_lo, "new_hi": new_hi, "past_lo": past_lo, "past_hi": past_hi, "block": block, "fmt": fmt,
+            "pattern": pattern, **more}
+
+
+def listed():
+    return [
+        # one decoded token of the 70B layer: launch latency
+        _norm("norm 70B, 1 token", 1, 8192),
+        # a prompt's 8192 tokens through the 70B layer (the layer-inference workload)
+        _norm("norm 70B, 8192 tokens", 8192, 8192),
+        # the GPT-111M training step's 2048 tokens
+        _grad("norm gradient 111M", 2048, 768),
+        # the 13B backward workload's 4096 tokens, one short of even
+        _grad("norm gradient 13B", 4095, 5120),
+        # a served batch writes one token for each of 64 conversations
+        _cache("append 70B, 64 x 1 token", "append", 64, 64, 8, 128, 1, 1, 17, 8000, x="fp32", rope="halves"),
+        # four prompts of different length enter the 7B cache
+        _cache("append 7B, 4 prompts", "append", 4, 32, 32, 128, 700, 4000, 0, 90, x="fp32", rope="halves"),
+        # a short conversation is read back
+        _cache("read 111M, 3 x 300", "read", 3, 12, 12, 64, 90, 300, 0, 0),
+        # prefixes of eight 70B conversations are read back (to move or re-encode them)
+        _cache("read 70B, 8 x 16384", "read", 8, 64, 8, 128, 9000, 16384, 0, 0),
+        # one token of a single short 7B conversation: latency
+        _cache("attention 7B, 1 x 500", "attention", 1, 32, 32, 128, 1, 1, 500, 500, window=0),
+        # one token for each of 32 ragged 70B conversations
+        _cache("attention 70B, 32 x 8192", "attention", 32, 64, 8, 128, 1, 1, 1000, 8191, window=0),
+        # one token at the end of one very long 70B context
+        _cache("attention 70B, 1 x 131071", "attention", 1, 64, 8, 128, 1, 1, 131070, 131070, window=0),
+        # two prompts, the second half of each on top of its cached first half
+        _cache("attention 70B, prompts", "attention", 2, 64, 8, 128, 1777, 2048, 1500, 2048, window=0),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    """A whole number spread over lo..hi by its logarithm."""
+    return max(lo, min(hi, int(round(lo * (hi / lo) ** rng.random()))))
+
+
+def draw(rng):
+    op = rng.choice(("norm", "norm_grad", "append", "read", "attention", "attention"))
+    if op in ("norm", "norm_grad"):
+        d = rng.choice((768, 1024, 2048, 4096, 5120, 8192, 8 * rng.randint(90, 1024), rng.randint(700, 8191)))
+        rows = _log_int(rng, 1, 8192 if op == "norm" else 4095)
+        if op == "norm":
+            return {**_norm("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32", "none")),
+                            rng.choice(("quantize", "cast", "bf16")), rng.choice((E4M3, E4M3, E5M2)))}
+        return {**_grad("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32")), rng.random() < 0.7)}
+    q_heads, kv_heads, head_dim = rng.choice(((12, 12, 64), (32, 32, 128), (40, 40, 128), (64, 8, 128), (32, 8, 64),
+                                              (16, 1, 128), (16, 4, 256)))
+    common = {"block": rng.choice((16, 32, 64, 64, 128)), "fmt": rng.choice((E4M3, E4M3, E5M2)),
+              "pattern": rng.randint(1, 1 << 20)}
+    shape = ("", op, 1, q_heads, kv_heads, head_dim)
+    token = kv_heads * head_dim          # elements of one cached token's keys
+    if op == "append":
+        if rng.random() < 0.5:
+            batch, new, past = _log_int(rng, 1, 128), rng.randint(1, 5), _log_int(rng, 1, 8000)
+        else:
+            batch, new, past = rng.randint(1, 5), _log_int(rng, 6, 1500), rng.randint(0, 200)
+        c = _cache(*shape, max(1, new // 3), new, past // 3, past, x=rng.choice(("fp32", "bf16")),
+                   rope=rng.choice(("none", "halves", "pairs")), **common)
+    elif op == "read":
+        batch = _log_int(rng, 1, 16)
+        new = _log_int(rng, 1, max(2, 8 * 16384 * 1024 // (token * batch) // 2))
+        c = _cache(*shape, max(1, new // 2), min(new, 30000), 0, 0, **common)
+    else:
+        c = None
+        if rng.random() < 0.6:
+            batch, new = _log_int(rng, 1, 32), rng.choice((1, 1, 1, 2, 4))
+            past = _log_int(rng, 1, max(2, 32 * 4096 * 1024 // (token * batch)))
+            past = min(past, 131000)
+        else:
+            batch, new = rng.randint(1, 3), _log_int(rng, 5, 1600)
+            past = _log_int(rng, 1, 1600)
+        c = _cache(*shape, max(1, new // 2), new, past // 4, past,
+                   window=rng.choice((0, 0, 0, rng.randint(1, 4000))), **common)
+    c["batch"] = batch
+    del c["name"]
+    return c
+
+
+def _drawn_lengths(case):
+    """(new, past) tokens of each sequence: from the case alone."""
+    r = random.Random(case["pattern"])
+    new = [r.randint(case["new_lo"], case["new_hi"]) for _ in range(case["batch"])]
+    past = [r.randint(case["past_lo"], case["past_hi"]) for _ in range(case["batch"])]
+    return new, past
+
+
+# ------------------------------------------------------------------ inputs
+def _dtype(name):
+    return torch.float32 if name == "fp32" else torch.bfloat16
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(g, *shape, std=1.0):
+    return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32).mul_(std)
+
+
+def _activations(g, rows, d):
+    """Rows of unit scale with a few strong columns, as a residual stream has."""
+    x = _normal(g, rows, d)
+    strong = torch.randint(0, d, (max(1, d // 200),), generator=g, device="cuda")
+    x[:, strong] *= 12.0
+    return x
+
+
+def _codes(g, fmt, *shape):
+    """Cache contents: normal values that fill the format to about its maximum."""
+    return _normal(g, *shape, std=FMT_MAX[fmt] / 5.0).clamp_(-FMT_MAX[fmt], FMT_MAX[fmt]).to(FLOAT8[fmt]).view(torch.uint8)
+
+
+def _prepare_cache(case, g):
+    new, past = _drawn_lengths(case)
+    B, H, D, BS, fmt = case["batch"], case["kv_heads"], case["head_dim"], case["block"], case["fmt"]
+    lens = [a + b for a, b in zip(new, past)]
+    used = [-(-n // BS) for n in lens]
+    blocks, width = sum(used) + 3, max(max(used), 1)
+    order = torch.randperm(blocks, generator=g, device="cuda").to(torch.int32).cpu()
+    table, at = torch.zeros(B, width, dtype=torch.int32), 0
+    for i, u in enumerate(used):
+        table[i, :u] = order[at:at + u]
+        at += u
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = EMAX[fmt] - 1    # values of scale about one
+    return {"k": _codes(g, fmt, blocks, H, BS, D), "v": _codes(g, fmt, blocks, H, D, BS),
+            "k_bias": torch.randint(e - 2, e + 1, (blocks, H), generator=g, device="cuda", dtype=torch.int32),
+            "v_bias": torch.randint(e - 2, e + 1, (blocks, H), generator=g, device="cuda", dtype=torch.int32),
+            "cu": i32(cu), "lens": i32(lens), "table": table.cuda(), "tokens": cu[-1], "max_new": max(new),
+            "max_len": max(lens)}
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op = case["op"]
+    s = {"case": case}
+    if op == "norm":
+        rows, d = case["rows"], case["d"]
+        s["x"] = _normal(g, rows, d, std=0.3).to(_dtype(case["x"]))
+        if case["residual"] != "none":
+            s["residual"] = _activations(g, rows, d).to(_dtype(case["residual"]))
+        s["w"] = 1.0 + _normal(g, d, std=0.1)
+        if case["out"] == "cast":     # a scale calibrated beforehand
+            s["bias"] = torch.tensor([EMAX[case["fmt"]] - 5], dtype=torch.int32, device="cuda")
+    elif op == "norm_grad":
+        rows, d = case["rows"], case["d"]
+        s["h"] = _activations(g, rows, d).to(_dtype(case["h"]))
+        s["w"] = 1.0 + _normal(g, d, std=0.1)
+        s["rstd"] = torch.rsqrt(s["h"].double().square().mean(1) + EPS).float()
+        s["dy"] = _normal(g, rows, d, std=1e-2).to(_dtype(case["dy"]))
+        if case["residual"]:
+            s["dh"] = _normal(g, rows, d, std=1e-2).to(_dtype(case["h"]))
+    else:
+        s.update(_prepare_cache(case, g))
+        T, H, Hq, D = s["tokens"], case["kv_heads"], case["q_heads"], case["head_dim"]
+        if op == "append":
+            # the fused query / key / value product's output, one row a token
+            s["qkv"] = _normal(g, T, (Hq + 2 * H) * D).to(_dtype(case["x"]))
+            if case["rope"] != "none":
+                inv = 10000.0 ** (-torch.arange(0, D, 2, device="cuda", dtype=torch.float64) / D)
+                angle = torch.arange(s["max_len"], device="cuda", dtype=torch.float64)[:, None] * inv
+                s["cos"], s["sin"] = angle.cos().float(), angle.sin().float()
+        elif op == "attention":
+            s["q"] = _normal(g, T, Hq, D).to(torch.bfloat16)
+        if own:
+            from fp8_precision_linear_amd import attention as fa
+            s["cache"] = fa.KVCache.from_tensors(s["k"], s["v"], s["k_bias"], s["v_bias"], fmt=case["fmt"])
+            s["batch"] = fa.KVBatch(s["cu"], s["lens"], s["table"], max_new=s["max_new"], max_len=s["max_len"],
+                                    tokens=T)
+            if op == "attention":
+                s["workspace"] = fa.attention_workspace(s["cache"], s["batch"], Hq)
+    return s
+
+
+# ------------------------------------------------------------------ the framework's calls
+def _run_own(s):
+    case = s["case"]
+    op = case["op"]
+    if op == "norm":
+        from fp8_precision_linear_amd import norm
+        if case["out"] == "bf16":
+            y, h, rstd = norm.rmsnorm_fwd(s["x"], s["w"], residual=s.get("residual"), eps=EPS)
+            return {"y": y, "h": h, "rstd": rstd}
+        if case["out"] == "cast":
+            y8, h, rstd = norm.rmsnorm_cast(s["x"], s["w"], s["bias"], case["fmt"], residual=s.get("residual"), eps=EPS)
+            return {"y8": y8.view(FLOAT8[case["fmt"]]), "h": h, "rstd": rstd}
+        y8, bias, amax, h, rstd = norm.rmsnorm_quantize(s["x"], s["w"], case["fmt"], residual=s.get("residual"), eps=EPS)
+        return {"y8": y8.view(FLOAT8[case["fmt"]]), "bias": bias, "amax": amax, "h": h, "rstd": rstd}
+    if op == "norm_grad":
+        from fp8_precision_linear_amd import norm
+        dx, dw = norm.rmsnorm_bwd(s["dy"], s["h"], s["w"], s["rstd"], dh=s.get("dh"))
+        return {"dx": dx, "dw": dw}
+    from fp8_precision_linear_amd import attention as fa
+    if op == "append":
+        q, k, v = _split(s)
+        rope = (s["cos"], s["sin"]) if case["rope"] != "none" else None
+        q_out = fa.kv_append(s["cache"], s["batch"], k, v, q=q, rope=rope, rope_pairs=case["rope"] == "pairs")
+        return _cache_outputs(s, q_out)
+    if op == "read":
+        return fa.kv_read(s["cache"], s["batch"])
+    out, lse = fa.kv_attention(s["cache"], s["batch"], s["q"], window=case["window"], return_lse=True,
+                               workspace=s["workspace"])
+    return {"out": out, "lse": lse}
+
+
+# ------------------------------------------------------------------ plain forms, fp32
+def _split(s):
+    """The query, key and value heads in a row of the fused product."""
+    c = s["case"]
+    T, H, Hq, D = s["tokens"], c["kv_heads"], c["q_heads"], c["head_dim"]
+    x = s["qkv"].view(T, Hq + 2 * H, D)
+    return x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:]
+
+
+def _cache_outputs(s, q):
+    f8 = FLOAT8[s["case"]["fmt"]]
+    return {"q": q, "k": s["k"].view(f8), "v": s["v"].view(f8), "k_bias": s["k_bias"], "v_bias": s["v_bias"]}
+
+
+def _pow2(e):
+    """2^e as fp32, exactly, for whole e in -126..127."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _bias_of(amax, fmt):
+    """The largest whole b with amax * 2^b <= FMT_MAX (amax a normal number)."""
+    m, e = torch.frexp(amax)
+    return EMAX[fmt] - (e - 1) - (m > 0.875).to(torch.int32)
+
+
+def _cast(x, scale, fmt):
+    return (x * scale).clamp(-FMT_MAX[fmt], FMT_MAX[fmt]).to(FLOAT8[fmt]).view(torch.uint8)
+
+
+def _plain_norm(s):
+    case, f32 = s["case"], torch.float32
+    h = s["x"]
+    if "residual" in s:
+        h = (s["x"].to(f32) + s["residual"].to(f32)).to(s["residual"].dtype)
+    hf = h.to(f32)
+    rstd = torch.rsqrt(hf.square().mean(1) + EPS)
+    y = hf * rstd[:, None] * s["w"]
+    if case["out"] == "bf16":
+        return {"y": y.to(torch.bfloat16), "h": h, "rstd": rstd}
+    f8 = FLOAT8[case["fmt"]]
+    if case["out"] == "cast":
+        return {"y8": _cast(y, _pow2(s["bias"]), case["fmt"]).view(f8), "h": h, "rstd": rstd}
+    amax = y.abs().max().reshape(1)
+    bias = _bias_of(amax, case["fmt"])
+    return {"y8": _cast(y, _pow2(bias), case["fmt"]).view(f8), "bias": bias, "amax": amax, "h": h, "rstd": rstd}
+
+
+def _plain_norm_grad(s):
+    f32 = torch.float32
+    dy, r = s["dy"].to(f32), s["rstd"][:, None]
+    xhat = s["h"].to(f32) * r
+    g = dy * s["w"]
+    dx = r * (g - xhat * (g * xhat).mean(1, keepdim=True))
+    if "dh" in s:
+        dx = dx + s["dh"].to(f32)
+    return {"dx": dx.to(s["h"].dtype), "dw": (dy * xhat).sum(0)}
+
+
+def _places(s):
+    """For each new token: its sequence, position, cache block and slot."""
+    BS = s["case"]["block"]
+    cu, lens = s["cu"].long(), s["lens"].long()
+    t = torch.arange(s["tokens"], device="cuda")
+    seq = torch.searchsorted(cu, t, right=True) - 1
+    pos = lens[seq] - cu[seq + 1] + t
+    return seq, pos, s["table"][seq, pos // BS].long(), pos % BS
+
+
+def _rotate(x, pos, s):
+    x = x.to(torch.float32)
+    rope = s["case"]["rope"]
+    if rope == "none":
+        return x
+    c, n = s["cos"][pos][:, None], s["sin"][pos][:, None]
+    if rope == "halves":
+        a, b = x.chunk(2, -1)
+        return torch.cat((a * c - b * n, b * c + a * n), -1)
+    a, b = x[..., 0::2], x[..., 1::2]
+    return torch.stack((a * c - b * n, b * c + a * n), -1).flatten(-2)
+
+
+def _store(x, codes, bias, s, blk, slot, values):
+    """New tokens x [T, H, D] into codes / bias; values: a value cache's layout."""
+    case = s["case"]
+    fmt, BS = case["fmt"], case["block"]
+    f8 = FLOAT8[fmt]
+    nb, H = bias.shape
+    # the largest finite magnitude of the new tokens of each block and head
+    a = torch.where(x.isfinite(), x.abs(), 0.0).amax(2)
+    amax = torch.zeros(nb, H, device="cuda").scatter_reduce(0, blk[:, None].expand(-1, H), a, "amax")
+    b_new = torch.where(amax > 0, _bias_of(amax, fmt), NO_SCALE).clamp(max=NO_SCALE)
+    first = torch.full((nb,), BS, device="cuda").scatter_reduce(0, blk, slot, "amin")  # lowest new slot
+    touched, fresh = (first < BS)[:, None], (first == 0)[:, None]
+    b = torch.where(touched, torch.where(fresh, b_new, torch.minimum(bias, b_new)), bias).to(torch.int32)
+    # tokens that were there in a sequence's first touched block: coded again at the new scale
+    cu, lens, table = s["cu"].long(), s["lens"].long(), s["table"]
+    start = lens - (cu[1:] - cu[:-1])
+    b0 = table.gather(1, (start // BS).clamp(max=table.shape[1] - 1)[:, None])[:, 0].long()
+    at = torch.arange(BS, device="cuda")[None] < (start % BS)[:, None]                 # [B, BS]
+    at = at[:, None, None, :] if values else at[:, None, :, None]
+    old = codes[b0]
+    scaled = _cast(old.view(f8).to(torch.float32), _pow2(b[b0] - bias[b0])[..., None, None], fmt)
+    codes[b0] = torch.where(at, scaled, old)
+    c = _cast(x, _pow2(b[blk])[..., None], fmt)
+    if values:
+        codes[blk, :, :, slot] = c
+    else:
+        codes[blk, :, slot] = c
+    bias.copy_(b)
+
+
+def _plain_append(s):
+    q, k, v = _split(s)
+    _, pos, blk, slot = _places(s)
+    _store(_rotate(k, pos, s), s["k"], s["k_bias"], s, blk, slot, False)
+    _store(v.to(torch.float32), s["v"], s["v_bias"], s, blk, slot, True)
+    return _cache_outputs(s, _rotate(q, pos, s).to(torch.bfloat16))
+
+
+def _plain_read(s):
+    f8 = FLOAT8[s["case"]["fmt"]]
+    _, _, blk, slot = _places(s)
+    k = s["k"][blk, :, slot].view(f8).to(torch.float32) * _pow2(-s["k_bias"][blk])[..., None]
+    v = s["v"][blk, :, :, slot].view(f8).to(torch.float32) * _pow2(-s["v_bias"][blk])[..., None]
+    return k.to(torch.bfloat16), v.to(torch.bfloat16)
+
+
+def _plain_attention(s):
+    case, f32 = s["case"], torch.float32
+    B, H, Hq, D, BS = case["batch"], case["kv_heads"], case["q_heads"], case["head_dim"], case["block"]
+    f8, G, n = FLOAT8[case["fmt"]], Hq // H, s["max_new"]
+    cu, lens, table = s["cu"].long(), s["lens"].long(), s["table"].long()
+    L = table.shape[1] * BS
+    j = torch.arange(L, device="cuda")
+    # [B, blocks, H, BS, D] -> [B, H, L, D]; slots past a sequence's end hold anything
+    k = s["k"][table].view(f8).to(f32) * _pow2(-s["k_bias"][table])[..., None, None]
+    k = k.transpose(1, 2).reshape(B, H, L, D)
+    v = s["v"][table].view(f8).to(f32) * _pow2(-s["v_bias"][table])[..., None, None]
+    v = v.permute(0, 2, 1, 4, 3).reshape(B, H, L, D)
+    v = torch.where((j[None] < lens[:, None])[:, None, :, None], v, 0.0)
+    # queries padded to [B, H, n * G, D]
+    t = torch.arange(n, device="cuda")
+    count = cu[1:] - cu[:-1]
+    row = (cu[:-1, None] + torch.minimum(t[None], count[:, None] - 1)).clamp(min=0)
+    q = s["q"][row].to(f32).view(B, n, H, G, D).transpose(1, 2).reshape(B, H, n * G, D)
+    score = torch.matmul(q, k.transpose(2, 3).contiguous()) * D ** -0.5
+    pos = (lens - count)[:, None] + t[None]                                     # [B, n]
+    see = (j <= pos[..., None]) & (j < lens[:, None, None])
+    if case["window"]:
+        see = see & (j > pos[..., None] - case["window"])
+    see = see[:, None, :, None].expand(B, H, n, G, L).reshape(B, H, n * G, L)
+    score = torch.where(see, score, -torch.inf)
+    m = score.amax(3, keepdim=True).clamp(min=-3e38)
+    p = torch.exp(score - m)
+    total = p.sum(3, keepdim=True)
+    o = torch.matmul(p, v) / torch.where(total > 0, total, 1.0)
+    lse = (m + torch.log(total))[..., 0]
+    seq = torch.searchsorted(cu, torch.arange(s["tokens"], device="cuda"), right=True) - 1
+    i = torch.arange(s["tokens"], device="cuda") - cu[seq]
+    o = o.view(B, H, n, G, D)[seq, :, i].reshape(-1, Hq, D)
+    lse = lse.view(B, H, n, G)[seq, :, i].reshape(-1, Hq)
+    return {"out": o.to(torch.bfloat16), "lse": lse}
+
+
+PLAIN = {"norm": _plain_norm, "norm_grad": _plain_norm_grad, "append": _plain_append, "read": _plain_read,
+         "attention": _plain_attention}
+
+
+def run(state):
+    return _run_own(state) if own else PLAIN[state["case"]["op"]](state)
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+def work(case):
+    op = case["op"]
+    if op in ("norm", "norm_grad"):
+        n = case["rows"] * case["d"]
+        size = lambda t: 0 if t == "none" else 4 if t == "fp32" else 2  # noqa: E731
+        if op == "norm":
+            per = size(case["x"]) + 2 * size(case["residual"]) + (2 if case["out"] == "bf16" else 1)
+            return {"bytes": n * per + 4 * case["d"] + 4 * case["rows"], "flops": 6 * n}
+        per = size(case["dy"]) + size(case["h"]) * (3 if case["residual"] else 2)
+        return {"bytes": n * per + 8 * case["d"] + 4 * case["rows"], "flops": 12 * n}
+    new, past = _drawn_lengths(case)
+    T, H, Hq, D = sum(new), case["kv_heads"], case["q_heads"], case["head_dim"]
+    if op == "append":
+        e = 4 if case["x"] == "fp32" else 2
+        angles = 0 if case["rope"] == "none" else 4 * D * T
+        return {"bytes": T * D * (e * (Hq + 2 * H) + 2 * Hq + 2 * H) + angles, "flops": 6 * T * D * (Hq + 2 * H)}
+    if op == "read":
+        return {"bytes": T * D * H * (2 + 4), "flops": 2 * T * D * H}
+    window = case["window"]
+    pairs = cached = 0
+    for n, p in zip(new, past):
+        cached += n + p if not window else min(n + p, n + window - 1)
+        pairs += sum(min(p + i + 1, window) if window else p + i + 1 for i in range(n))
+    return {"bytes": 2 * cached * H * D + T * Hq * (4 * D + 4), "flops": 4 * pairs * Hq * D}
+
+
+# ------------------------------------------------------------------ the definitions in 64 bits
+_VALUES = {}
+
+
+def _value_table(fmt):
+    """The 256 values of a format, from its bit fields."""
+    if fmt not in _VALUES:
+        mant, off = (3, 7) if fmt == E4M3 else (2, 15)
+        out = []
+        for c in range(256):
+            e, f = (c & 0x7F) >> mant, c & ((1 << mant) - 1)
+            v = f * 2.0 ** (1 - off - mant) if e == 0 else (1 + f / (1 << mant)) * 2.0 ** (e - off)
+            if fmt == E4M3 and (c & 0x7F) == 0x7F or fmt == E5M2 and e == 31 and f:
+                v = float("nan")
+            elif fmt == E5M2 and e == 31:
+                v = float("inf")
+            out.append(-v if c & 0x80 else v)
+        _VALUES[fmt] = torch.tensor(out, dtype=torch.float64, device="cuda")
+    return _VALUES[fmt]
+
+
+def _sequence(s, i, codes, bias, values):
+    """Cached keys or values of sequence i: [H, len, D] in fp64."""
+    fmt, BS = s["case"]["fmt"], s["case"]["block"]
+    n = int(s["lens"][i])
+    blocks = s["table"][i, : -(-n // BS)].long()
+    x = _value_table(fmt)[codes[blocks].long()] * torch.pow(2.0, -bias[blocks].double())[..., None, None]
+    x = x.transpose(2, 3) if values else x
+    return x.transpose(0, 1).reshape(x.shape[1], -1, x.shape[3])[:, :n]
+
+
+def exact(case, seed):
+    """Results from the definitions in fp64, sequence by sequence.  The codes,
+    scales and rotated keys of the cache have no value of their own here
+    (None): they are roundings of the inputs, equal on both sides."""
+    s = prepare(case, seed)
+    op, f64 = case["op"], torch.float64
+    if op == "norm":
+        h = s["x"].to(f64)
+        if "residual" in s:
+            h = (h + s["residual"].to(f64)).to(torch.float32).to(s["residual"].dtype).to(f64)
+        rstd = (h.pow(2).sum(1) / case["d"] + EPS).pow(-0.5)
+        y = h * rstd[:, None] * s["w"].to(f64)
+        out = {"h": None, "rstd": rstd}
+        if case["out"] == "bf16":
+            return {**out, "y": y}
+        if case["out"] == "cast":
+            return {**out, "y8": y * 2.0 ** int(s["bias"])}
+        amax = y.abs().max().reshape(1)
+        top, b = float(amax), 0
+        while top * 2.0 ** (b + 1) <= FMT_MAX[case["fmt"]]:
+            b += 1
+        while top * 2.0 ** b > FMT_MAX[case["fmt"]]:
+            b -= 1
+        return {**out, "y8": y * 2.0 ** b, "amax": amax, "bias": None}
+    if op == "norm_grad":
+        dy, h, w, r = (s[k].to(f64) for k in ("dy", "h", "w", "rstd"))
+        g = dy * w
+        dot = (g * h).sum(1)
+        dx = r[:, None] * g - h * (r ** 3 * dot / case["d"])[:, None]
+        return {"dx": dx + s["dh"].to(f64) if "dh" in s else dx, "dw": torch.mv((dy * h).t(), r)}
+    if op == "append":
+        if case["rope"] == "none":
+            return {"q": _split(s)[0].to(f64), "k": None, "v": None, "k_bias": None, "v_bias": None}
+        _, pos, _, _ = _places(s)
+        q = _split(s)[0].to(f64)
+        T, Hq, D = q.shape
+        z = torch.complex(*((q[..., : D // 2], q[..., D // 2:]) if case["rope"] == "halves"
+                            else (q[..., 0::2], q[..., 1::2])))
+        z = z * torch.complex(s["cos"].to(f64), s["sin"].to(f64))[pos][:, None]
+        q = torch.cat((z.real, z.imag), -1) if case["rope"] == "halves" else torch.view_as_real(z).flatten(-2)
+        return {"q": q, "k": None, "v": None, "k_bias": None, "v_bias": None}
+    new, past = _drawn_lengths(case)
+    if op == "read":
+        ks, vs = [], []
+        for i in range(case["batch"]):
+            ks.append(_sequence(s, i, s["k"], s["k_bias"], False).transpose(0, 1)[past[i]:])
+            vs.append(_sequence(s, i, s["v"], s["v_bias"], True).transpose(0, 1)[past[i]:])
+        return torch.cat(ks), torch.cat(vs)
+    outs, lses = [], []
+    H, Hq, D = case["kv_heads"], case["q_heads"], case["head_dim"]
+    for i in range(case["batch"]):
+        n, p = new[i], past[i]
+        k = _sequence(s, i, s["k"], s["k_bias"], False).repeat_interleave(Hq // H, 0)
+        v = _sequence(s, i, s["v"], s["v_bias"], True).repeat_interleave(Hq // H, 0)
+        q = s["q"][int(s["cu"][i]):int(s["cu"][i]) + n].to(f64).transpose(0, 1)        # [Hq, n, D]
+        at = p + torch.arange(n, device="cuda")[:, None]
+        j = torch.arange(n + p, device="cuda")[None]
+        hide = (j > at) | ((j <= at - case["window"]) if case["window"] else (j < 0))
+        score = (torch.matmul(q, k.transpose(1, 2).contiguous()) / D ** 0.5).masked_fill_(hide, -torch.inf)
+        lse = torch.logsumexp(score, 2)
+        outs.append(torch.matmul(torch.exp(score - lse[..., None]), v).transpose(0, 1))
+        lses.append(lse.transpose(0, 1))
+    return {"out": torch.cat(outs), "lse": torch.cat(lses)}
