@@ -87,9 +87,12 @@ def draw(rng):
         d = rng.choice((768, 1024, 2048, 4096, 5120, 8192, 8 * rng.randint(90, 1024), rng.randint(700, 8191)))
         rows = _log_int(rng, 1, 8192 if op == "norm" else 4095)
         if op == "norm":
-            return {**_norm("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32", "none")),
-                            rng.choice(("quantize", "cast", "bf16")), rng.choice((E4M3, E4M3, E5M2)))}
-        return {**_grad("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32")), rng.random() < 0.7)}
+            c = _norm("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32", "none")),
+                      rng.choice(("quantize", "cast", "bf16")), rng.choice((E4M3, E4M3, E5M2)))
+        else:
+            c = _grad("", rows, d, rng.choice(("fp32", "bf16")), rng.choice(("bf16", "fp32")), rng.random() < 0.7)
+        del c["name"]
+        return c
     q_heads, kv_heads, head_dim = rng.choice(((12, 12, 64), (32, 32, 128), (40, 40, 128), (64, 8, 128), (32, 8, 64),
                                               (16, 1, 128), (16, 4, 256)))
     common = {"block": rng.choice((16, 32, 64, 64, 128)), "fmt": rng.choice((E4M3, E4M3, E5M2)),
