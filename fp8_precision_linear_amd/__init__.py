@@ -11,7 +11,10 @@ activations) or E5M2 (gradients) -> FP8 matmul, unscaled afterwards.
 
 Layers built on these calls: ``fp8_precision_linear_amd.linear`` (FP8Linear,
 the layer with current or delayed scaling) and ``fp8_precision_linear_amd.mlp``
-(the chained FP8 MLP with SwiGLU).
+(the chained FP8 MLP with SwiGLU).  The operators around them:
+``fp8_precision_linear_amd.norm`` (RMS norm with the residual's addition and
+FP8 output), ``fp8_precision_linear_amd.attention`` (the paged FP8 cache and
+attention over it), run together by ``fp8_precision_linear_amd.decoder``.
 
 Importing this module loads the library and raises ImportError if it is not
 built; build it with ``python fp8_precision_linear_amd/build.py``.
@@ -40,7 +43,7 @@ MATH_EXACT, MATH_NATIVE_FP8 = 0, 1
 OP_FWD, OP_DGRAD, OP_WGRAD = 0, 1, 2
 
 # Exported symbols and their C signatures (include/fp8lin.h).
-_vp, _i64, _i32, _ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+_vp, _i64, _i32, _ci, _cf = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "fp8_status_string": (ctypes.c_char_p, [_ci]),
     "fp8_amax": (_ci, [_vp, _ci, _i64, _vp, _vp]),
@@ -63,6 +66,17 @@ SIGNATURES = {
     "fp8_scaled_gemm_wgrad": (_ci, [_vp, _ci, _vp, _vp, _ci, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp8_swiglu_fwd": (_ci, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "fp8_swiglu_bwd": (_ci, [_vp, _vp, _i64, _i64, _vp, _vp, _vp]),
+    # include/fp8lin_block.h
+    "fp8_rmsnorm_fwd": (_ci, [_vp, _ci, _vp, _ci, _vp, _ci, _i64, _i64, _cf, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_rmsnorm_cast": (_ci, [_vp, _ci, _vp, _ci, _vp, _ci, _i64, _i64, _cf, _vp, _vp, _vp, _ci, _vp, _vp, _vp]),
+    "fp8_rmsnorm_quantize": (_ci, [_vp, _ci, _vp, _ci, _vp, _ci, _i64, _i64, _cf, _vp, _vp, _ci, _i32, _vp, _vp, _vp,
+                                   _vp, _vp]),
+    "fp8_rmsnorm_bwd_workspace_bytes": (_i64, [_i64, _i64]),
+    "fp8_rmsnorm_bwd": (_ci, [_vp, _ci, _vp, _ci, _vp, _ci, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_kv_append": (_ci, [_vp, _vp, _vp, _i64, _vp, _i64, _ci, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _vp]),
+    "fp8_kv_read": (_ci, [_vp, _vp, _ci, _vp, _vp, _vp]),
+    "fp8_kv_attention_workspace_bytes": (_i64, [_vp, _vp, _i32]),
+    "fp8_kv_attention": (_ci, [_vp, _vp, _vp, _i64, _i32, _cf, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
 }
 
 

@@ -16,6 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8lin.so")
 SOURCES = ["quant.hip", "gemm_fwd.hip", "gemm_dgrad.hip", "gemm_wgrad.hip", "gemm_group.hip", "swiglu.hip",
+           "norm_fwd.hip", "norm_bwd.hip", "kv_cache.hip", "kv_attention.hip", "attn_rows.hip", "attn_tile.hip",
            "capi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,210 @@
+// What the attention kernels over the paged FP8 cache share.
+//
+//   t_j = scale * log2(e) * 2^-kb * (q . k8_j)          logits in base 2
+//   p_j = 2^(t_j - m)          m: running reference of the row
+//   l = sum p_j,  O = sum p_j v8_j 2^-vb,  out = O / l,  lse = ln 2 (m + log2 l)
+//
+// kb, vb: the key and value bias of token j's block and head.  Blocks hold a
+// multiple of 16 tokens, so a "granule" of 16 aligned tokens has one block and
+// one bias of each kind.
+//
+// Products.  S^T = K Q^T and O^T = V^T P^T, so that a lane owns one query row
+// from the logits to the output: its row statistics need one or two cross-lane
+// steps, and the probabilities it holds are already the B operand of the
+// second product.  Which token a row of S^T's A operand stands for, and which
+// dimension a slot of its contraction, is free as long as both operands agree:
+// they are chosen so that every lane's A operand of either product is 16
+// consecutive bytes of the cache (a token's 16 dimensions of K; a dimension's
+// 16 tokens of V, which the cache holds transposed).  Nothing is shuffled or
+// transposed on the way.
+//
+// Arithmetic.  Keys widen exactly to bf16, the queries' type; products and
+// sums of the 16-bit MFMA are fp32.  Values widen to fp16, scaled by
+// 2^(bref - vb + kHead) in the conversion itself, where bref is the smallest
+// value bias met so far (O is rescaled when it drops): the largest values sit
+// at the top of fp16's range, so a value loses bits only 2^30 below them.
+// Probabilities are fp16 scaled by 2^kShift relative to the reference: 11 bits
+// down to 2^-22 of the largest, against bf16's 8 bits.  The reference follows
+// the row maximum lazily: it moves only when a logit exceeds it by
+// kShift - 1, so that most tiles rescale nothing and p stays below 2^15.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_device.h"
+
+namespace fp8lin {
+
+struct AttnArgs {
+  fp8_kv_cache_t cache;
+  fp8_kv_batch_t batch;
+  const uint16_t* q;
+  int64_t q_stride;
+  int q_heads;
+  int group;        // query heads per key head
+  float scale_log2;
+  int causal, window;
+  uint16_t* out;
+  float* lse;
+  float* part_o;    // [splits][tokens][q_heads][D], normalised
+  float* part_lse;  // [splits][tokens][q_heads], base 2
+  int chunk;        // keys per split, a multiple of kAttnTile
+  int splits;       // most chunks of any row tile
+  int row_tiles;    // most row tiles of any sequence
+};
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+constexpr int kAttnTile = 64;          // keys per step
+constexpr float kShift = 8.0f;
+constexpr float kLazy = 15.0f;         // rescale when t > m + kLazy (m includes the shift)
+constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
+constexpr int kNoBias = 1 << 20;       // value bias before the first block
+template <int FMT>
+constexpr int kHead = FMT == FP8_E4M3 ? 7 : 0;  // 448 * 2^7 and 57344 both fit fp16
+
+// A workgroup's place: workgroups that read the same keys differ by a multiple
+// of the head count in their index, and the last row tiles (which see the most
+// keys) come first.
+struct AttnPlace {
+  int head, split, seq, row_tile;
+};
+__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a) {
+  AttnPlace p;
+  uint32_t x = blockIdx.x;
+  p.head = x % a.cache.heads;
+  x /= a.cache.heads;
+  p.split = x % a.splits;
+  x /= a.splits;
+  p.seq = x % a.batch.batch;
+  p.row_tile = a.row_tiles - 1 - (int)(x / a.batch.batch);
+  return p;
+}
+
+// The keys a tile of rows [row0, row0 + count) of sequence s reads, and its
+// chunks; rows run over (token, head of the group).
+struct AttnSpan {
+  int lo, hi, chunks;
+};
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const KVSeq& s, int row0, int count) {
+  const int last = min(row0 + count, s.n * a.group) - 1;
+  AttnSpan p;
+  p.hi = a.causal ? min(s.len, s.start + last / a.group + 1) : s.len;
+  p.lo = a.window ? max(0, s.start + row0 / a.group - a.window + 1) & ~(kAttnTile - 1) : 0;
+  p.chunks = max(1, (p.hi - p.lo + a.chunk - 1) / a.chunk);
+  return p;
+}
+
+// 2^e as a float for the conversions' scale operand, e clamped to normals.
+__device__ __forceinline__ float pow2_scale(int e) {
+  return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23);
+}
+
+// 8 codes -> 8 bf16, exactly.
+template <int FMT>
+__device__ __forceinline__ v8b widen_bf16(uint32_t c0, uint32_t c1) {
+  v2b r[4];
+  if constexpr (FMT == FP8_E4M3) {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, false);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, 1.0f, true);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true);
+  } else {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c0, 1.0f, false);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c0, 1.0f, true);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c1, 1.0f, false);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c1, 1.0f, true);
+  }
+  return v8b{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+// 8 codes -> 8 fp16 of value * scale (a power of two).
+template <int FMT>
+__device__ __forceinline__ v8h widen_f16(uint32_t c0, uint32_t c1, float scale) {
+  v2h r[4];
+  if constexpr (FMT == FP8_E4M3) {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c0, scale, false);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c0, scale, true);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c1, scale, false);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c1, scale, true);
+  } else {
+    r[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c0, scale, false);
+    r[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c0, scale, true);
+    r[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c1, scale, false);
+    r[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c1, scale, true);
+  }
+  return v8h{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+__device__ __forceinline__ v8h pack_f16(const float* p) {
+  v2h r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = __builtin_convertvector((v2f{p[2 * e], p[2 * e + 1]}), v2h);
+  return v8h{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2b));
+}
+
+// 0xFF in every byte of w that holds a NaN (or, in E5M2, infinity) code.
+template <int FMT>
+__device__ __forceinline__ uint32_t bad_bytes(uint32_t w) {
+  const uint32_t top = (((w & 0x7F7F7F7Fu) + (FMT == FP8_E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u) >> 7;
+  return top * 0xFFu;
+}
+
+// 1.0 where the byte is set, as fp16.
+__device__ __forceinline__ v8h ones_f16(uint32_t m0, uint32_t m1) {
+  v8h r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    r[e] = (m0 >> (8 * e)) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
+    r[4 + e] = (m1 >> (8 * e)) & 1u ? (_Float16)1.0f : (_Float16)0.0f;
+  }
+  return r;
+}
+
+// Reductions over the lanes that share a query row: l ^ 32, and l ^ 16.
+__device__ __forceinline__ float swap32_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float swap16_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float swap32_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap16_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ int swap32_min(int v) {
+  const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  return min((int)r[0], (int)r[1]);
+}
+__device__ __forceinline__ int swap16_min(int v) {
+  const auto r = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  return min((int)r[0], (int)r[1]);
+}
+
+}  // namespace
+
+// Launchers (attn_rows.hip, attn_tile.hip).  The rows kernel takes row tiles of
+// 16 * row_blocks rows (1 or 2; 1 for head_dim 256), the tile kernel of 128.
+constexpr int kAttnTileRows = 128;
+hipError_t launch_attn_rows(const AttnArgs& a, int row_blocks, uint32_t groups, hipStream_t stream);
+hipError_t launch_attn_tile(const AttnArgs& a, uint32_t groups, hipStream_t stream);
+
+}  // namespace fp8lin

@@ -3,6 +3,7 @@
 // per-device "is this gfx950" flag and the per-device address of the static
 // scratch that fp8_scaled_gemm_noalloc uses.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "internal.h"
@@ -92,6 +93,48 @@ int quantize_checks(const void* x, int dtype, int64_t n, int fmt, int32_t margin
   if (n > 0 && (misaligned(x) || misaligned(y))) return FP8_ERR_ALIGN;
   return FP8_OK;
 }
+
+// The checks that the norm's forward entry points share.
+int norm_checks(const void* x, int x_dtype, const void* r, int r_dtype, const void* w, int w_dtype, int64_t rows,
+                int64_t d, const void* h, const float* rstd, const void* y) {
+  if (rows < 0 || rows > (int64_t)0x7FFFFFFF || d < 1) return FP8_ERR_SIZE;
+  if (d > (d % 4 == 0 ? fp8lin::kNormMaxD : fp8lin::kNormMaxOddD)) return FP8_ERR_SIZE;
+  if (bad_dtype(x_dtype) || bad_dtype(w_dtype) || (r && bad_dtype(r_dtype))) return FP8_ERR_DTYPE;
+  if (rows > 0 && (!x || !w || !y || (r && !h))) return FP8_ERR_NULL;
+  if (rows > 0 && (misaligned(x) || misaligned(w) || misaligned(y))) return FP8_ERR_ALIGN;
+  if (rows > 0 && r && (misaligned(r) || misaligned(h))) return FP8_ERR_ALIGN;
+  if (misaligned_word(rstd)) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+
+// A cache's and a batch's host-side fields (no device call).
+int kv_checks(const fp8_kv_cache_t* c, const fp8_kv_batch_t* b) {
+  if (!c || !b) return FP8_ERR_NULL;
+  if (c->num_blocks < 1 || c->heads < 1) return FP8_ERR_SIZE;
+  if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128) return FP8_ERR_SIZE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FP8_ERR_SIZE;
+  if (bad_operand_format(c->fmt)) return FP8_ERR_FORMAT;
+  if (b->batch < 0 || b->table_width < 0 || b->tokens < 0 || b->max_new < 0 || b->max_len < 0) return FP8_ERR_SIZE;
+  if (b->max_len > (1 << 30) || b->max_len > (int64_t)b->table_width * c->block_size) return FP8_ERR_SIZE;
+  if (b->batch == 0 || b->tokens == 0 || b->max_new == 0) return FP8_OK;  // nothing to do
+  if (!c->k || !c->v || !c->k_bias || !c->v_bias || !b->cu_tokens || !b->lens || (b->table_width > 0 && !b->block_table))
+    return FP8_ERR_NULL;
+  if (misaligned(c->k) || misaligned(c->v)) return FP8_ERR_ALIGN;
+  if (misaligned_word(c->k_bias) || misaligned_word(c->v_bias) || misaligned_word(b->cu_tokens) ||
+      misaligned_word(b->lens) || misaligned_word(b->block_table))
+    return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+
+// Rows of packed heads, `stride` elements of `bytes` each apart.
+int rows_checks(const void* p, int64_t stride, int64_t heads, int64_t head_dim, int bytes) {
+  if (!p) return FP8_ERR_NULL;
+  if (stride < heads * head_dim || stride > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  if (misaligned(p) || (stride * bytes) % 16 != 0) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+
+bool kv_empty(const fp8_kv_batch_t* b) { return b->batch == 0 || b->tokens == 0 || b->max_new == 0; }
 
 }  // namespace
 
@@ -480,6 +523,136 @@ int fp8_swiglu_bwd(const float* h, const float* da, int64_t rows, int64_t f, uin
   return hip_status(fp8lin::launch_swiglu_bwd(h, da, rows, f, dh,
                                               reinterpret_cast<uint32_t*>(out_amax),
                                               (hipStream_t)stream));
+}
+
+int fp8_rmsnorm_fwd(const void* x, fp8_dtype_t x_dtype, const void* residual, fp8_dtype_t r_dtype, const void* w,
+                    fp8_dtype_t w_dtype, int64_t rows, int64_t d, float eps, void* h, float* rstd, uint16_t* y,
+                    float* y_amax, void* stream) {
+  int st = norm_checks(x, x_dtype, residual, r_dtype, w, w_dtype, rows, d, h, rstd, y);
+  if (st == FP8_OK && misaligned_word(y_amax)) st = FP8_ERR_ALIGN;
+  if (st != FP8_OK || (rows == 0 && !y_amax)) return st;
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::NormProblem p{x, (int)x_dtype, residual, (int)r_dtype, w, (int)w_dtype, rows, d, eps, h, rstd};
+  return hip_status(fp8lin::launch_norm_fwd(p, y, reinterpret_cast<uint32_t*>(y_amax), (hipStream_t)stream));
+}
+
+int fp8_rmsnorm_cast(const void* x, fp8_dtype_t x_dtype, const void* residual, fp8_dtype_t r_dtype, const void* w,
+                     fp8_dtype_t w_dtype, int64_t rows, int64_t d, float eps, void* h, float* rstd,
+                     const int32_t* bias, fp8_format_t fmt, uint8_t* y, float* y_amax, void* stream) {
+  int st = norm_checks(x, x_dtype, residual, r_dtype, w, w_dtype, rows, d, h, rstd, y);
+  if (st != FP8_OK) return st;
+  if (bad_operand_format(fmt)) return FP8_ERR_FORMAT;
+  if (!bias) return FP8_ERR_NULL;
+  if (misaligned_word(bias) || misaligned_word(y_amax)) return FP8_ERR_ALIGN;
+  if (rows == 0 && !y_amax) return FP8_OK;
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::NormProblem p{x, (int)x_dtype, residual, (int)r_dtype, w, (int)w_dtype, rows, d, eps, h, rstd};
+  return hip_status(
+      fp8lin::launch_norm_cast(p, bias, fmt, y, reinterpret_cast<uint32_t*>(y_amax), (hipStream_t)stream));
+}
+
+int fp8_rmsnorm_quantize(const void* x, fp8_dtype_t x_dtype, const void* residual, fp8_dtype_t r_dtype, const void* w,
+                         fp8_dtype_t w_dtype, int64_t rows, int64_t d, float eps, void* h, float* rstd,
+                         fp8_format_t fmt, int32_t margin, uint8_t* y, float* row_amax, float* amax, int32_t* bias,
+                         void* stream) {
+  int st = norm_checks(x, x_dtype, residual, r_dtype, w, w_dtype, rows, d, h, rstd, y);
+  if (st != FP8_OK) return st;
+  if (bad_operand_format(fmt)) return FP8_ERR_FORMAT;
+  if (margin > FP8_MAX_MARGIN || margin < -FP8_MAX_MARGIN) return FP8_ERR_MARGIN;
+  if (!amax || !bias || (rows > 0 && (!rstd || !row_amax))) return FP8_ERR_NULL;
+  if (misaligned_word(amax) || misaligned_word(bias) || misaligned_word(row_amax)) return FP8_ERR_ALIGN;
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::NormProblem p{x, (int)x_dtype, residual, (int)r_dtype, w, (int)w_dtype, rows, d, eps, h, rstd};
+  return hip_status(fp8lin::launch_norm_quantize(p, fmt, margin, y, reinterpret_cast<uint32_t*>(row_amax),
+                                                 reinterpret_cast<uint32_t*>(amax), bias, (hipStream_t)stream));
+}
+
+int64_t fp8_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t d) {
+  if (rows < 0 || rows > (int64_t)0x7FFFFFFF || d < 1) return FP8_ERR_SIZE;
+  if (d > (d % 4 == 0 ? fp8lin::kNormMaxD : fp8lin::kNormMaxOddD)) return FP8_ERR_SIZE;
+  return fp8lin::norm_bwd_workspace_bytes(rows, d);
+}
+
+int fp8_rmsnorm_bwd(const void* dy, fp8_dtype_t dy_dtype, const void* h, fp8_dtype_t h_dtype, const void* w,
+                    fp8_dtype_t w_dtype, const float* rstd, const void* dh, int64_t rows, int64_t d, void* dx,
+                    float* dw, float* dx_amax, void* ws, int64_t ws_bytes, void* stream) {
+  const int64_t need = fp8_rmsnorm_bwd_workspace_bytes(rows, d);
+  if (need < 0) return (int)need;
+  if (bad_dtype(dy_dtype) || bad_dtype(h_dtype) || bad_dtype(w_dtype)) return FP8_ERR_DTYPE;
+  if (!dw || (rows > 0 && (!dy || !h || !w || !rstd || !dx || !ws))) return FP8_ERR_NULL;
+  if (misaligned_word(rstd) || misaligned_word(dx_amax) || misaligned(dw)) return FP8_ERR_ALIGN;
+  if (rows > 0 && (misaligned(dy) || misaligned(h) || misaligned(w) || misaligned(dh) || misaligned(dx) ||
+                   misaligned(ws)))
+    return FP8_ERR_ALIGN;
+  if (ws_bytes < need) return FP8_ERR_SIZE;
+  const int st = device_ok();
+  if (st != FP8_OK) return st;
+  return hip_status(fp8lin::launch_norm_bwd(dy, dy_dtype, h, h_dtype, w, w_dtype, rstd, dh, rows, d, dx, dw,
+                                            reinterpret_cast<uint32_t*>(dx_amax), static_cast<float*>(ws),
+                                            (hipStream_t)stream));
+}
+
+int fp8_kv_append(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, const void* k, int64_t k_stride,
+                  const void* v, int64_t v_stride, fp8_dtype_t dtype, const void* q, int64_t q_stride,
+                  int32_t q_heads, uint16_t* q_out, const float* cos, const float* sin, int32_t rope_rows,
+                  int32_t rope_pairs, void* stream) {
+  int st = kv_checks(cache, batch);
+  if (st != FP8_OK) return st;
+  if (bad_dtype(dtype)) return FP8_ERR_DTYPE;
+  if (q && q_heads < 1) return FP8_ERR_SIZE;
+  if (!cos != !sin) return FP8_ERR_NULL;
+  if (cos && rope_rows < batch->max_len) return FP8_ERR_SIZE;
+  if (kv_empty(batch)) return FP8_OK;
+  const int bytes = dtype == FP8_IN_FP32 ? 4 : 2;
+  if ((st = rows_checks(k, k_stride, cache->heads, cache->head_dim, bytes)) != FP8_OK) return st;
+  if ((st = rows_checks(v, v_stride, cache->heads, cache->head_dim, bytes)) != FP8_OK) return st;
+  if (q) {
+    if ((st = rows_checks(q, q_stride, q_heads, cache->head_dim, bytes)) != FP8_OK) return st;
+    if (!q_out) return FP8_ERR_NULL;
+    if (misaligned(q_out)) return FP8_ERR_ALIGN;
+  }
+  if (misaligned(cos) || misaligned(sin)) return FP8_ERR_ALIGN;
+  if (fp8lin::kv_append_groups(*cache, *batch, q != nullptr) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  if ((st = device_ok()) != FP8_OK) return st;
+  return hip_status(fp8lin::launch_kv_append(*cache, *batch, k, k_stride, v, v_stride, dtype, q, q_stride, q_heads,
+                                             q_out, cos, sin, rope_rows, rope_pairs, (hipStream_t)stream));
+}
+
+int fp8_kv_read(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, fp8_dtype_t out_dtype, void* k_out,
+                void* v_out, void* stream) {
+  int st = kv_checks(cache, batch);
+  if (st != FP8_OK) return st;
+  if (bad_dtype(out_dtype)) return FP8_ERR_DTYPE;
+  if (misaligned(k_out) || misaligned(v_out)) return FP8_ERR_ALIGN;
+  if (kv_empty(batch) || (!k_out && !v_out)) return FP8_OK;
+  if (fp8lin::kv_append_groups(*cache, *batch, false) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  if ((st = device_ok()) != FP8_OK) return st;
+  return hip_status(fp8lin::launch_kv_read(*cache, *batch, out_dtype, k_out, v_out, (hipStream_t)stream));
+}
+
+int64_t fp8_kv_attention_workspace_bytes(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, int32_t q_heads) {
+  const int st = kv_checks(cache, batch);
+  if (st != FP8_OK) return st;
+  if (q_heads < 1 || q_heads % cache->heads != 0) return FP8_ERR_SIZE;
+  if (kv_empty(batch)) return 0;
+  return fp8lin::kv_attention_workspace_bytes(*cache, *batch, q_heads);
+}
+
+int fp8_kv_attention(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, const uint16_t* q, int64_t q_stride,
+                     int32_t q_heads, float scale, int32_t causal, int32_t window, uint16_t* out, float* lse, void* ws,
+                     int64_t ws_bytes, void* stream) {
+  const int64_t need = fp8_kv_attention_workspace_bytes(cache, batch, q_heads);
+  if (need < 0) return (int)need;
+  if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
+  if (kv_empty(batch)) return FP8_OK;
+  int st = rows_checks(q, q_stride, q_heads, cache->head_dim, 2);
+  if (st != FP8_OK) return st;
+  if (!out || (need > 0 && !ws)) return FP8_ERR_NULL;
+  if (misaligned(out) || misaligned_word(lse) || misaligned(ws)) return FP8_ERR_ALIGN;
+  if (ws_bytes < need) return FP8_ERR_SIZE;
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::AttnProblem p{*cache, *batch, q, q_stride, q_heads, scale, causal, window, out, lse};
+  return hip_status(fp8lin::launch_kv_attention(p, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

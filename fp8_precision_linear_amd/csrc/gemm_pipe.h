@@ -47,6 +47,7 @@
 #pragma once
 
 #include "gemm_kernel.h"
+#include "lds_dma.h"
 
 namespace fp8lin {
 namespace gemm_detail {
@@ -55,14 +56,6 @@ constexpr int kPipeBK = 64;     // contraction bytes per stage
 constexpr int kPipeStages = 4;  // ring depth
 
 typedef int v2i __attribute__((ext_vector_type(2)));
-
-// s_waitcnt with only vmcnt constrained (gfx9 encoding: vmcnt bits [3:0] and
-// [15:14], expcnt [6:4] = 7 and lgkmcnt [11:8] = 15 mean "no wait").
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
 
 // s_waitcnt lgkmcnt(0) only: every LDS read this wave issued has returned.
 __device__ __forceinline__ void wait_lgkm0() {
@@ -77,10 +70,6 @@ __device__ __forceinline__ void wait_stages(int younger) {
   else if (younger == 1) wait_vmcnt<D>();
   else wait_vmcnt<0>();
 }
-
-// A bare barrier: no memory access may move across it (asm "memory" clobber),
-// and it waits for nothing the explicit waits did not.
-__device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 // Chunk swizzles of the K-major and MN-major stage tiles.
 __device__ __forceinline__ int kswz(int r) { return (r >> 2) & 3; }
@@ -102,27 +91,6 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 __device__ __forceinline__ int64_t opaque64(int64_t x) {
   asm volatile("" : "+v"(x));
   return x;
-}
-
-// LDS byte address of a __shared__ object.
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) const void*)p);
-}
-
-// One LDS-DMA load: 16 bytes per lane from `src` into LDS at
-// `lds_kb + 16 * lane` (lds_kb: the wave-uniform LDS byte address of the
-// destination KB).  Issued from inline assembly so that the compiler does not
-// treat it as a write it must wait for before every later LDS read: the ring
-// protocol waits for it explicitly (wait_vmcnt + barrier).  Vector memory
-// operations complete in issue order, so the compiler's own vmcnt waits stay
-// correct (they can only wait longer).
-__device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds_kb) {
-  asm volatile(
-      "s_mov_b32 m0, %1\n\t"
-      "global_load_lds_dwordx4 %0, off"
-      :
-      : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds_kb))
-      : "memory", "m0");
 }
 
 // The DMA loads one wave issues per stage for an R-wide operand tile, shared

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "fp8lin.h"
+#include "fp8lin_block.h"
 
 namespace fp8lin {
 
@@ -51,6 +52,61 @@ hipError_t launch_swiglu_bwd(const float* h, const float* da, int64_t rows, int6
                              uint32_t* amax, hipStream_t stream);
 // Blocks the SwiGLU launches use for a rows x f output (must fit a 32-bit grid).
 int64_t swiglu_blocks(int64_t rows, int64_t f);
+
+// RMS norm with the residual's addition (norm_fwd.hip, norm_bwd.hip): h = round(x + r) in r's
+// type (h = x where r is null), rstd per row, y = h * rstd * w.
+// Longest rows (they stay in registers): d a multiple of 4, any d.
+constexpr int64_t kNormMaxD = 32768, kNormMaxOddD = 16384;
+struct NormProblem {
+  const void* x;
+  int x_dtype;
+  const void* r;  // optional
+  int r_dtype;
+  const void* w;
+  int w_dtype;
+  int64_t rows, d;
+  float eps;
+  void* h;      // written where r is given
+  float* rstd;  // optional but for launch_norm_quantize
+};
+// amax: optional, cleared then folded with max |y|.
+hipError_t launch_norm_fwd(const NormProblem& p, uint16_t* y, uint32_t* amax, hipStream_t stream);
+hipError_t launch_norm_cast(const NormProblem& p, const int32_t* bias, int fmt, uint8_t* y, uint32_t* amax,
+                            hipStream_t stream);
+// Current scaling: one launch for one row, two for more (the codes need every
+// row's amax).
+hipError_t launch_norm_quantize(const NormProblem& p, int fmt, int32_t margin, uint8_t* y, uint32_t* row_amax,
+                                uint32_t* amax, int32_t* bias, hipStream_t stream);
+int64_t norm_bwd_workspace_bytes(int64_t rows, int64_t d);
+hipError_t launch_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dtype, const void* w, int w_dtype,
+                           const float* rstd, const void* dh, int64_t rows, int64_t d, void* dx, float* dw,
+                           uint32_t* amax, float* ws, hipStream_t stream);
+
+// The paged FP8 cache (kv_cache.hip).  Workgroups an append or read of the
+// batch launches, or 2^31 for too many.
+int64_t kv_append_groups(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, bool queries);
+hipError_t launch_kv_append(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, int dtype, const void* q, int64_t q_stride, int q_heads,
+                            uint16_t* q_out, const float* cos, const float* sin, int rope_rows, int rope_pairs,
+                            hipStream_t stream);
+hipError_t launch_kv_read(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch, int out_dtype, void* k, void* v,
+                          hipStream_t stream);
+// Attention over the cache (kv_attention.hip).
+struct AttnProblem {
+  fp8_kv_cache_t cache;
+  fp8_kv_batch_t batch;
+  const uint16_t* q;
+  int64_t q_stride;
+  int q_heads;
+  float scale;
+  int causal, window;
+  uint16_t* out;
+  float* lse;  // optional
+};
+// Workspace bytes of the split over the keys (0: not split), or a negative
+// status where the launch would not fit a 32-bit grid.
+int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads);
+hipError_t launch_kv_attention(const AttnProblem& p, void* ws, hipStream_t stream);
 
 // Product arithmetic (the values of fp8_scaled_gemm's `math` argument).
 #define FP8LIN_MATH_EXACT FP8_GEMM_EXACT

@@ -1,0 +1,185 @@
+// RMS norm, backward (norm_kernel.h).
+#include "norm_kernel.h"
+
+namespace fp8lin {
+namespace {
+
+struct BwdArgs {
+  const void* dy;
+  const void* h;
+  const void* w;
+  int w_dtype;
+  const float* rstd;
+  const void* dh;  // optional
+  int64_t rows;
+  int d;
+  void* dx;
+  float* partial;  // [gridDim.x][d]
+  uint32_t* amax;  // optional, cleared before
+};
+
+// Each workgroup walks rows blockIdx.x, + gridDim.x, ...; this lane's share of
+// dw stays in registers, and the weight where they suffice.  dw leaves as one row of `partial` per
+// workgroup, added in a fixed order by norm_dw_kernel.
+template <int YT, int HT, int V, int U, int W>
+__global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
+  constexpr int kLanes = 64 * W;
+  constexpr int kRows = kBlock<W> / kLanes;
+  __shared__ float part[2][W];
+  const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int sub = W == 1 ? threadIdx.x >> 6 : 0;
+  const int d = a.d;
+  // sixteen waves leave 128 registers a lane, too few to keep w as well
+  constexpr bool kKeepW = W < 16;
+  float w[kKeepW ? U : 1][V], dw[U][V];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int j = (u * kLanes + t) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[u][e] = 0.0f;
+    if constexpr (kKeepW) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[u][e] = 0.0f;
+      if (j < d) load_cached<V>(a.w, a.w_dtype, j, w[u]);
+    }
+  }
+  uint32_t top = 0;
+  int parity = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+    const int64_t base = row * d;
+    float g[U][V], xh[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = (u * kLanes + t) * V;
+      if (j < d) {
+        load_stream<YT, V>(a.dy, base + j, g[u]);
+        load_stream<HT, V>(a.h, base + j, xh[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[u][e] = xh[u][e] = 0.0f;
+      }
+    }
+    const float rs = a.rstd[row];
+    float c = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float* wu = w[kKeepW ? u : 0];
+      if constexpr (!kKeepW) {
+        int j = (u * kLanes + t) * V;
+        asm volatile("" : "+v"(j));  // or the loads leave the loop, into registers again
+        float ww[V] = {};
+        if (j < d) load_cached<V>(a.w, a.w_dtype, j, ww);
+#pragma unroll
+        for (int e = 0; e < V; ++e) wu[e] = ww[e];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        xh[u][e] *= rs;
+        dw[u][e] = fmaf(g[u][e], xh[u][e], dw[u][e]);
+        g[u][e] *= wu[e];
+        c = fmaf(g[u][e], xh[u][e], c);
+      }
+    }
+    c = row_sum<W>(c, part[parity]) / (float)d;
+    parity ^= 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = (u * kLanes + t) * V;
+      if (j < d) {
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = rs * (g[u][e] - xh[u][e] * c);
+        if (a.dh) {
+          float r[V];
+          load_stream<HT, V>(a.dh, base + j, r);
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] += r[e];
+        }
+        round_to<HT, V>(o);
+        store_as<HT, V>(a.dx, base + j, o);
+#pragma unroll
+        for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(o[e]) & 0x7FFFFFFFu);
+      }
+    }
+  }
+  if (a.amax) fold_amax_wave(top, a.amax);
+  // a workgroup of four one-wave rows adds its waves' shares in wave order
+  if constexpr (kRows > 1) {
+    __shared__ float acc[kRows - 1][U * V][64];
+    if (sub > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[sub - 1][u * V + e][t] = dw[u][e];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+#pragma unroll
+        for (int s = 0; s < kRows - 1; ++s) dw[u][e] += acc[s][u * V + e][t];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int j = (u * kLanes + t) * V;
+    if (j < d) store_as<FP8_IN_FP32, V>(a.partial, (int64_t)blockIdx.x * d + j, dw[u]);
+  }
+}
+
+// dw[j] = sum over the `parts` rows of partial, 16 interleaved shares of the
+// rows first, then those in order.
+constexpr int kDwCols = 64, kDwShares = 16;
+__global__ __launch_bounds__(kDwCols* kDwShares) void norm_dw_kernel(const float* partial, int parts, int d,
+                                                                    float* dw) {
+  __shared__ float s[kDwShares][kDwCols];
+  const int c = threadIdx.x & (kDwCols - 1), q = threadIdx.x / kDwCols;
+  const int j = blockIdx.x * kDwCols + c;
+  float v = 0.0f;
+  if (j < d) {
+#pragma unroll 8
+    for (int p = q; p < parts; p += kDwShares) v += partial[(int64_t)p * d + j];
+  }
+  s[q][c] = v;
+  __syncthreads();
+  if (q == 0 && j < d) {
+    for (int k = 1; k < kDwShares; ++k) v += s[k][c];
+    dw[j] = v;
+  }
+}
+
+// Workgroups (and rows of partial sums) of the backward pass.
+int bwd_parts(int64_t rows, int64_t d) {
+  const int64_t rows_per = d % 4 == 0 && d <= 2048 ? 4 : 1;
+  const int64_t blocks = (rows + rows_per - 1) / rows_per;
+  return (int)(blocks < 512 ? blocks : 512);
+}
+
+}  // namespace
+
+int64_t norm_bwd_workspace_bytes(int64_t rows, int64_t d) { return (int64_t)bwd_parts(rows, d) * d * 4; }
+
+hipError_t launch_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dtype, const void* w, int w_dtype,
+                           const float* rstd, const void* dh, int64_t rows, int64_t d, void* dx, float* dw,
+                           uint32_t* amax, float* ws, hipStream_t stream) {
+  if (amax) hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, stream, amax);
+  const int parts = bwd_parts(rows, d);
+  if (rows > 0) {
+    const BwdArgs a{dy, h, w, w_dtype, rstd, dh, rows, (int)d, dx, ws, amax};
+    for_dtype(dy_dtype, [&](auto yt) {
+      for_dtype(h_dtype, [&](auto ht) {
+        if constexpr (yt.value != kNone && ht.value != kNone)
+          for_shape((int)d, [&](auto v, auto u, auto w_) {
+            hipLaunchKernelGGL((norm_bwd_kernel<yt.value, ht.value, v.value, u.value, w_.value>),
+                               dim3((uint32_t)parts), dim3(kBlock<w_.value>), 0, stream, a);
+          });
+      });
+    });
+  }
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((uint32_t)((d + kDwCols - 1) / kDwCols)), dim3(kDwCols * kDwShares), 0,
+                     stream, ws, parts, (int)d, dw);
+  return hipGetLastError();
+}
+
+}  // namespace fp8lin

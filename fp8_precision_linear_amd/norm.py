@@ -1,0 +1,219 @@
+"""RMS norm with the residual's addition in front of an FP8 product
+(include/fp8lin_block.h), and its backward pass.
+
+    h = x + residual (in the residual's type; h = x without one)
+    y = h * rstd * w,   rstd = (mean(h^2) + eps)^-1/2 per row
+
+rmsnorm_quantize returns y as FP8 codes with current scaling, rmsnorm_cast at a
+given bias (static or delayed scaling), rmsnorm_fwd in bf16.  FP8NormLinear is
+the norm and the FP8-AMAX linear layer behind it as one autograd module: the
+codes go straight into the product.
+"""
+import torch
+
+from . import (E4M3, E5M2, OP_DGRAD, OP_FWD, OP_WGRAD, Fp8Error, _check, _dtype_code, _empty, _need_kind, _places,
+               _ptr, _stream, lib, scaled_gemm_accumulate, scaled_gemm_auto)
+from .linear import ScalingState
+
+MAX_D, MAX_ODD_D = 32768, 16384   # longest rows: a multiple of 4, any
+
+
+def _fwd_args(x, w, residual, eps, h, rstd, stream, want_rstd):
+    """Checks; (rows, d, arguments up to rstd, h, rstd) of the forward calls.
+    x and residual: [..., d]."""
+    for t, name in ((x, "x"), (w, "w"), (residual, "residual")):
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+    if x.dim() < 1 or w.dim() != 1 or x.shape[-1] != w.shape[0]:
+        raise ValueError(f"x [..., d] and w [d] do not match: {tuple(x.shape)}, {tuple(w.shape)}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    d = w.shape[0]
+    if not 1 <= d <= (MAX_D if d % 4 == 0 else MAX_ODD_D):
+        raise ValueError(f"rows of {d} elements: 1 to {MAX_D}, or {MAX_ODD_D} where not a multiple of 4")
+    rows = x.numel() // d
+    xt, wt = _dtype_code(x), _dtype_code(w)
+    rt = 0
+    if residual is not None:
+        rt = _dtype_code(residual)
+        _need_kind(residual, "residual", residual.dtype, shape=x.shape)
+        if h is not None:
+            _need_kind(h, "h", residual.dtype, shape=x.shape)
+    elif h is not None:
+        raise ValueError("h is written only where there is a residual")
+    if rstd is not None:
+        _need_kind(rstd, "rstd", torch.float32, numel=rows)
+    _places(x.device, (x, "x"), (w, "w"), (residual, "residual"), (h, "h"), (rstd, "rstd"))
+    if residual is not None and h is None:
+        h = _empty(x.shape, residual.dtype, x.device, stream)
+    if rstd is None and want_rstd:
+        rstd = _empty(rows, torch.float32, x.device, stream)
+    args = (_ptr(x), xt, _ptr(residual), rt, _ptr(w), wt, rows, d, float(eps), _ptr(h), _ptr(rstd))
+    return rows, args, (x if residual is None else h), rstd
+
+
+def rmsnorm_fwd(x, w, residual=None, eps=1e-5, out=None, h=None, rstd=None, amax=None, stream=None):
+    """(y, h, rstd): y in bf16 (fp8_rmsnorm_fwd).  h is x itself without a
+    residual.  amax: optional float32[1] device tensor that receives max |y|."""
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
+    if out is not None:
+        _need_kind(out, "out", torch.bfloat16, shape=x.shape)
+    if amax is not None:
+        _need_kind(amax, "amax", torch.float32, numel=1)
+    _places(x.device, (out, "out"), (amax, "amax"))
+    out = _empty(x.shape, torch.bfloat16, x.device, stream) if out is None else out
+    _check("fp8_rmsnorm_fwd", lib.fp8_rmsnorm_fwd(*args, _ptr(out), _ptr(amax), _stream(stream)))
+    return out, h_out, rstd
+
+
+def rmsnorm_cast(x, w, bias, fmt, residual=None, eps=1e-5, out=None, h=None, rstd=None, amax=None, stream=None):
+    """(codes, h, rstd): y as FP8 codes at `bias` (int32[1] device tensor)
+    (fp8_rmsnorm_cast).  amax: optional float32[1] device tensor that receives
+    max |y| -- delayed scaling takes the next step's bias from it."""
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
+    _need_kind(bias, "bias", torch.int32, numel=1)
+    if out is not None:
+        _need_kind(out, "out", torch.uint8, shape=x.shape)
+    if amax is not None:
+        _need_kind(amax, "amax", torch.float32, numel=1)
+    _places(x.device, (bias, "bias"), (out, "out"), (amax, "amax"))
+    out = _empty(x.shape, torch.uint8, x.device, stream) if out is None else out
+    _check("fp8_rmsnorm_cast", lib.fp8_rmsnorm_cast(*args, _ptr(bias), int(fmt), _ptr(out), _ptr(amax),
+                                                    _stream(stream)))
+    return out, h_out, rstd
+
+
+def rmsnorm_quantize(x, w, fmt, residual=None, eps=1e-5, margin=0, out=None, bias=None, amax=None, h=None, rstd=None,
+                     row_amax=None, stream=None):
+    """(codes, bias, amax, h, rstd): y as FP8 codes with current scaling
+    (fp8_rmsnorm_quantize).  row_amax: optional float32[rows] device tensor
+    that receives every row's max |y|."""
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
+    for t, name, dtype, kind in ((out, "out", torch.uint8, {"shape": x.shape}), (bias, "bias", torch.int32, {"numel": 1}),
+                                 (amax, "amax", torch.float32, {"numel": 1}),
+                                 (row_amax, "row_amax", torch.float32, {"numel": rows})):
+        if t is not None:
+            _need_kind(t, name, dtype, **kind)
+    _places(x.device, (out, "out"), (bias, "bias"), (amax, "amax"), (row_amax, "row_amax"))
+    dev = x.device
+    out = _empty(x.shape, torch.uint8, dev, stream) if out is None else out
+    bias = _empty(1, torch.int32, dev, stream) if bias is None else bias
+    amax = _empty(1, torch.float32, dev, stream) if amax is None else amax
+    row_amax = _empty(rows, torch.float32, dev, stream) if row_amax is None else row_amax
+    _check("fp8_rmsnorm_quantize",
+           lib.fp8_rmsnorm_quantize(*args, int(fmt), int(margin), _ptr(out), _ptr(row_amax), _ptr(amax), _ptr(bias),
+                                    _stream(stream)))
+    return out, bias, amax, h_out, rstd
+
+
+def rmsnorm_bwd_workspace_bytes(rows, d):
+    """Workspace bytes of rmsnorm_bwd (fp8_rmsnorm_bwd_workspace_bytes)."""
+    v = lib.fp8_rmsnorm_bwd_workspace_bytes(int(rows), int(d))
+    if v < 0:
+        raise Fp8Error("fp8_rmsnorm_bwd_workspace_bytes", v)
+    return v
+
+
+def rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, amax=None, workspace=None, stream=None):
+    """(dx, dw) of the norm (fp8_rmsnorm_bwd): dx in h's type (the gradient of x
+    and of the residual), dw float32.  dh: the gradient that reaches h past the
+    norm, added into dx.  amax: optional float32[1] device tensor that receives
+    max |dx|.  workspace: optional device tensor of at least
+    rmsnorm_bwd_workspace_bytes(rows, d) bytes."""
+    for t, name in ((dy, "dy"), (h, "h"), (w, "w")):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+    if h.dim() < 1 or w.dim() != 1 or h.shape[-1] != w.shape[0] or dy.shape != h.shape:
+        raise ValueError(f"dy, h [..., d] and w [d] do not match: {tuple(dy.shape)}, {tuple(h.shape)}, {tuple(w.shape)}")
+    d = w.shape[0]
+    rows = h.numel() // max(d, 1)
+    yt, ht, wt = _dtype_code(dy), _dtype_code(h), _dtype_code(w)
+    nbytes = rmsnorm_bwd_workspace_bytes(rows, d)
+    _need_kind(rstd, "rstd", torch.float32, numel=rows)
+    for t, name, dtype, kind in ((dh, "dh", h.dtype, {"shape": h.shape}), (dx, "dx", h.dtype, {"shape": h.shape}),
+                                 (dw, "dw", torch.float32, {"shape": w.shape}), (amax, "amax", torch.float32, {"numel": 1})):
+        if t is not None:
+            _need_kind(t, name, dtype, **kind)
+    dev = h.device
+    _places(dev, (dy, "dy"), (h, "h"), (w, "w"), (rstd, "rstd"), (dh, "dh"), (dx, "dx"), (dw, "dw"), (amax, "amax"),
+            (workspace, "workspace"))
+    dx = _empty(h.shape, h.dtype, dev, stream) if dx is None else dx
+    dw = _empty(w.shape, torch.float32, dev, stream) if dw is None else dw
+    workspace = _empty(nbytes, torch.uint8, dev, stream) if workspace is None else workspace
+    _check("fp8_rmsnorm_bwd",
+           lib.fp8_rmsnorm_bwd(_ptr(dy), yt, _ptr(h), ht, _ptr(w), wt, _ptr(rstd), _ptr(dh), rows, d, _ptr(dx),
+                               _ptr(dw), _ptr(amax), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                               _stream(stream)))
+    return dx, dw
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(y bf16, h) = norm(x + residual) w; gradients for x, residual and w."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w, eps):
+        y, h, rstd = rmsnorm_fwd(x.contiguous(), w.contiguous(), residual=None if residual is None else
+                                 residual.contiguous(), eps=eps)
+        ctx.save_for_backward(h, w, rstd)
+        ctx.has_residual = residual is not None
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, w, rstd = ctx.saved_tensors
+        dx, dw = rmsnorm_bwd(dy.contiguous(), h.contiguous(), w.contiguous(), rstd,
+                             dh=None if dh is None else dh.contiguous())
+        return dx, (dx if ctx.has_residual else None), dw.to(w.dtype), None
+
+
+class FP8NormLinearFunction(torch.autograd.Function):
+    """(y, h): h = x + residual, y = fp8_linear(norm(h) w_norm, w)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w_norm, w, state, eps):
+        x = x.contiguous()
+        n8, bn, an, h, rstd = rmsnorm_quantize(x, w_norm.contiguous(), E4M3, eps=eps, margin=state.margins["x"],
+                                               residual=None if residual is None else residual.contiguous())
+        state.amax["x"] = an
+        if state.log is not None:
+            state.log.record("x", bn)
+        n8 = n8.reshape(-1, n8.shape[-1])
+        w8, bw = state.quantise("w", w.contiguous())
+        y = scaled_gemm_auto(OP_FWD, n8, E4M3, bn, w8, E4M3, bw, math=state.math)
+        ctx.saved = (n8, bn, w8, bw, h, rstd)
+        ctx.state, ctx.weight, ctx.w_norm, ctx.has_residual = state, w, w_norm, residual is not None
+        y = y.reshape(*x.shape[:-1], w.shape[0])
+        return (y, h) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        n8, bn, w8, bw, h, rstd = ctx.saved
+        state, w = ctx.state, ctx.weight
+        dy8, bdy = state.quantise("dy", dy.contiguous().reshape(-1, dy.shape[-1]))
+        dn = scaled_gemm_auto(OP_DGRAD, dy8, E5M2, bdy, w8, E4M3, bw, math=state.math)
+        if state.fuse_wgrad_accumulation and w.grad is not None:
+            scaled_gemm_accumulate(OP_WGRAD, dy8, E5M2, bdy, n8, E4M3, bn, w.grad, math=state.math)
+            dw = None
+        else:
+            dw = scaled_gemm_auto(OP_WGRAD, dy8, E5M2, bdy, n8, E4M3, bn, math=state.math)
+        dx, dwn = rmsnorm_bwd(dn.reshape(h.shape), h, ctx.w_norm.contiguous(), rstd,
+                              dh=None if dh is None else dh.contiguous())
+        ctx.saved = ctx.weight = None
+        return dx, (dx if ctx.has_residual else None), dwn.to(ctx.w_norm.dtype), dw, None, None
+
+
+class FP8NormLinear(torch.nn.Module):
+    """The RMS norm and the FP8-AMAX linear layer behind it.  layer(x) is y;
+    layer(x, residual) is (y, x + residual).  Scaling of the normed activations
+    is current; the other tensors' as in FP8Linear."""
+
+    def __init__(self, in_features, out_features, eps=1e-5, margins=None, log=None, device=None, dtype=torch.float32,
+                 std=0.02, **state):
+        super().__init__()
+        self.eps = eps
+        self.state = ScalingState("current", margins, log=log, **state)
+        self.norm_weight = torch.nn.Parameter(torch.ones(in_features, device=device, dtype=dtype))
+        self.weight = torch.nn.Parameter(torch.randn(out_features, in_features, device=device, dtype=dtype) * std)
+
+    def forward(self, x, residual=None):
+        return FP8NormLinearFunction.apply(x, residual, self.norm_weight, self.weight, self.state, self.eps)
