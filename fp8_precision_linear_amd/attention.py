@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import (E4M3, E5M2, Fp8Error, _check, _dtype_code, _empty, _need_kind, _need_place, _places, _ptr, _stream, lib)
+from . import (E4M3, E5M2, Fp8Error, _check, _dtype_code, _empty, _need_kind, _need_place, _places, _stream, lib)
 
 BLOCK_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128, 256)
@@ -119,6 +119,10 @@ class KVBatch:
         return cls(i32(cu), i32(list(lens)).reshape(-1), table, max([0, *new]), max([0, *lens]), cu[-1])
 
 
+def _opt(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _pair(cache, batch):
     if not isinstance(cache, KVCache) or not isinstance(batch, KVBatch):
         raise ValueError("cache is a KVCache and batch a KVBatch")
@@ -131,16 +135,17 @@ def _pair(cache, batch):
 
 def _head_rows(t, name, tokens, heads, d, device, dtype=None):
     """Row stride in elements of [tokens, heads, d] rows with packed heads."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or tuple(t.shape) != (tokens, heads, d):
+    if not isinstance(t, torch.Tensor) or t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be a [{tokens}, {heads}, {d}] tensor, got "
                          f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor on {device}, got {t.device}")
-    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    row, head, one = t.stride()
+    if tokens and (one != 1 or (heads > 1 and head != d)):
         raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if tokens > 1 else heads * d
+    return row if tokens > 1 else heads * d
 
 
 def kv_append(cache, batch, k, v, q=None, rope=None, rope_pairs=False, q_out=None, stream=None):
@@ -179,8 +184,8 @@ def kv_append(cache, batch, k, v, q=None, rope=None, rope_pairs=False, q_out=Non
                 raise ValueError(f"{name} holds {t.shape[0]} positions, the batch up to {batch.max_len}")
             _need_place(t, name, dev)
     _check("fp8_kv_append",
-           lib.fp8_kv_append(cache._ref, batch._ref, _ptr(k), ks, _ptr(v), vs, dt, _ptr(q), qs, heads, _ptr(q_out),
-                             _ptr(cos), _ptr(sin), 0 if cos is None else cos.shape[0], int(bool(rope_pairs)),
+           lib.fp8_kv_append(cache._ref, batch._ref, k.data_ptr(), ks, v.data_ptr(), vs, dt, _opt(q), qs, heads, _opt(q_out),
+                             _opt(cos), _opt(sin), 0 if cos is None else cos.shape[0], int(bool(rope_pairs)),
                              _stream(stream)))
     return q_out
 
@@ -198,7 +203,7 @@ def kv_read(cache, batch, dtype=torch.bfloat16, k_out=None, v_out=None, stream=N
             _need_place(t, name, dev)
     k_out = _empty(shape, dtype, dev, stream) if k_out is None else k_out
     v_out = _empty(shape, dtype, dev, stream) if v_out is None else v_out
-    _check("fp8_kv_read", lib.fp8_kv_read(cache._ref, batch._ref, _dtype_code(k_out), _ptr(k_out), _ptr(v_out),
+    _check("fp8_kv_read", lib.fp8_kv_read(cache._ref, batch._ref, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(),
                                           _stream(stream)))
     return k_out, v_out
 
@@ -253,7 +258,7 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, l
         lse = _empty((T, heads), torch.float32, dev, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("fp8_kv_attention",
-           lib.fp8_kv_attention(cache._ref, batch._ref, _ptr(q), qs, heads,
-                                float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window), _ptr(out),
-                                _ptr(lse), _ptr(workspace), nbytes, _stream(stream)))
+           lib.fp8_kv_attention(cache._ref, batch._ref, q.data_ptr(), qs, heads,
+                                float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window), out.data_ptr(),
+                                _opt(lse), _opt(workspace), nbytes, _stream(stream)))
     return (out, lse) if return_lse else out

@@ -42,15 +42,20 @@ struct AttnArgs {
   int64_t q_stride;
   int q_heads;
   int group;        // query heads per key head
-  float scale_log2;
+  int block_shift;  // log2 of the block size
+  float scale;       // its sign, and zero
+  float scale_log2;  // |scale| * log2(e), 1 for a scale of zero
   int causal, window;
   uint16_t* out;
   float* lse;
   float* part_o;    // [splits][tokens][q_heads][D], normalised
   float* part_lse;  // [splits][tokens][q_heads], base 2
-  int chunk;        // keys per split, a multiple of kAttnTile
-  int splits;       // most chunks of any row tile
+  int chunk;        // tile kernel: keys per split, a multiple of kAttnTile
+  int splits;       // tile kernel: most chunks of any row tile
   int row_tiles;    // most row tiles of any sequence
+  int shares;       // rows kernel: workgroups that share all keys evenly, or 0
+  int2* segments;   // rows kernel, shares > 0: [batch][row_tiles][heads], the
+                    // first and last workgroup of a segment
 };
 
 namespace {
@@ -89,6 +94,13 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a) {
   return p;
 }
 
+// The logits' factor scale * log2(e) is positive in the kernels: a negative
+// scale negates the queries, a scale of zero clears them.
+__device__ __forceinline__ uint4 sign_queries(uint4 v, float scale) {
+  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;
+  return scale == 0.0f ? make_uint4(0, 0, 0, 0) : make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+}
+
 // The keys a tile of rows [row0, row0 + count) of sequence s reads, and its
 // chunks; rows run over (token, head of the group).
 struct AttnSpan {
@@ -106,6 +118,12 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const KVSeq& s,
 // 2^e as a float for the conversions' scale operand, e clamped to normals.
 __device__ __forceinline__ float pow2_scale(int e) {
   return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23);
+}
+
+// log2(e) * scale * 2^-kb, at least the smallest normal number: an invisible
+// logit of -inf times it stays -inf.
+__device__ __forceinline__ float key_scale(float scale_log2, int kb) {
+  return fmaxf(scale_log2 * pow2_scale(-kb), 0x1p-126f);
 }
 
 // 8 codes -> 8 bf16, exactly.
@@ -173,6 +191,10 @@ __device__ __forceinline__ v8h ones_f16(uint32_t m0, uint32_t m1) {
   return r;
 }
 
+// The larger of two logits in one instruction (fmaxf first quiets what the
+// compiler cannot prove quiet); a NaN loses to any number.
+__device__ __forceinline__ float raw_max(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+
 // Reductions over the lanes that share a query row: l ^ 32, and l ^ 16.
 __device__ __forceinline__ float swap32_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -205,6 +227,8 @@ __device__ __forceinline__ int swap16_min(int v) {
 // 16 * row_blocks rows (1 or 2; 1 for head_dim 256), the tile kernel of 128.
 constexpr int kAttnTileRows = 128;
 hipError_t launch_attn_rows(const AttnArgs& a, int row_blocks, uint32_t groups, hipStream_t stream);
+// Workgroups of the rows kernel that run at the same time on 256 CUs.
+int attn_rows_resident(int head_dim, int row_blocks);
 hipError_t launch_attn_tile(const AttnArgs& a, uint32_t groups, hipStream_t stream);
 
 }  // namespace fp8lin

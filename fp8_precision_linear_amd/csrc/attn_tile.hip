@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   const int r32 = lane & 31, h = lane >> 5;
   const AttnPlace at = attn_place(a);
   const int BS = a.cache.block_size, H = a.cache.heads, G = a.group;
-  const KVSeq s = kv_seq(a.batch, BS, at.seq);
+  const KVSeq s = kv_seq_uniform(a.batch, BS, at.seq);
   const int rows = s.n * G, row0 = at.row_tile * kAttnTileRows;
   if (row0 >= rows) return;
   const AttnSpan span = attn_span(a, s, row0, kAttnTileRows);
@@ -65,8 +65,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
     const uint16_t* qp = a.q + (int64_t)(s.first + row / G) * a.q_stride + (at.head * G + row % G) * D + 16 * h;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      q[j][0] = *reinterpret_cast<const v8b*>(qp + 32 * j);
-      q[j][1] = *reinterpret_cast<const v8b*>(qp + 32 * j + 8);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        q[j][c] = __builtin_bit_cast(v8b, sign_queries(*reinterpret_cast<const uint4*>(qp + 32 * j + 8 * c), a.scale));
     }
   }
   // the wave's keys: none past the last of its rows' or before the first's
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int pos = T + 16 * g;
-      r.b[g] = pos < kend ? kv_block(a.cache, a.batch, at.seq, pos / BS) : -1;
+      r.b[g] = pos < kend ? kv_block(a.cache, a.batch, at.seq, pos >> a.block_shift) : -1;
     }
     return r;
   };

@@ -1,23 +1,29 @@
 // Attention over the paged FP8 cache: which kernel takes a batch, how its keys
 // are split, and the join of split results (attn_common.h, attn_rows.hip,
 // attn_tile.hip).
+#include <cmath>
+
 #include "attn_common.h"
 
 namespace fp8lin {
 namespace {
 
 struct AttnPlan {
-  bool few;          // the rows kernel
-  int row_blocks;    // of 16, rows kernel
-  int tile_rows;     // rows per row tile
-  int row_tiles;     // most of any sequence
-  int chunk, splits;
+  bool few;             // the rows kernel
+  int row_blocks;       // of 16, rows kernel
+  int tile_rows;        // rows per row tile
+  int row_tiles;        // most of any sequence
+  int shares;           // rows kernel: workgroups of the even shares, or 0
+  int chunk, splits;    // tile kernel
   int64_t base;         // workgroups without a split
-  int64_t most_splits;  // whatever the window
+  int64_t most_splits;  // tile kernel, whatever the window
 };
 
-// Workgroups wanted in flight: four (rows) or two (tiles) for each of 256 CUs.
-constexpr int64_t kWantRows = 1024, kWantTiles = 512;
+// Tile kernel: workgroups wanted in flight, two for each of 256 CUs.
+constexpr int64_t kWantTiles = 512;
+// Rows kernel: even shares where a segment may hold more tiles than this (a
+// join costs about as long as the tiles it takes off the longest workgroup).
+constexpr int64_t kWholeTiles = 24;
 
 AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int window) {
   AttnPlan p{};
@@ -27,13 +33,18 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
   p.tile_rows = p.few ? 16 * p.row_blocks : kAttnTileRows;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   p.base = (int64_t)p.row_tiles * b.batch * c.heads;
+  p.chunk = kAttnTile, p.splits = 1, p.most_splits = 1;
+  if (p.few) {
+    const int resident = attn_rows_resident(c.head_dim, p.row_blocks);
+    if ((b.max_len + kAttnTile - 1) / kAttnTile > kWholeTiles && p.base < 16 * (int64_t)resident) p.shares = resident;
+    return p;
+  }
   int64_t span = b.max_len;  // most keys of a row tile
   if (window > 0) span = span < (int64_t)window + b.max_new + kAttnTile ? span : (int64_t)window + b.max_new + kAttnTile;
   const int64_t tiles = span > 0 ? (span + kAttnTile - 1) / kAttnTile : 1;
-  // no chunk below four tiles (one for each wave of the rows kernel)
-  const int64_t want = ((p.few ? kWantRows : kWantTiles) + p.base - 1) / p.base;
+  const int64_t want = (kWantTiles + p.base - 1) / p.base;
   int64_t per = (tiles + want - 1) / want;
-  per = (per + 3) / 4 * 4;
+  per = (per + 3) / 4 * 4;  // no chunk below four tiles
   p.splits = (int)((tiles + per - 1) / per);
   p.chunk = (int)(per * kAttnTile);
   const int64_t full = ((int64_t)b.max_len + 4 * kAttnTile - 1) / (4 * kAttnTile);
@@ -41,47 +52,103 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
   return p;
 }
 
-// One workgroup per new token: joins the chunks of each of its heads that was
-// split.  out = sum_c 2^(lse_c - L) out_c, L = log2 sum_c 2^lse_c.
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int tile_rows) {
-  const int i = blockIdx.x % a.batch.batch, nth = blockIdx.x / a.batch.batch;
-  const KVSeq s = kv_seq(a.batch, a.cache.block_size, i);
+// Rows of partial results.
+int64_t part_rows(const AttnPlan& p, const fp8_kv_batch_t& b, int q_heads, int64_t splits) {
+  return p.few ? 2 * (int64_t)p.shares * p.tile_rows : splits * b.tokens * q_heads;
+}
+
+// One workgroup per (new token, query head) whose keys were split joins its
+// parts (chunks, or shares): out = sum_c 2^(lse_c - L) out_c, L = log2 sum_c 2^lse_c.  The parts
+// are dealt to groups of lanes, which meet in LDS in order; a part
+// without visible keys has lse = -inf and adds nothing.
+constexpr int kJoin = 256;
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows) {
+  __shared__ v4f so[kJoin];
+  __shared__ float ss[kJoin], st[kJoin];
+  uint32_t x = blockIdx.x;
+  const int head = x % a.q_heads;
+  x /= a.q_heads;
+  const int i = x % a.batch.batch, nth = x / a.batch.batch;
+  const int row = nth * a.group + head % a.group, tile = row / tile_rows;
+  int2 w{0, 0};
+  if (a.shares) w = a.segments[((int64_t)i * a.row_tiles + tile) * a.cache.heads + head / a.group];
+  const KVSeq s = kv_seq_uniform(a.batch, a.cache.block_size, i);
   if (nth >= s.n) return;
-  const int D = a.cache.head_dim, G = a.group, upr = D / 4;
-  const int64_t row0 = (int64_t)(s.first + nth) * a.q_heads;
-  const int64_t step = (int64_t)a.batch.tokens * a.q_heads;
-  for (int x = threadIdx.x; x < a.q_heads * upr; x += 256) {
-    const int head = x / upr, d = 4 * (x % upr);
-    const int tile = (nth * G + head % G) / tile_rows;
-    const int chunks = attn_span(a, s, tile * tile_rows, tile_rows).chunks;
-    if (chunks == 1) continue;
-    const int64_t at = row0 + head;
-    float top = -INFINITY;
-    for (int c = 0; c < chunks; ++c) top = fmaxf(top, a.part_lse[c * step + at]);
-    float total = 0.0f;
-    v4f sum{0, 0, 0, 0};
-    for (int c = 0; c < chunks; ++c) {
-      const float lse = a.part_lse[c * step + at];
-      // a chunk without visible keys has lse = -inf and adds nothing
-      const float f = lse == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lse - top);
-      total += f;
-      sum += *reinterpret_cast<const v4f*>(a.part_o + (c * step + at) * D + d) * f;
-    }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    *reinterpret_cast<uint2*>(a.out + at * D + d) =
-        make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
-    if (d == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
+  const int64_t at = (int64_t)(s.first + nth) * a.q_heads + head;
+  // part c's row of part_o and part_lse: first for c = 0, then from `base` by step
+  int64_t first = at, base = at, step = (int64_t)a.batch.tokens * a.q_heads;
+  int chunks;
+  if (a.shares) {
+    chunks = w.y - w.x + 1;
+    first = (2 * (int64_t)w.x + 1) * tile_rows + row % tile_rows;
+    base = 2 * (int64_t)w.x * tile_rows + row % tile_rows;
+    step = 2 * tile_rows;
+  } else {
+    chunks = attn_span(a, s, tile * tile_rows, tile_rows).chunks;
   }
+  if (chunks <= 1) return;
+  const int D = a.cache.head_dim, lanes = D / 4, t = threadIdx.x;
+  const int share = t / lanes, shares = kJoin / lanes, d = 4 * (t % lanes);
+  // four parts at a time, their results and sums loaded together
+  constexpr int kAhead = 4;
+  float top = -INFINITY, total = 0.0f;
+  v4f sum{0, 0, 0, 0};
+  for (int c0 = share; c0 < chunks; c0 += kAhead * shares) {
+    float lse[kAhead];
+    v4f v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = c0 + u * shares;
+      const int64_t p = c == 0 ? first : base + (c < chunks ? c : c0) * step;
+      lse[u] = c < chunks ? a.part_lse[p] : -INFINITY;
+      v[u] = *reinterpret_cast<const v4f*>(a.part_o + (c0 == 0 && c >= chunks ? first : p) * D + d);
+    }
+    float up = top;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) up = fmaxf(up, lse[u]);
+    const float f0 = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - up);
+    sum *= f0;
+    total *= f0;
+    top = up;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float f = lse[u] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lse[u] - top);
+      total += f;
+      if (f != 0.0f) sum += v[u] * f;
+    }
+  }
+  so[t] = sum;
+  ss[t] = total;
+  st[t] = top;
+  __syncthreads();
+  if (t >= lanes) return;
+  for (int k = 0; k < shares; ++k) top = fmaxf(top, st[k * lanes + t]);
+  sum = v4f{0, 0, 0, 0};
+  total = 0.0f;
+  for (int k = 0; k < shares; ++k) {
+    const float part = st[k * lanes + t];
+    const float f = part == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(part - top);
+    if (f != 0.0f) sum += so[k * lanes + t] * f;
+    total += ss[k * lanes + t] * f;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  *reinterpret_cast<uint2*>(a.out + at * D + d) =
+      make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+  if (t == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads) {
-  // the window may shorten the span and so raise the split, up to this
+  // the window may shorten the span and so raise the split, up to most_splits
   const AttnPlan p = plan_of(c, b, q_heads, 0);
   if (p.base > 0x7FFFFFFF / p.most_splits) return FP8_ERR_SIZE;
-  if (p.most_splits == 1) return 0;
-  return p.most_splits * b.tokens * q_heads * (c.head_dim + 1) * 4;
+  // tiles of a sequence over its heads are counted in 32 bits
+  if ((int64_t)c.heads * (b.max_len / kAttnTile + 1) > 0x7FFFFFFF) return FP8_ERR_SIZE;
+  if (p.shares == 0 && p.most_splits == 1) return 0;
+  // the join's workgroups
+  if ((int64_t)b.batch * b.max_new > 0x7FFFFFFF / q_heads) return FP8_ERR_SIZE;
+  return part_rows(p, b, q_heads, p.most_splits) * (c.head_dim + 1) * 4 + (p.shares ? p.base * 8 : 0);
 }
 
 hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stream) {
@@ -93,22 +160,27 @@ hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stre
   a.q_stride = pr.q_stride;
   a.q_heads = pr.q_heads;
   a.group = pr.q_heads / pr.cache.heads;
-  a.scale_log2 = pr.scale * 1.44269504088896340736f;
+  a.block_shift = __builtin_ctz(pr.cache.block_size);
+  a.scale = pr.scale;
+  a.scale_log2 = pr.scale == 0.0f ? 1.0f : fabsf(pr.scale) * 1.44269504088896340736f;
   a.causal = pr.causal;
   a.window = pr.window;
   a.out = pr.out;
   a.lse = pr.lse;
   a.part_o = static_cast<float*>(ws);
-  a.part_lse = a.part_o + (int64_t)p.splits * pr.batch.tokens * pr.q_heads * pr.cache.head_dim;
+  const int64_t parts = part_rows(p, pr.batch, pr.q_heads, p.splits);
+  a.part_lse = a.part_o + parts * pr.cache.head_dim;
+  a.segments = reinterpret_cast<int2*>(a.part_lse + parts);
+  a.shares = p.shares;
   a.chunk = p.chunk;
   a.splits = p.splits;
   a.row_tiles = p.row_tiles;
-  const uint32_t groups = (uint32_t)(p.base * p.splits);
+  const uint32_t groups = p.shares ? (uint32_t)p.shares : (uint32_t)(p.base * p.splits);
   hipError_t e = p.few ? launch_attn_rows(a, p.row_blocks, groups, stream)
                        : launch_attn_tile(a, groups, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t tokens = (int64_t)pr.batch.batch * pr.batch.max_new;
-  hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)tokens), dim3(256), 0, stream, a, p.tile_rows);
+  if (e != hipSuccess || (p.splits == 1 && p.shares == 0)) return e;
+  const int64_t joins = (int64_t)pr.batch.batch * pr.batch.max_new * pr.q_heads;
+  hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)joins), dim3(kJoin), 0, stream, a, p.tile_rows);
   return hipGetLastError();
 }
 

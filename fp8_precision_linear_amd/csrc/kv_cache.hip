@@ -112,7 +112,7 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   if ((int64_t)blockIdx.x >= a.kv_groups) {  // one token's queries
     const int64_t g = (int64_t)blockIdx.x - a.kv_groups;
     const int i = (int)(g / a.batch.max_new), nth = (int)(g % a.batch.max_new);
-    const KVSeq s = kv_seq(a.batch, BS, i);
+    const KVSeq s = kv_seq_uniform(a.batch, BS, i);
     if (nth >= s.n) return;
     const bool halves = a.rope.cos && !a.rope.pairs;
     const int64_t row = s.first + nth;
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   const int head = (int)(g % H);
   g /= H;
   const int nth_block = (int)(g % a.blocks_per_seq), i = (int)(g / a.blocks_per_seq);
-  const KVSeq s = kv_seq(a.batch, BS, i);
+  const KVSeq s = kv_seq_uniform(a.batch, BS, i);
   if (s.n == 0) return;
   const int block_at = s.start / BS + nth_block;          // of the sequence
   const int p0 = max(s.start, block_at * BS);             // first new position in the block
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
   const int nth_block = (int)(g % a.blocks_per_seq), i = (int)(g / a.blocks_per_seq);
   void* out = values ? a.v : a.k;
   if (!out) return;
-  const KVSeq s = kv_seq(a.batch, BS, i);
+  const KVSeq s = kv_seq_uniform(a.batch, BS, i);
   if (s.n == 0) return;
   const int block_at = s.start / BS + nth_block;
   const int p0 = max(s.start, block_at * BS), p1 = min(s.start + s.n, block_at * BS + BS);

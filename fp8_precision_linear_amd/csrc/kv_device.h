@@ -25,6 +25,13 @@ __device__ __forceinline__ KVSeq kv_seq(const fp8_kv_batch_t& b, int block_size,
   return s;
 }
 
+// The same for an i that is the same in every lane: scalar values.
+__device__ __forceinline__ KVSeq kv_seq_uniform(const fp8_kv_batch_t& b, int block_size, int i) {
+  const KVSeq s = kv_seq(b, block_size, i);
+  return {__builtin_amdgcn_readfirstlane(s.first), __builtin_amdgcn_readfirstlane(s.n),
+          __builtin_amdgcn_readfirstlane(s.start), __builtin_amdgcn_readfirstlane(s.len)};
+}
+
 // Block of sequence i that holds its tokens [block_at * block_size, ...), or
 // -1.  block_at < table_width (max_len <= table_width * block_size).
 __device__ __forceinline__ int kv_block(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int i, int block_at) {

@@ -11,24 +11,36 @@ codes go straight into the product.
 """
 import torch
 
-from . import (E4M3, E5M2, OP_DGRAD, OP_FWD, OP_WGRAD, Fp8Error, _check, _dtype_code, _empty, _need_kind, _places,
-               _ptr, _stream, lib, scaled_gemm_accumulate, scaled_gemm_auto)
+from . import (E4M3, E5M2, OP_DGRAD, OP_FWD, OP_WGRAD, Fp8Error, _check, _dtype_code, _empty, _need, _need_kind,
+               _need_place, _places, _ptr, _stream, lib, scaled_gemm_accumulate, scaled_gemm_auto)
 from .linear import ScalingState
 
 MAX_D, MAX_ODD_D = 32768, 16384   # longest rows: a multiple of 4, any
 
 
-def _fwd_args(x, w, residual, eps, h, rstd, stream, want_rstd):
-    """Checks; (rows, d, arguments up to rstd, h, rstd) of the forward calls.
+def _like(t, dtype, stream):
+    """A new tensor of t's shape for a call on `stream` (as _empty)."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    return _empty(t.shape, dtype, t.device, stream)
+
+
+def _opt(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _fwd_args(x, w, residual, eps, h, rstd, stream):
+    """Checks; (rows, arguments up to rstd, h, rstd) of the forward calls.
     x and residual: [..., d]."""
     for t, name in ((x, "x"), (w, "w"), (residual, "residual")):
         if t is not None and not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-    if x.dim() < 1 or w.dim() != 1 or x.shape[-1] != w.shape[0]:
-        raise ValueError(f"x [..., d] and w [d] do not match: {tuple(x.shape)}, {tuple(w.shape)}")
+    shape = x.shape
+    if x.dim() < 1 or w.dim() != 1 or shape[-1] != w.shape[0]:
+        raise ValueError(f"x [..., d] and w [d] do not match: {tuple(shape)}, {tuple(w.shape)}")
     if not eps >= 0:
         raise ValueError(f"eps must not be negative, got {eps}")
-    d = w.shape[0]
+    d = shape[-1]
     if not 1 <= d <= (MAX_D if d % 4 == 0 else MAX_ODD_D):
         raise ValueError(f"rows of {d} elements: 1 to {MAX_D}, or {MAX_ODD_D} where not a multiple of 4")
     rows = x.numel() // d
@@ -36,32 +48,41 @@ def _fwd_args(x, w, residual, eps, h, rstd, stream, want_rstd):
     rt = 0
     if residual is not None:
         rt = _dtype_code(residual)
-        _need_kind(residual, "residual", residual.dtype, shape=x.shape)
+        if residual.shape != shape:
+            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
         if h is not None:
-            _need_kind(h, "h", residual.dtype, shape=x.shape)
+            _need_kind(h, "h", residual.dtype, shape=shape)
     elif h is not None:
         raise ValueError("h is written only where there is a residual")
     if rstd is not None:
         _need_kind(rstd, "rstd", torch.float32, numel=rows)
-    _places(x.device, (x, "x"), (w, "w"), (residual, "residual"), (h, "h"), (rstd, "rstd"))
-    if residual is not None and h is None:
-        h = _empty(x.shape, residual.dtype, x.device, stream)
-    if rstd is None and want_rstd:
-        rstd = _empty(rows, torch.float32, x.device, stream)
-    args = (_ptr(x), xt, _ptr(residual), rt, _ptr(w), wt, rows, d, float(eps), _ptr(h), _ptr(rstd))
+    dev = x.device
+    _need_place(x, "x", dev)
+    _need_place(w, "w", dev)
+    if residual is not None:
+        _need_place(residual, "residual", dev)
+    if h is not None:
+        _need_place(h, "h", dev)
+    elif residual is not None:
+        h = _like(residual, residual.dtype, stream)
+    if rstd is not None:
+        _need_place(rstd, "rstd", dev)
+    else:
+        rstd = _empty(rows, torch.float32, dev, stream)
+    args = (x.data_ptr(), xt, _opt(residual), rt, w.data_ptr(), wt, rows, d, eps, _opt(h), rstd.data_ptr())
     return rows, args, (x if residual is None else h), rstd
 
 
 def rmsnorm_fwd(x, w, residual=None, eps=1e-5, out=None, h=None, rstd=None, amax=None, stream=None):
     """(y, h, rstd): y in bf16 (fp8_rmsnorm_fwd).  h is x itself without a
     residual.  amax: optional float32[1] device tensor that receives max |y|."""
-    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream)
     if out is not None:
         _need_kind(out, "out", torch.bfloat16, shape=x.shape)
     if amax is not None:
         _need_kind(amax, "amax", torch.float32, numel=1)
     _places(x.device, (out, "out"), (amax, "amax"))
-    out = _empty(x.shape, torch.bfloat16, x.device, stream) if out is None else out
+    out = _like(x, torch.bfloat16, stream) if out is None else out
     _check("fp8_rmsnorm_fwd", lib.fp8_rmsnorm_fwd(*args, _ptr(out), _ptr(amax), _stream(stream)))
     return out, h_out, rstd
 
@@ -70,14 +91,14 @@ def rmsnorm_cast(x, w, bias, fmt, residual=None, eps=1e-5, out=None, h=None, rst
     """(codes, h, rstd): y as FP8 codes at `bias` (int32[1] device tensor)
     (fp8_rmsnorm_cast).  amax: optional float32[1] device tensor that receives
     max |y| -- delayed scaling takes the next step's bias from it."""
-    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream)
     _need_kind(bias, "bias", torch.int32, numel=1)
     if out is not None:
         _need_kind(out, "out", torch.uint8, shape=x.shape)
     if amax is not None:
         _need_kind(amax, "amax", torch.float32, numel=1)
     _places(x.device, (bias, "bias"), (out, "out"), (amax, "amax"))
-    out = _empty(x.shape, torch.uint8, x.device, stream) if out is None else out
+    out = _like(x, torch.uint8, stream) if out is None else out
     _check("fp8_rmsnorm_cast", lib.fp8_rmsnorm_cast(*args, _ptr(bias), int(fmt), _ptr(out), _ptr(amax),
                                                     _stream(stream)))
     return out, h_out, rstd
@@ -88,21 +109,28 @@ def rmsnorm_quantize(x, w, fmt, residual=None, eps=1e-5, margin=0, out=None, bia
     """(codes, bias, amax, h, rstd): y as FP8 codes with current scaling
     (fp8_rmsnorm_quantize).  row_amax: optional float32[rows] device tensor
     that receives every row's max |y|."""
-    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream, True)
-    for t, name, dtype, kind in ((out, "out", torch.uint8, {"shape": x.shape}), (bias, "bias", torch.int32, {"numel": 1}),
-                                 (amax, "amax", torch.float32, {"numel": 1}),
-                                 (row_amax, "row_amax", torch.float32, {"numel": rows})):
-        if t is not None:
-            _need_kind(t, name, dtype, **kind)
-    _places(x.device, (out, "out"), (bias, "bias"), (amax, "amax"), (row_amax, "row_amax"))
+    rows, args, h_out, rstd = _fwd_args(x, w, residual, eps, h, rstd, stream)
     dev = x.device
-    out = _empty(x.shape, torch.uint8, dev, stream) if out is None else out
-    bias = _empty(1, torch.int32, dev, stream) if bias is None else bias
-    amax = _empty(1, torch.float32, dev, stream) if amax is None else amax
-    row_amax = _empty(rows, torch.float32, dev, stream) if row_amax is None else row_amax
+    if out is not None:
+        _need_kind(out, "out", torch.uint8, shape=x.shape)
+        _need_place(out, "out", dev)
+    else:
+        out = _like(x, torch.uint8, stream)
+    if bias is not None:
+        _need(bias, "bias", torch.int32, dev, numel=1)
+    else:
+        bias = _empty(1, torch.int32, dev, stream)
+    if amax is not None:
+        _need(amax, "amax", torch.float32, dev, numel=1)
+    else:
+        amax = _empty(1, torch.float32, dev, stream)
+    if row_amax is not None:
+        _need(row_amax, "row_amax", torch.float32, dev, numel=rows)
+    else:   # one row: its amax is the tensor's
+        row_amax = amax if rows == 1 else _empty(rows, torch.float32, dev, stream)
     _check("fp8_rmsnorm_quantize",
-           lib.fp8_rmsnorm_quantize(*args, int(fmt), int(margin), _ptr(out), _ptr(row_amax), _ptr(amax), _ptr(bias),
-                                    _stream(stream)))
+           lib.fp8_rmsnorm_quantize(*args, int(fmt), int(margin), out.data_ptr(), row_amax.data_ptr(),
+                                    amax.data_ptr(), bias.data_ptr(), _stream(stream)))
     return out, bias, amax, h_out, rstd
 
 
@@ -130,20 +158,25 @@ def rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, amax=None, workspace=
     yt, ht, wt = _dtype_code(dy), _dtype_code(h), _dtype_code(w)
     nbytes = rmsnorm_bwd_workspace_bytes(rows, d)
     _need_kind(rstd, "rstd", torch.float32, numel=rows)
-    for t, name, dtype, kind in ((dh, "dh", h.dtype, {"shape": h.shape}), (dx, "dx", h.dtype, {"shape": h.shape}),
-                                 (dw, "dw", torch.float32, {"shape": w.shape}), (amax, "amax", torch.float32, {"numel": 1})):
-        if t is not None:
-            _need_kind(t, name, dtype, **kind)
     dev = h.device
-    _places(dev, (dy, "dy"), (h, "h"), (w, "w"), (rstd, "rstd"), (dh, "dh"), (dx, "dx"), (dw, "dw"), (amax, "amax"),
-            (workspace, "workspace"))
-    dx = _empty(h.shape, h.dtype, dev, stream) if dx is None else dx
-    dw = _empty(w.shape, torch.float32, dev, stream) if dw is None else dw
+    _places(dev, (dy, "dy"), (h, "h"), (w, "w"), (rstd, "rstd"), (dh, "dh"), (workspace, "workspace"))
+    if dh is not None:
+        _need_kind(dh, "dh", h.dtype, shape=h.shape)
+    if amax is not None:
+        _need(amax, "amax", torch.float32, dev, numel=1)
+    if dx is not None:
+        _need(dx, "dx", h.dtype, dev, shape=h.shape)
+    else:
+        dx = _like(h, h.dtype, stream)
+    if dw is not None:
+        _need(dw, "dw", torch.float32, dev, shape=w.shape)
+    else:
+        dw = _like(w, torch.float32, stream)
     workspace = _empty(nbytes, torch.uint8, dev, stream) if workspace is None else workspace
     _check("fp8_rmsnorm_bwd",
-           lib.fp8_rmsnorm_bwd(_ptr(dy), yt, _ptr(h), ht, _ptr(w), wt, _ptr(rstd), _ptr(dh), rows, d, _ptr(dx),
-                               _ptr(dw), _ptr(amax), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream(stream)))
+           lib.fp8_rmsnorm_bwd(dy.data_ptr(), yt, h.data_ptr(), ht, w.data_ptr(), wt, rstd.data_ptr(), _opt(dh), rows,
+                               d, dx.data_ptr(), dw.data_ptr(), _opt(amax), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(stream)))
     return dx, dw
 
 
