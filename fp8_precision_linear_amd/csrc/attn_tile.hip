@@ -19,6 +19,10 @@ namespace fp8lin {
 namespace {
 
 constexpr int kWaves = 4;
+// A lane's 32 probabilities of a tile may add up to this before its row's
+// reference moves: 32 keys level with the maximum that set it (2^kShift each)
+// stay below, and none can pass fp16's range.
+constexpr float kMostPart = 32768.0f;
 
 // Bits of a key row that tell apart the rows 16 lanes of a fragment read
 // ({0..7, 16..23} or {8..15, 24..31} of 32) and share a bank window.
@@ -34,12 +38,20 @@ __device__ __forceinline__ v4i lds_read16(uint32_t at) {
   return *(__attribute__((address_space(3))) const v4i*)(uintptr_t)at;
 }
 
-template <int D, int FMT>
+__device__ __forceinline__ void lds_write16(uint32_t at, v4i v) {
+  *(__attribute__((address_space(3))) v4i*)(uintptr_t)at = v;
+}
+
+// ONE: blocks hold whole tiles, so a tile has one block; otherwise each of its
+// four granules of 16 keys has its own.
+template <int D, int FMT, bool ONE>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
+  constexpr int NB = ONE ? 1 : 4;
   constexpr int J = D / 32;   // 32-dimension steps of the logits
   constexpr int DT = D / 32;  // 32-dimension tiles of the output
   constexpr int kTileBytes = kAttnTile * D;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][kTileBytes];  // [buffer][keys, values]
+  __shared__ int found[kWaves];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r32 = lane & 31, h = lane >> 5;
@@ -76,6 +88,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   const int whi = idle ? 0 : (a.causal ? min(s.len, s.start + wrow1 / G + 1) : s.len);
   const int wlo = a.window ? s.start + wrow0 / G - a.window + 1 : 0;
 
+  // the keys that every row of the workgroup sees
+  const int row_last = min(row0 + kAttnTileRows, rows) - 1;
+  const int all_hi = a.causal ? min(s.len, s.start + row0 / G + 1) : s.len;
+  const int all_lo = a.window ? s.start + row_last / G - a.window + 1 : 0;
+
   v16f o[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -84,19 +101,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   float m = kNoRef, l = 0.0f;
   int bref = kNoBias;
 
-  // blocks and biases of a tile's four granules of 16 keys, the same in every
-  // lane; read a tile ahead, so that nothing waits for them before the tile's own
-  // wait does
+  // blocks and biases of a tile, the same in every lane; read a tile ahead, so
+  // that nothing waits for them before the tile's own wait does
   struct Blocks {
-    int b[4];
+    int b[NB];
   };
   struct Biases {
-    int k[4], v[4];
+    int k[NB], v[NB];
   };
   auto blocks_of = [&](int T) {
     Blocks r;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < NB; ++g) {
       const int pos = T + 16 * g;
       r.b[g] = pos < kend ? kv_block(a.cache, a.batch, at.seq, pos >> a.block_shift) : -1;
     }
@@ -105,14 +121,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   auto biases_of = [&](const Blocks& b) {
     Biases r;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < NB; ++g) {
       const int64_t c = (int64_t)max(b.b[g], 0) * H + at.head;
       r.k[g] = a.cache.k_bias[c];
-      r.v[g] = b.b[g] < 0 ? kNoBias : a.cache.v_bias[c];
+      r.v[g] = a.cache.v_bias[c];
     }
     return r;
   };
-  auto pick = [](const int (&v)[4], int g) { return g < 2 ? (g == 0 ? v[0] : v[1]) : (g == 2 ? v[2] : v[3]); };
+  auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  // granule g's entry
+  auto pick = [](const int (&v)[NB], int g) {
+    if constexpr (ONE) return v[0];
+    else return g < 2 ? (g == 0 ? v[0] : v[1]) : (g == 2 ? v[2] : v[3]);
+  };
   const uint32_t ring0 = lds_addr(ring);
   // this wave's quarter of a tile: D / 64 KB of keys and of values
   auto issue = [&](int T, const Blocks& b, int buf) {
@@ -143,32 +164,77 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 #pragma unroll
   for (int sub = 0; sub < 2; ++sub) vfrag[sub] = kTileBytes + r32 * 64 + (((2 * sub + h) ^ ((r32 >> 2) & 3)) << 4);
 
-  Blocks nb = blocks_of(kbeg);
-  issue(kbeg, nb, 0);
-  Biases nbias = biases_of(nb);
-  Blocks cur = nb;
-  nb = blocks_of(kbeg + kAttnTile);
-  int buf = 0;
-  for (int T = kbeg; T < kend; T += kAttnTile, buf ^= 1) {
-    wait_all();
-    bare_barrier();  // this tile is whole, and every wave is done with the other buffer
-    Blocks blocks;
-    Biases bias;
+  // No code of a slot that a row does not see may turn 0 * code into NaN.  So a
+  // tile that some row of the workgroup does not see whole is searched for NaN
+  // (and infinity) codes of values; if it holds any, the outputs of the rows
+  // that do see them become NaN -- counted by a product of visibility with "is
+  // bad" -- and then the codes become zeros, in LDS, for every wave.
+  auto clean = [&](int T, uint32_t values, const Blocks& blocks) {
+    uint32_t bad = 0;
+    const uint32_t mine = values + threadIdx.x * (kTileBytes / (64 * kWaves));
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      blocks.b[g] = __builtin_amdgcn_readfirstlane(cur.b[g]);
-      bias.k[g] = __builtin_amdgcn_readfirstlane(nbias.k[g]);
-      bias.v[g] = __builtin_amdgcn_readfirstlane(nbias.v[g]);
+    for (int i = 0; i < kTileBytes / (64 * kWaves); i += 16) {
+      const v4i w = lds_read16(mine + i);
+      bad |= bad_bytes<FMT>(w[0]) | bad_bytes<FMT>(w[1]) | bad_bytes<FMT>(w[2]) | bad_bytes<FMT>(w[3]);
     }
-    if (T + kAttnTile < kend) {
-      issue(T + kAttnTile, nb, buf ^ 1);
-      nbias = biases_of(nb);
-      cur = nb;
-      nb = blocks_of(T + 2 * kAttnTile);
+    const bool any = __any(bad != 0);
+    if (lane == 0) found[wave] = any;
+    __syncthreads();
+    if (found[0] | found[1] | found[2] | found[3]) {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const bool there = (h ? pick(blocks.b, 2 * sub + 1) : pick(blocks.b, 2 * sub)) >= 0;
+        v8h see[2];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = T + 32 * sub + 16 * h + e;
+          see[e >> 3][e & 7] = there && key >= lo && key < hi ? (_Float16)1.0f : (_Float16)0.0f;
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          __builtin_amdgcn_sched_barrier(0);
+          const v4i w = lds_read16(values - kTileBytes + vfrag[sub] + d * 32 * 64);
+          v16f n;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) n[e] = 0.0f;
+          n = __builtin_amdgcn_mfma_f32_32x32x16_f16(ones_f16(bad_bytes<FMT>(w[0]), bad_bytes<FMT>(w[1])), see[0], n, 0,
+                                                     0, 0);
+          n = __builtin_amdgcn_mfma_f32_32x32x16_f16(ones_f16(bad_bytes<FMT>(w[2]), bad_bytes<FMT>(w[3])), see[1], n, 0,
+                                                     0, 0);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] = n[e] > 0.0f ? NAN : o[d][e];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kTileBytes / (64 * kWaves); i += 16) {
+        v4i w = lds_read16(mine + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] &= ~bad_bytes<FMT>(w[e]);
+        lds_write16(mine + i, w);
+      }
     }
-    if (T >= whi || T + kAttnTile <= wlo) continue;  // nothing for this wave's rows
-    const uint32_t tile = ring0 + buf * 2 * kTileBytes;
+    __syncthreads();
+  };
 
+  // O and l times f, O at the value bias `low` (O is zero before the first one)
+  auto rescale = [&](float f, int low) {
+    l *= f;
+    const float fo = f * pow2_scale(low - bref);
+    bref = low;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] *= fo;
+  };
+  auto join = [](const v2h* p) {
+    return v8h{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+  };
+
+  // one tile for this wave's rows; masked: some row does not see all of it
+  auto consume = [&](bool masked, int T, uint32_t tile, const Blocks& blocks, const Biases& bias) {
+    auto seen = [&](int sub, int e) {
+      const int key = T + 32 * sub + 16 * h + e;
+      return (h ? pick(blocks.b, 2 * sub + 1) : pick(blocks.b, 2 * sub)) >= 0 && key >= lo && key < hi;
+    };
     v16f sacc[2];
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
@@ -182,104 +248,101 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
         sacc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16<FMT>(w[0], w[1]), q[j][0], sacc[sub], 0, 0, 0);
         sacc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16<FMT>(w[2], w[3]), q[j][1], sacc[sub], 0, 0, 0);
       }
-
-    const bool missing = blocks.b[0] < 0 || blocks.b[1] < 0 || blocks.b[2] < 0 || blocks.b[3] < 0;
-    const bool masked = missing || !__all(T + kAttnTile <= hi && T >= lo);
-    float t[2][16];
-    float top = -INFINITY;
+    if (masked) {
+      asm volatile("");  // a branch: as selects it would cost every tile
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sacc[sub][e] = seen(sub, e) ? sacc[sub][e] : -INFINITY;
+    }
+    int low = bref;
+#pragma unroll
+    for (int g = 0; g < NB; ++g) low = blocks.b[g] < 0 ? low : min(low, bias.v[g]);
+    if (low < bref) rescale(1.0f, low);
+    float kscale[2], vscale[2];
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      const float kscale = a.scale_log2 * pow2_scale(-(h ? bias.k[2 * sub + 1] : bias.k[2 * sub]));
-#pragma unroll
-      for (int e = 0; e < 16; ++e) t[sub][e] = sacc[sub][e] * kscale;
-      if (masked) {
-        const int first = T + 32 * sub + 16 * h;
-        const bool gone = (h ? blocks.b[2 * sub + 1] : blocks.b[2 * sub]) < 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (gone || first + e < lo || first + e >= hi) t[sub][e] = -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, t[sub][e]);
+      kscale[sub] = key_scale(a.scale_log2, h ? pick(bias.k, 2 * sub + 1) : pick(bias.k, 2 * sub));
+      // (a missing granule's bias is block 0's: anything)
+      vscale[sub] = pow2_scale(min(0, bref - (h ? pick(bias.v, 2 * sub + 1) : pick(bias.v, 2 * sub))) + kHead<FMT>);
     }
-    top = swap32_max(top);
-    const bool move = top > m + kLazy;
-    if (__any(move)) {
-      const float to = move ? top - kShift : m;
-      const float f = __builtin_amdgcn_exp2f(m - to);
-      m = to;
-      l *= f;
+    // Probabilities against the reference as it is; their sum tells whether a
+    // logit has outgrown it (it always has in a row's first tile), and only
+    // then are the maxima taken and the tile done again.
+    v2h p[2][8];
+    float part;
+    auto probabilities = [&] {
+      part = 0.0f;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] *= f;
-    }
-    v8h p[2][2];
+      for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+        for (int e = 0; e < 8; ++e) {
+          v2f t;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        t[sub][e] = __builtin_amdgcn_exp2f(t[sub][e] - m);
-        l += t[sub][e];
-      }
-      p[sub][0] = pack_f16(t[sub]);
-      p[sub][1] = pack_f16(t[sub] + 8);
-    }
-
-    const int low = min(min(bias.v[0], bias.v[1]), min(bias.v[2], bias.v[3]));
-    if (low < bref) {
-      if (bref != kNoBias) {
-        const float f = pow2_scale(low - bref);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= f;
-      }
-      bref = low;
-    }
-    uint32_t bad = 0;
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const int vbias = h ? bias.v[2 * sub + 1] : bias.v[2 * sub];
-      const float vscale = pow2_scale(min(bref, 1000) - min(vbias, 1000) + kHead<FMT>);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        v4i w = lds_read16(tile + vfrag[sub] + d * 32 * 64);
-        if (masked) {  // no code of an invisible slot may turn 0 * code into NaN
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b = bad_bytes<FMT>(w[e]);
-            bad |= b;
-            w[e] &= ~b;
-          }
+          for (int c = 0; c < 2; ++c)
+            t[c] = __builtin_amdgcn_exp2f(fmaf(sacc[sub][2 * e + c], kscale[sub], -m));
+          p[sub][e] = __builtin_convertvector(t, v2h);
+          part += t[0];  // of the fp32 values: the sum is held to fp32's precision
+          part += t[1];
         }
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[0], w[1], vscale), p[sub][0], o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[2], w[3], vscale), p[sub][1], o[d], 0, 0, 0);
-      }
-    }
-    if (masked && __any(bad != 0)) {
-      // a NaN value reaches the rows that see its token: counted by a product
-      // of visibility with "is bad"
+    };
+    probabilities();
+    if (__any(!(part <= kMostPart))) {
+      float top = -INFINITY;
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
-        const int first = T + 32 * sub + 16 * h;
-        const bool gone = (h ? blocks.b[2 * sub + 1] : blocks.b[2 * sub]) < 0;
-        v8h see[2];
+        float s = sacc[sub][0];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          see[e >> 3][e & 7] = gone || first + e < lo || first + e >= hi ? (_Float16)0.0f : (_Float16)1.0f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const v4i w = lds_read16(tile + vfrag[sub] + d * 32 * 64);
-          v16f n;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) n[e] = 0.0f;
-          n = __builtin_amdgcn_mfma_f32_32x32x16_f16(ones_f16(bad_bytes<FMT>(w[0]), bad_bytes<FMT>(w[1])), see[0], n, 0,
-                                                     0, 0);
-          n = __builtin_amdgcn_mfma_f32_32x32x16_f16(ones_f16(bad_bytes<FMT>(w[2]), bad_bytes<FMT>(w[3])), see[1], n, 0,
-                                                     0, 0);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (n[e] > 0.0f) o[d][e] = NAN;
-        }
+        for (int e = 1; e < 16; ++e) s = raw_max(s, sacc[sub][e]);
+        top = fmaxf(top, s * kscale[sub]);
       }
+      top = swap32_max(top);
+      const float to = top - kShift > m ? top - kShift : m;
+      const float f = __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      rescale(f, bref);
+      probabilities();
     }
+    l += part;
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const v4i w = lds_read16(tile + vfrag[sub] + d * 32 * 64);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[0], w[1], vscale[sub]), join(p[sub]), o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[2], w[3], vscale[sub]), join(p[sub] + 4), o[d], 0, 0, 0);
+      }
+  };
+
+  Blocks cur = blocks_of(kbeg);
+  Biases nbias = biases_of(cur);
+#pragma unroll
+  for (int g = 0; g < NB; ++g) cur.b[g] = scalar(cur.b[g]);
+  issue(kbeg, cur, 0);
+  Blocks nb = blocks_of(kbeg + kAttnTile);
+  int buf = 0;
+  for (int T = kbeg; T < kend; T += kAttnTile, buf ^= 1) {
+    wait_all();
+    bare_barrier();  // this tile is whole, and every wave is done with the other buffer
+    const Blocks blocks = cur;
+    Biases bias;
+#pragma unroll
+    for (int g = 0; g < NB; ++g) bias.k[g] = scalar(nbias.k[g]), bias.v[g] = scalar(nbias.v[g]);
+    if (T + kAttnTile < kend) {
+#pragma unroll
+      for (int g = 0; g < NB; ++g) cur.b[g] = scalar(nb.b[g]);
+      issue(T + kAttnTile, cur, buf ^ 1);
+      nbias = biases_of(cur);
+      nb = blocks_of(T + 2 * kAttnTile);
+    }
+    const uint32_t tile = ring0 + buf * 2 * kTileBytes;
+    bool there = true;
+#pragma unroll
+    for (int g = 0; g < NB; ++g) there = there && blocks.b[g] >= 0;
+    if (!there || T + kAttnTile > all_hi || T < all_lo) clean(T, tile + kTileBytes, blocks);
+    if (T >= whi || T + kAttnTile <= wlo) continue;  // nothing for this wave's rows
+    const bool whole = there && T + kAttnTile <= hi && T >= lo;
+    consume(!__all(whole), T, tile, blocks, bias);
   }
   wait_vmcnt<0>();
 
@@ -312,10 +375,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 
 template <int D>
 void run(const AttnArgs& a, uint32_t groups, hipStream_t stream) {
-  if (a.cache.fmt == FP8_E4M3)
-    hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E4M3>), dim3(groups), dim3(64 * kWaves), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E5M2>), dim3(groups), dim3(64 * kWaves), 0, stream, a);
+  const dim3 grid(groups), block(64 * kWaves);
+  const bool one = a.cache.block_size >= kAttnTile;
+  if (a.cache.fmt == FP8_E4M3) {
+    if (one) hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E4M3, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E4M3, false>), grid, block, 0, stream, a);
+  } else {
+    if (one) hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E5M2, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attn_tile_kernel<D, FP8_E5M2, false>), grid, block, 0, stream, a);
+  }
 }
 
 }  // namespace
