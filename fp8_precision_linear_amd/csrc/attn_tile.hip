@@ -135,21 +135,37 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
     else return g < 2 ? (g == 0 ? v[0] : v[1]) : (g == 2 ? v[2] : v[3]);
   };
   const uint32_t ring0 = lds_addr(ring);
-  // this wave's quarter of a tile: D / 64 KB of keys and of values
-  auto issue = [&](int T, const Blocks& b, int buf) {
-    const uint32_t kdst = ring0 + buf * 2 * kTileBytes, vdst = kdst + kTileBytes;
+  // This wave's quarter of a tile's keys (values), D / 64 KB: KB i holds key rows
+  // (dimensions) 4 i KBs past the first's, whose swizzle is the same -- but for
+  // D = 256, where every other i is 16 rows on, in the other half of fk.
+  const int kr = wave * (1024 / D) + lane / (D / 16), kc = (lane % (D / 16)) ^ fk<D>(kr);
+  const int vd = wave * 16 + lane / 4, vc = (lane & 3) ^ ((vd >> 2) & 3);
+  const uint32_t k_lane = kr * D + 16 * kc, v_lane = vd * BS + 16 * vc;
+  auto issue_k = [&](int T, const Blocks& b, int buf) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const int piece = wave + kWaves * i;
-      {
-        const int r = piece * (1024 / D) + lane / (D / 16), c = (lane % (D / 16)) ^ fk<D>(r);
+      const uint32_t to = ring0 + buf * 2 * kTileBytes + (wave + kWaves * i) * 1024;
+      const int turn = D == 256 && (i & 1) ? 8 : 0;
+      if constexpr (ONE) {
+        const int64_t cell = (int64_t)max(b.b[0], 0) * H + at.head;
+        dma16(a.cache.k + (cell * BS + (T & (BS - 1)) + 4096 / D * i) * D, k_lane ^ (16 * turn), to);
+      } else {
+        const int r = kr + 4096 / D * i;
         const int64_t cell = (int64_t)max(pick(b.b, r >> 4), 0) * H + at.head;
-        dma16(a.cache.k + (cell * BS + ((T + r) & (BS - 1))) * D + 16 * c, kdst + piece * 1024);
+        dma16(a.cache.k + (cell * BS + ((T + r) & (BS - 1))) * D + 16 * (kc ^ turn), to);
       }
-      {
-        const int d = piece * 16 + lane / 4, c = (lane & 3) ^ ((d >> 2) & 3);
-        const int64_t cell = (int64_t)max(pick(b.b, c), 0) * H + at.head;
-        dma16(a.cache.v + (cell * D + d) * BS + ((T + 16 * c) & (BS - 1)), vdst + piece * 1024);
+    }
+  };
+  auto issue_v = [&](int T, const Blocks& b, int buf) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint32_t to = ring0 + (2 * buf + 1) * kTileBytes + (wave + kWaves * i) * 1024;
+      if constexpr (ONE) {
+        const int64_t cell = (int64_t)max(b.b[0], 0) * H + at.head;
+        dma16(a.cache.v + (cell * D + 64 * i) * BS + (T & (BS - 1)), v_lane, to);
+      } else {
+        const int64_t cell = (int64_t)max(pick(b.b, vc), 0) * H + at.head;
+        dma16(a.cache.v + (cell * D + vd + 64 * i) * BS + ((T + 16 * vc) & (BS - 1)), to);
       }
     }
   };
@@ -158,11 +174,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   // key 16 ((r32 >> 2) & 1) + 4 (r32 >> 3) + (r32 & 3): S^T's result v of a
   // lane is then key 32 sub + 16 h + v.
   const int krow = 16 * ((r32 >> 2) & 1) + 4 * (r32 >> 3) + (r32 & 3);
-  uint32_t kfrag[J], vfrag[2];
-#pragma unroll
-  for (int j = 0; j < J; ++j) kfrag[j] = krow * D + (((2 * j + h) ^ fk<D>(krow)) << 4);
-#pragma unroll
-  for (int sub = 0; sub < 2; ++sub) vfrag[sub] = kTileBytes + r32 * 64 + (((2 * sub + h) ^ ((r32 >> 2) & 3)) << 4);
+  // chunk 2 j + h of its row, and chunk 2 sub + h: the swizzle is an XOR, so j
+  // and sub are too
+  const uint32_t kfrag = krow * D + ((h ^ fk<D>(krow)) << 4);
+  const uint32_t vfrag = kTileBytes + r32 * 64 + ((h ^ ((r32 >> 2) & 3)) << 4);
 
   // No code of a slot that a row does not see may turn 0 * code into NaN.  So a
   // tile that some row of the workgroup does not see whole is searched for NaN
@@ -193,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           __builtin_amdgcn_sched_barrier(0);
-          const v4i w = lds_read16(values - kTileBytes + vfrag[sub] + d * 32 * 64);
+          const v4i w = lds_read16(((values - kTileBytes + vfrag) ^ (32 * sub)) + d * 32 * 64);
           v16f n;
 #pragma unroll
           for (int e = 0; e < 16; ++e) n[e] = 0.0f;
@@ -235,6 +250,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
       const int key = T + 32 * sub + 16 * h + e;
       return (h ? pick(blocks.b, 2 * sub + 1) : pick(blocks.b, 2 * sub)) >= 0 && key >= lo && key < hi;
     };
+    // LDS reads well ahead of their use: all keys before the first product, all
+    // values before the probabilities (each wait on a read costs more than the
+    // product it feeds)
+    v4i kw[J][2], vw[2][DT];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) kw[j][sub] = lds_read16(((tile + kfrag) ^ (32 * j)) + sub * 32 * D);
+    __builtin_amdgcn_sched_barrier(0);
+    // the wave in a product goes first: its widening feeds the matrix core while
+    // the SIMD's other wave forms probabilities (prompts 426 -> 406 us)
+    __builtin_amdgcn_s_setprio(1);
     v16f sacc[2];
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
@@ -243,11 +270,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const v4i w = lds_read16(tile + kfrag[j] + sub * 32 * D);
-        sacc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16<FMT>(w[0], w[1]), q[j][0], sacc[sub], 0, 0, 0);
-        sacc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16<FMT>(w[2], w[3]), q[j][1], sacc[sub], 0, 0, 0);
-      }
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+          sacc[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16<FMT>(kw[j][sub][2 * c], kw[j][sub][2 * c + 1]),
+                                                              q[j][c], sacc[sub], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vw[sub][d] = lds_read16(((tile + vfrag) ^ (32 * sub)) + d * 32 * 64);
+    __builtin_amdgcn_sched_barrier(0);
     if (masked) {
       asm volatile("");  // a branch: as selects it would cost every tile
 #pragma unroll
@@ -304,21 +338,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
       probabilities();
     }
     l += part;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const v4i w = lds_read16(tile + vfrag[sub] + d * 32 * 64);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[0], w[1], vscale[sub]), join(p[sub]), o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16<FMT>(w[2], w[3], vscale[sub]), join(p[sub] + 4), o[d], 0, 0, 0);
+      for (int c = 0; c < 2; ++c) {
+        const v8h pc = join(p[sub] + 4 * c);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              widen_f16<FMT>(vw[sub][d][2 * c], vw[sub][d][2 * c + 1], vscale[sub]), pc, o[d], 0, 0, 0);
       }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   Blocks cur = blocks_of(kbeg);
   Biases nbias = biases_of(cur);
 #pragma unroll
   for (int g = 0; g < NB; ++g) cur.b[g] = scalar(cur.b[g]);
-  issue(kbeg, cur, 0);
+  issue_k(kbeg, cur, 0);
+  issue_v(kbeg, cur, 0);
   Blocks nb = blocks_of(kbeg + kAttnTile);
   int buf = 0;
   for (int T = kbeg; T < kend; T += kAttnTile, buf ^= 1) {
@@ -331,7 +370,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
     if (T + kAttnTile < kend) {
 #pragma unroll
       for (int g = 0; g < NB; ++g) cur.b[g] = scalar(nb.b[g]);
-      issue(T + kAttnTile, cur, buf ^ 1);
+      issue_k(T + kAttnTile, cur, buf ^ 1);
+      issue_v(T + kAttnTile, cur, buf ^ 1);
       nbias = biases_of(cur);
       nb = blocks_of(T + 2 * kAttnTile);
     }

@@ -153,6 +153,13 @@ __device__ __forceinline__ uint32_t cast4_f32(uint4 v, bool hw, int32_t b, uint3
 }
 
 
+// Two fp32 values -> two bf16 words, rounded to nearest even (v_cvt_pk_bf16_f32;
+// NaN stays NaN).
+typedef float hw_v2f __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((hw_v2f{a, b}), hw_v2bf));
+}
+
 // Four fp32 values -> four codes of v * 2^b for any b, branch-free but for NaN:
 // scaled first (exact, as in fp8_code), clamped to fmt_max in magnitude (which
 // also saturates infinities), converted at unit scale; a NaN, which the clamp

@@ -32,14 +32,7 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, float* v) {
   }
 }
 
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;
-  return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
-}
-__device__ __forceinline__ uint2 bf16x4(const float* v) {
-  return make_uint2(bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16));
-}
+__device__ __forceinline__ uint2 bf16x4(const float* v) { return make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3])); }
 
 struct Rope {
   const float* cos;  // null: no rotation

@@ -43,4 +43,14 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds_kb) {
       : "memory", "m0");
 }
 
+// The same from a wave-uniform base and a 32-bit byte offset per lane.
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t offset, uint32_t lds_kb) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds_kb))
+      : "memory", "m0");
+}
+
 }  // namespace fp8lin

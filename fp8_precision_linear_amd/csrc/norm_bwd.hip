@@ -45,21 +45,47 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
   }
   uint32_t top = 0;
   int parity = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+  // a row's inputs, loaded one row ahead (the sixteen-wave shape has no
+  // registers for that: its loads stand where they are used)
+  constexpr bool kAhead = W < 16;
+  Raw<YT, V> ry[U];
+  Raw<HT, V> rh[U], rd[U];
+  float rs_next = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= a.rows) return;
     const int64_t base = row * d;
-    float g[U][V], xh[U][V];
+    rs_next = a.rstd[row];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = (u * kLanes + t) * V;
       if (j < d) {
-        load_stream<YT, V>(a.dy, base + j, g[u]);
-        load_stream<HT, V>(a.h, base + j, xh[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[u][e] = xh[u][e] = 0.0f;
+        ry[u] = load_raw<YT, V>(a.dy, base + j);
+        rh[u] = load_raw<HT, V>(a.h, base + j);
+        if (kAhead && a.dh) rd[u] = load_raw<HT, V>(a.dh, base + j);
       }
     }
-    const float rs = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  if constexpr (kAhead) fetch(row);
+  for (; row < a.rows; row += step) {
+    if constexpr (!kAhead) fetch(row);
+    const int64_t base = row * d;
+    const float rs = rs_next;
+    float g[U][V], xh[U][V];
+    Raw<HT, V> rd_now[kAhead ? U : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = (u * kLanes + t) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) g[u][e] = xh[u][e] = 0.0f;
+      if (j < d) {
+        unpack<YT, V>(ry[u], g[u]);
+        unpack<HT, V>(rh[u], xh[u]);
+        if constexpr (kAhead) rd_now[u] = rd[u];
+      }
+    }
+    if constexpr (kAhead) fetch(row + step);
     float c = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -90,10 +116,11 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = rs * (g[u][e] - xh[u][e] * c);
         if (a.dh) {
-          float r[V];
-          load_stream<HT, V>(a.dh, base + j, r);
+          float past[V];
+          if constexpr (kAhead) unpack<HT, V>(rd_now[u], past);
+          else load_stream<HT, V>(a.dh, base + j, past);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += r[e];
+          for (int e = 0; e < V; ++e) o[e] += past[e];
         }
         round_to<HT, V>(o);
         store_as<HT, V>(a.dx, base + j, o);

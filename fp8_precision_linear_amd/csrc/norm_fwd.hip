@@ -41,6 +41,19 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
   int parity = 0;
   int32_t bias = 0;
   if constexpr (OUT == kOutCodes) bias = *a.bias_in;
+  // the weight stays in registers over the workgroup's rows (where sixteen
+  // waves leave enough), its loads in flight with the first row's
+  constexpr bool kKeepW = W < 16;
+  float w[kKeepW ? U : 1][V];
+  if constexpr (kKeepW) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = (u * kLanes + t) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[u][e] = 0.0f;
+      if (j < d) load_cached<V>(a.w, a.w_dtype, j, w[u]);
+    }
+  }
   for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.rows; row += (int64_t)gridDim.x * kRows) {
     const int64_t base = row * d;
     float h[U][V];
@@ -84,16 +97,13 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
     for (int u = 0; u < U; ++u) {
       const int j = (u * kLanes + t) * V;
       if (j < d) {
-        float w[V];
-        load_cached<V>(a.w, a.w_dtype, j, w);
+        float* wu = w[kKeepW ? u : 0];
+        if constexpr (!kKeepW) load_cached<V>(a.w, a.w_dtype, j, w[0]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[u][e] = h[u][e] * rstd * w[e];
-          if constexpr (OUT == kOutBf16)
-            m = max(m, (bf16_bits(h[u][e]) & 0x7FFFu) << 16);
-          else
-            m = max(m, __float_as_uint(h[u][e]) & 0x7FFFFFFFu);
-        }
+        for (int e = 0; e < V; ++e) h[u][e] = h[u][e] * rstd * wu[e];
+        if constexpr (OUT == kOutBf16) round_to<FP8_IN_BF16, V>(h[u]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = max(m, __float_as_uint(h[u][e]) & 0x7FFFFFFFu);
         if constexpr (OUT == kOutBf16) store_as<FP8_IN_BF16, V>(a.y, base + j, h[u]);
         if constexpr (OUT == kOutCodes) store_codes<V>(static_cast<uint8_t*>(a.y), base + j, h[u], a.fmt, bias);
       }
@@ -123,34 +133,71 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
 }
 
 // The second half of fp8_rmsnorm_quantize: the tensor's amax from every row's,
-// the bias from it, and the codes of y formed again from h.  The rows are
-// walked from the last one: what the first half wrote last is still cached.
-template <int V>
-__global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, int h_dtype, const float* rstd,
-                                                        const void* w, int w_dtype, int64_t rows, int d,
-                                                        const uint32_t* row_amax, int fmt, int32_t margin,
-                                                        uint8_t* y, uint32_t* amax, int32_t* bias) {
+// the bias from it, and the codes of y formed again from h.  A workgroup takes
+// 256 V columns, whose weights its lanes keep, of every `groups`-th row, four
+// rows in flight; the first ones' loads stand before the amax.  Rows are walked
+// from the last one: what the first half wrote last is still cached.
+constexpr int kCastRows = 4;
+template <int HT, int V>
+__global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const float* rstd, const void* w, int w_dtype,
+                                                        int64_t rows, int d, int col_blocks, int groups,
+                                                        const uint32_t* row_amax, int fmt, int32_t margin, uint8_t* y,
+                                                        uint32_t* amax, int32_t* bias) {
   __shared__ uint32_t part[4];
+  const int t = threadIdx.x;
+  const int j = ((int)(blockIdx.x % col_blocks) * 256 + t) * V;
+  const int64_t group = blockIdx.x / col_blocks;
+  const bool live = j < d;
+  float ww[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) ww[e] = 0.0f;
+  if (live) load_cached<V>(w, w_dtype, j, ww);
+  Raw<HT, V> x[kCastRows];
+  float rs[kCastRows];
+  auto fetch = [&](int64_t k) {
+#pragma unroll
+    for (int q = 0; q < kCastRows; ++q) {
+      const int64_t at = k + (int64_t)q * groups;
+      if (live && at < rows) {
+        const int64_t row = rows - 1 - at;
+        rs[q] = rstd[row];
+        using E = std::conditional_t<HT == FP8_IN_FP32, float, uint16_t>;
+        x[q] = *reinterpret_cast<const Raw<HT, V>*>(static_cast<const E*>(h) + row * d + j);
+      }
+    }
+  };
+  fetch(group);
   uint32_t m = 0;
-  for (int64_t i = threadIdx.x; i < rows; i += 256) m = max(m, row_amax[i]);
+  int64_t done = 0;
+  if (((uintptr_t)row_amax & 15u) == 0) {
+    const uint4* v = reinterpret_cast<const uint4*>(row_amax);
+#pragma unroll 4
+    for (int64_t i = t; i < rows / 4; i += 256) {
+      const uint4 q = v[i];
+      m = max(max(m, max(q.x, q.y)), max(q.z, q.w));
+    }
+    done = rows / 4 * 4;
+  }
+  for (int64_t i = done + t; i < rows; i += 256) m = max(m, row_amax[i]);
   m = row_max<4>(m, part);
   const int32_t b = bias_from_amax_bits(m, fmt, margin);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  if (blockIdx.x == 0 && t == 0) {
     *amax = m;
     *bias = b;
   }
-  for (int64_t k = blockIdx.x; k < rows; k += gridDim.x) {
-    const int64_t row = rows - 1 - k;
-    const float rs = rstd[row];
-#pragma unroll 4
-    for (int j = threadIdx.x * V; j < d; j += 256 * V) {
-      float v[V], ww[V];
-      load_cached<V>(h, h_dtype, row * d + j, v);
-      load_cached<V>(w, w_dtype, j, ww);
+  for (int64_t k = group; k < rows; k += (int64_t)kCastRows * groups) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = v[e] * rs * ww[e];
-      store_codes<V>(y, row * d + j, v, fmt, b);
+    for (int q = 0; q < kCastRows; ++q) {
+      const int64_t at = k + (int64_t)q * groups;
+      if (live && at < rows) {
+        float v[V];
+        unpack<HT, V>(x[q], v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = v[e] * rs[q] * ww[e];
+        store_codes<V>(y, (rows - 1 - at) * d + j, v, fmt, b);
+      }
     }
+    fetch(k + (int64_t)kCastRows * groups);
   }
 }
 
@@ -224,13 +271,27 @@ hipError_t launch_norm_quantize(const NormProblem& p, int fmt, int32_t margin, u
   if (p.rows == 1) return hipGetLastError();
   const void* h = p.r ? p.h : p.x;
   const int h_dtype = p.r ? p.r_dtype : p.x_dtype;
-  const int64_t blocks = p.rows < kMaxBlocks ? (p.rows > 0 ? p.rows : 1) : kMaxBlocks;
-  if (p.d % 4 == 0)
-    hipLaunchKernelGGL(norm_cast_kernel<4>, dim3((uint32_t)blocks), dim3(256), 0, stream, h, h_dtype, p.rstd, p.w,
-                       p.w_dtype, p.rows, (int)p.d, row_amax, fmt, margin, y, amax, bias);
-  else
-    hipLaunchKernelGGL(norm_cast_kernel<1>, dim3((uint32_t)blocks), dim3(256), 0, stream, h, h_dtype, p.rstd, p.w,
-                       p.w_dtype, p.rows, (int)p.d, row_amax, fmt, margin, y, amax, bias);
+  const int V = p.d % 4 == 0 ? 4 : 1;
+  const int col_blocks = (int)((p.d + 256 * V - 1) / (256 * V));
+  // rows shared out so that kMaxBlocks workgroups run, each with whole batches
+  // of kCastRows where there are rows enough
+  int64_t groups = (p.rows + kCastRows - 1) / kCastRows;
+  const int64_t most = kMaxBlocks / col_blocks > 0 ? kMaxBlocks / col_blocks : 1;
+  groups = groups < most ? groups : most;
+  if (groups == 0) groups = 1;
+  auto run = [&](auto ht, auto v) {
+    hipLaunchKernelGGL((norm_cast_kernel<ht.value, v.value>), dim3((uint32_t)(groups * col_blocks)), dim3(256), 0,
+                       stream, h, p.rstd, p.w, p.w_dtype, p.rows, (int)p.d, col_blocks, (int)groups, row_amax, fmt,
+                       margin, y, amax, bias);
+  };
+  using std::integral_constant;
+  if (h_dtype == FP8_IN_FP32) {
+    if (V == 4) run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, 4>{});
+    else run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, 1>{});
+  } else {
+    if (V == 4) run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, 4>{});
+    else run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, 1>{});
+  }
   return hipGetLastError();
 }
 

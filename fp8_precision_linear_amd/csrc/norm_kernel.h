@@ -30,31 +30,35 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNone = -1;  // "no residual" as a type
 
-// How a row's elements are loaded: V consecutive per lane and unit.
-// DT: FP8_IN_BF16 or FP8_IN_FP32.  Streaming loads: each input is read once.
+// V consecutive elements of type DT (FP8_IN_BF16 or FP8_IN_FP32) as they lie in
+// memory, loaded past the caches (each input is read once), and as fp32.
+template <int DT, int V>
+using Raw = std::conditional_t<DT == FP8_IN_FP32, std::conditional_t<V == 4, f32x4, float>,
+                               std::conditional_t<V == 4, u32x2, uint16_t>>;
+template <int DT, int V>
+__device__ __forceinline__ Raw<DT, V> load_raw(const void* p, int64_t i) {
+  using E = std::conditional_t<DT == FP8_IN_FP32, float, uint16_t>;
+  return __builtin_nontemporal_load(reinterpret_cast<const Raw<DT, V>*>(static_cast<const E*>(p) + i));
+}
+template <int DT, int V>
+__device__ __forceinline__ void unpack(const Raw<DT, V>& r, float (&v)[V]) {
+  if constexpr (DT == FP8_IN_FP32 && V == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r[e];
+  } else if constexpr (DT == FP8_IN_FP32) {
+    v[0] = r;
+  } else if constexpr (V == 4) {
+    v[0] = __uint_as_float(r[0] << 16);
+    v[1] = __uint_as_float(r[0] & 0xFFFF0000u);
+    v[2] = __uint_as_float(r[1] << 16);
+    v[3] = __uint_as_float(r[1] & 0xFFFF0000u);
+  } else {
+    v[0] = __uint_as_float((uint32_t)r << 16);
+  }
+}
 template <int DT, int V>
 __device__ __forceinline__ void load_stream(const void* p, int64_t i, float (&v)[V]) {
-  if constexpr (DT == FP8_IN_FP32) {
-    const float* q = static_cast<const float*>(p) + i;
-    if constexpr (V == 4) {
-      const f32x4 t = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(q));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = t[e];
-    } else {
-      v[0] = __builtin_nontemporal_load(q);
-    }
-  } else {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-    if constexpr (V == 4) {
-      const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q));
-      v[0] = __uint_as_float(t[0] << 16);
-      v[1] = __uint_as_float(t[0] & 0xFFFF0000u);
-      v[2] = __uint_as_float(t[1] << 16);
-      v[3] = __uint_as_float(t[1] & 0xFFFF0000u);
-    } else {
-      v[0] = __uint_as_float((uint32_t)__builtin_nontemporal_load(q) << 16);
-    }
-  }
+  unpack<DT, V>(load_raw<DT, V>(p, i), v);
 }
 
 // Ordinary loads, the type chosen at run time (the weight, and h on its second
@@ -83,13 +87,6 @@ __device__ __forceinline__ void load_cached(const void* p, int dt, int64_t i, fl
   }
 }
 
-// fp32 -> bf16 bits, round to nearest even (overflow to inf); NaN stays NaN.
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (b >> 16) | 0x40u;
-  return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
-}
-
 template <int DT, int V>
 __device__ __forceinline__ void store_as(void* p, int64_t i, const float (&v)[V]) {
   if constexpr (DT == FP8_IN_FP32) {
@@ -101,10 +98,9 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, const float (&v)[V]
   } else {
     uint16_t* q = static_cast<uint16_t*>(p) + i;
     if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(q) = make_uint2(bf16_bits(v[0]) | (bf16_bits(v[1]) << 16),
-                                                bf16_bits(v[2]) | (bf16_bits(v[3]) << 16));
+      *reinterpret_cast<uint2*>(q) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
     else
-      *q = (uint16_t)bf16_bits(v[0]);
+      *q = (uint16_t)bf16x2(v[0], 0.0f);
   }
 }
 
@@ -112,8 +108,15 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, const float (&v)[V]
 template <int DT, int V>
 __device__ __forceinline__ void round_to(float (&v)[V]) {
   if constexpr (DT == FP8_IN_BF16) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __uint_as_float(bf16_bits(v[e]) << 16);
+    if constexpr (V == 4) {
+      const uint32_t a = bf16x2(v[0], v[1]), b = bf16x2(v[2], v[3]);
+      v[0] = __uint_as_float(a << 16);
+      v[1] = __uint_as_float(a & 0xFFFF0000u);
+      v[2] = __uint_as_float(b << 16);
+      v[3] = __uint_as_float(b & 0xFFFF0000u);
+    } else {
+      v[0] = __uint_as_float(bf16x2(v[0], 0.0f) << 16);
+    }
   }
 }
 
