@@ -160,41 +160,49 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((hw_v2f{a, b}), hw_v2bf));
 }
 
-// Four fp32 values -> four codes of v * 2^b for any b, branch-free but for NaN:
-// scaled first (exact, as in fp8_code), clamped to fmt_max in magnitude (which
-// also saturates infinities), converted at unit scale; a NaN, which the clamp
-// turned into fmt_max, gets its code afterwards.  The codes of fp8_code.
+// Four fp32 values -> the four codes of v * 2^b, as fp8_code gives them, for a
+// bias known beforehand.  The values are clamped to fmt_max * 2^-b, which is
+// the saturation (infinities too), and converted at the scale 2^-b; where that
+// or the bound is no normal number they are scaled first, exactly.  A NaN, which the clamp
+// would lose, shows in the sum of the four (as may infinities of both signs):
+// such a group takes fp8_code.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes4_f32(const float (&v)[4], int32_t b) {
+struct Coder {
   static_assert(kHwConvert<FMT>, "no hardware conversion for this format");
-  constexpr uint32_t kMax = FMT == FP8_E4M3 ? 0x43E00000u : 0x47600000u;  // 448, 57344
-  uint32_t bits[4];
-  float c[4];
-  bool nan = false;
+  int32_t b;
+  bool first;  // scale first
+  float bound, scale;
+  __device__ __forceinline__ explicit Coder(int32_t bias) : b(bias) {
+    first = b < (FMT == FP8_E4M3 ? -119 : -112) || b > kHwBiasMax;
+    bound = __uint_as_float(hw_bound_f32<FMT>(first ? 0 : b));
+    scale = __builtin_ldexpf(1.0f, first ? 0 : -b);
+  }
+  __device__ __forceinline__ uint32_t four(const float (&v)[4]) const {
+    float c[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bits[e] = __float_as_uint(__builtin_ldexpf(v[e], b));
-    const uint32_t m = bits[e] & 0x7FFFFFFFu;
-    nan |= m > 0x7F800000u;
-    c[e] = __uint_as_float((bits[e] & 0x80000000u) | min(m, kMax));
-  }
-  hw_v2s r = {0, 0};
-  if constexpr (FMT == FP8_E4M3) {
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[0], c[1], 1.0f, false);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[2], c[3], 1.0f, true);
-  } else {
-    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c[0], c[1], 1.0f, false);
-    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c[2], c[3], 1.0f, true);
-  }
-  uint32_t o = __builtin_bit_cast(uint32_t, r);
-  if (nan) {
+    for (int e = 0; e < 4; ++e) {
+      c[e] = v[e];
+      if (first) c[e] = __builtin_ldexpf(c[e], b);
+      c[e] = __builtin_amdgcn_fmed3f(c[e], -bound, bound);
+    }
+    hw_v2s r = {0, 0};
+    if constexpr (FMT == FP8_E4M3) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[0], c[1], scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c[2], c[3], scale, true);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c[0], c[1], scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c[2], c[3], scale, true);
+    }
+    uint32_t o = __builtin_bit_cast(uint32_t, r);
+    const float sum = (v[0] + v[1]) + (v[2] + v[3]);
+    if (__builtin_expect(sum != sum, 0)) {
+      o = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if ((bits[e] & 0x7FFFFFFFu) > 0x7F800000u)
-        o = (o & ~(0xFFu << (8 * e))) | ((0x7Fu | ((bits[e] >> 24) & 0x80u)) << (8 * e));
+      for (int e = 0; e < 4; ++e) o |= fp8_code<FMT>(__float_as_uint(v[e]), b) << (8 * e);
+    }
+    return o;
   }
-  return o;
-}
+};
 
 }  // namespace
 }  // namespace fp8lin

@@ -4,9 +4,9 @@
 // Append.  One workgroup per (sequence, touched block, head, keys | values)
 // holds that block's new tokens in registers between their largest magnitude
 // and the codes, so they are read once; the rotation is applied on the way.
-// Values change their order (tokens by dimensions -> dimensions by tokens)
-// through LDS bytes.  Further workgroups of the same launch rotate the
-// queries, one token each.  HBM-bound for prompts; for single tokens the
+// Values change their order (tokens by dimensions -> dimensions by tokens) four
+// by four codes in registers, then through LDS.  Further workgroups of the same
+// launch rotate the queries.  HBM-bound for prompts; for single tokens the
 // launch is most of the time.
 #include <type_traits>
 
@@ -34,30 +34,36 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, float* v) {
 
 __device__ __forceinline__ uint2 bf16x4(const float* v) { return make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3])); }
 
-struct Rope {
-  const float* cos;  // null: no rotation
-  const float* sin;
-  int rows;
-  int pairs;
-};
+// How keys and queries are rotated.
+constexpr int kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2;
 
 // A unit of a head's dimensions: two groups of four.  Rotated halves: [4u, +4)
 // and [D/2 + 4u, +4); otherwise [8u, +8).
-__device__ __forceinline__ int unit_lo(int u, bool halves) { return halves ? 4 * u : 8 * u; }
-__device__ __forceinline__ int unit_hi(int u, bool halves, int D) { return halves ? D / 2 + 4 * u : 8 * u + 4; }
+template <int D, int ROPE>
+__device__ __forceinline__ int unit_lo(int u) { return ROPE == kRopeHalves ? 4 * u : 8 * u; }
+template <int D, int ROPE>
+__device__ __forceinline__ int unit_hi(int u) { return ROPE == kRopeHalves ? D / 2 + 4 * u : 8 * u + 4; }
+
+struct Rope {
+  const float* cos;
+  const float* sin;
+  int rows;
+};
 
 // Rotates one unit of the token at `pos` in place.  Products and sums are
 // rounded separately, as the definition has them.
-__device__ __forceinline__ void rotate(float (&v)[8], int u, int pos, int D, const Rope& r) {
+template <int D, int ROPE>
+__device__ __forceinline__ void rotate(float (&v)[8], int u, int pos, const Rope& r) {
 #pragma clang fp contract(off)
+  if constexpr (ROPE == kRopeNone) return;
   const int64_t row = (int64_t)min(pos, r.rows - 1) * (D / 2);
   float c[4], s[4];
   load4<FP8_IN_FP32>(r.cos, row + 4 * u, c);
   load4<FP8_IN_FP32>(r.sin, row + 4 * u, s);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float& x = r.pairs ? v[2 * e] : v[e];
-    float& y = r.pairs ? v[2 * e + 1] : v[4 + e];
+    float& x = ROPE == kRopePairs ? v[2 * e] : v[e];
+    float& y = ROPE == kRopePairs ? v[2 * e + 1] : v[4 + e];
     const float a = x, b = y;
     const float ac = a * c[e], bs = b * s[e], bc = b * c[e], as = a * s[e];
     x = ac - bs;
@@ -79,6 +85,18 @@ __device__ __forceinline__ float code_value(uint32_t c) {
     return __builtin_amdgcn_cvt_f32_bf8((int)c, 0);
 }
 
+// The 4 x 4 bytes of r[0..3] (row i, byte j) transposed: r[j], byte i.
+__device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u);  // bytes 0 0 1 1 of rows 0 1
+  const uint32_t b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);  // bytes 2 2 3 3
+  const uint32_t c = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+  r[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  r[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  r[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  r[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
 struct AppendArgs {
   fp8_kv_cache_t cache;
   fp8_kv_batch_t batch;
@@ -91,81 +109,102 @@ struct AppendArgs {
   Rope rope;
   int blocks_per_seq;   // most blocks a sequence's new tokens touch
   int64_t kv_groups;    // workgroups of the keys and values; the others are the queries'
+  int q_tokens;         // tokens of one of the queries' workgroups
+  int q_groups;         // of them per sequence
 };
 
 constexpr int kUnits = 4;  // units a lane holds
 
-template <int DT, int FMT>
+template <int DT, int FMT, int D, int ROPE>
 __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
+  constexpr int kUpt = D / 8;       // units of a token and head
   extern __shared__ uint8_t lds[];  // values' codes, [D][block_size + 4]
   __shared__ uint32_t part[16];
   const int nt = blockDim.x, t = threadIdx.x;
-  const int D = a.cache.head_dim, BS = a.cache.block_size, H = a.cache.heads;
+  const int BS = a.cache.block_size, H = a.cache.heads;
 
-  if ((int64_t)blockIdx.x >= a.kv_groups) {  // one token's queries
-    const int64_t g = (int64_t)blockIdx.x - a.kv_groups;
-    const int i = (int)(g / a.batch.max_new), nth = (int)(g % a.batch.max_new);
+  if ((int64_t)blockIdx.x >= a.kv_groups) {  // some tokens' queries
+    const uint32_t g = (uint32_t)((int64_t)blockIdx.x - a.kv_groups);
+    const int i = g / a.q_groups, nth = (g % a.q_groups) * a.q_tokens;
     const KVSeq s = kv_seq_uniform(a.batch, BS, i);
-    if (nth >= s.n) return;
-    const bool halves = a.rope.cos && !a.rope.pairs;
-    const int64_t row = s.first + nth;
-    const int units = a.q_heads * (D / 8);
-    for (int x = t; x < units; x += nt) {
-      const int head = x / (D / 8), u = x % (D / 8);
-      const int lo = unit_lo(u, halves), hi = unit_hi(u, halves, D);
-      float v[8];
-      load4<DT>(a.q, row * a.q_stride + head * D + lo, v);
-      load4<DT>(a.q, row * a.q_stride + head * D + hi, v + 4);
-      if (a.rope.cos) rotate(v, u, s.start + nth, D, a.rope);
-      uint16_t* o = a.q_out + (row * a.q_heads + head) * D;
-      *reinterpret_cast<uint2*>(o + lo) = bf16x4(v);
-      *reinterpret_cast<uint2*>(o + hi) = bf16x4(v + 4);
+    const int count = min(a.q_tokens, s.n - nth);
+    if (count <= 0) return;
+    const int units = a.q_heads * kUpt;  // of a token
+    for (int tok = 0; tok < count; ++tok) {
+      const int64_t row = s.first + nth + tok;
+      for (int x0 = t; x0 < units; x0 += kUnits * nt) {
+        float v[kUnits][8];
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) {
+          const int x = x0 + q * nt, head = x / kUpt, u = x % kUpt;
+          if (x < units) {
+            load4<DT>(a.q, row * a.q_stride + head * D + unit_lo<D, ROPE>(u), v[q]);
+            load4<DT>(a.q, row * a.q_stride + head * D + unit_hi<D, ROPE>(u), v[q] + 4);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) {
+          const int x = x0 + q * nt, head = x / kUpt, u = x % kUpt;
+          if (x < units) {
+            rotate<D, ROPE>(v[q], u, s.start + nth + tok, a.rope);
+            uint16_t* o = a.q_out + (row * a.q_heads + head) * D;
+            *reinterpret_cast<uint2*>(o + unit_lo<D, ROPE>(u)) = bf16x4(v[q]);
+            *reinterpret_cast<uint2*>(o + unit_hi<D, ROPE>(u)) = bf16x4(v[q] + 4);
+          }
+        }
+      }
     }
     return;
   }
 
-  int64_t g = blockIdx.x;
+  uint32_t g = blockIdx.x;
   const bool values = g & 1;
   g >>= 1;
-  const int head = (int)(g % H);
+  const int head = g % H;
   g /= H;
-  const int nth_block = (int)(g % a.blocks_per_seq), i = (int)(g / a.blocks_per_seq);
+  const int nth_block = g % a.blocks_per_seq, i = g / a.blocks_per_seq;
   const KVSeq s = kv_seq_uniform(a.batch, BS, i);
   if (s.n == 0) return;
-  const int block_at = s.start / BS + nth_block;          // of the sequence
+  const int block_at = (s.start >> __builtin_ctz(BS)) + nth_block;          // of the sequence
   const int p0 = max(s.start, block_at * BS);             // first new position in the block
   const int p1 = min(s.start + s.n, block_at * BS + BS);  // one past the last
   if (p0 >= p1) return;
-  const int block = kv_block(a.cache, a.batch, i, block_at);
+  const int block = __builtin_amdgcn_readfirstlane(kv_block(a.cache, a.batch, i, block_at));
   if (block < 0) return;
-  const int slot0 = p0 - block_at * BS, count = p1 - p0;
+  const int slot0 = p0 - block_at * BS, slot1 = p1 - block_at * BS;
 
-  const bool rot = a.rope.cos && !values;
-  const bool halves = rot && !a.rope.pairs;
-  const void* src = values ? a.v : a.k;
-  const int64_t stride = values ? a.v_stride : a.k_stride;
-  const int64_t row0 = s.first + (p0 - s.start);
-  const int upt = D / 8, units = count * upt;
+  // This lane's units: keys, unit t + q * nt of the new tokens in order;
+  // values, dimensions u of the four tokens of an aligned quad of slots, which
+  // makes four codes of one dimension a word.
+  const int64_t row0 = s.first - s.start + (int64_t)block_at * BS;  // of slot 0
+  const int first = values ? slot0 >> 2 : slot0;
+  auto slot_of = [&](int q) { return values ? 4 * (first + t / kUpt) + q : first + (t + q * nt) / kUpt; };
+  const int u_value = t % kUpt;  // nt is a multiple of kUpt
   float v[kUnits][8];
   uint32_t m = 0;
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
-    const int x = q * nt + t;
-    if (x < units) {
-      const int tok = x / upt, u = x % upt;
-      const int64_t at = (row0 + tok) * stride + head * D;
-      load4<DT>(src, at + unit_lo(u, halves), v[q]);
-      load4<DT>(src, at + unit_hi(u, halves, D), v[q] + 4);
+    const int slot = slot_of(q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[q][e] = 0.0f;
+    if (slot >= slot0 && slot < slot1) {
+      if (values) {
+        const int64_t at = (row0 + slot) * a.v_stride + head * D + 8 * u_value;
+        load4<DT>(a.v, at, v[q]);
+        load4<DT>(a.v, at + 4, v[q] + 4);
+      } else {
+        const int64_t at = (row0 + slot) * a.k_stride + head * D;
+        load4<DT>(a.k, at + unit_lo<D, ROPE>(u_value), v[q]);
+        load4<DT>(a.k, at + unit_hi<D, ROPE>(u_value), v[q] + 4);
+      }
     }
   }
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
-    const int x = q * nt + t;
-    if (x < units) {
-      if (rot) rotate(v[q], x % upt, p0 + x / upt, D, a.rope);
+    const int slot = slot_of(q);
+    if (!values && slot < slot1) rotate<D, ROPE>(v[q], u_value, block_at * BS + slot, a.rope);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, finite_mag(v[q][e]));
-    }
+    for (int e = 0; e < 8; ++e) m = max(m, finite_mag(v[q][e]));
   }
   for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
   if ((t & 63) == 0) part[t >> 6] = m;
@@ -190,46 +229,50 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
     __syncthreads();  // every lane has read the old bias
   }
   if (t == 0) *bias = b;
+  const Coder<FMT> coder(b);
+  uint32_t code[kUnits][2];
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    code[q][0] = coder.four(*reinterpret_cast<const float(*)[4]>(v[q]));
+    code[q][1] = coder.four(*reinterpret_cast<const float(*)[4]>(v[q] + 4));
+  }
 
   if (!values) {
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
-      const int x = q * nt + t;
-      if (x < units) {
-        const int tok = x / upt, u = x % upt;
-        const float(&lo)[4] = *reinterpret_cast<const float(*)[4]>(v[q]);
-        const float(&hi)[4] = *reinterpret_cast<const float(*)[4]>(v[q] + 4);
-        uint8_t* o = codes + (slot0 + tok) * D;
-        *reinterpret_cast<uint32_t*>(o + unit_lo(u, halves)) = codes4_f32<FMT>(lo, b);
-        *reinterpret_cast<uint32_t*>(o + unit_hi(u, halves, D)) = codes4_f32<FMT>(hi, b);
+      const int slot = slot_of(q);
+      if (slot < slot1) {
+        uint8_t* o = codes + slot * D;
+        *reinterpret_cast<uint32_t*>(o + unit_lo<D, ROPE>(u_value)) = code[q][0];
+        *reinterpret_cast<uint32_t*>(o + unit_hi<D, ROPE>(u_value)) = code[q][1];
       }
     }
+    return;
+  }
+  if (slot1 - slot0 == 1) {  // one token: its codes go out byte by byte
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q)
+      if (slot_of(q) == slot0)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          codes[(8 * u_value + e) * BS + slot0] = (uint8_t)(code[q][e >> 2] >> (8 * (e & 3)));
     return;
   }
   const int pitch = BS + 4;
+  if (slot_of(0) < slot1) {
 #pragma unroll
-  for (int q = 0; q < kUnits; ++q) {
-    const int x = q * nt + t;
-    if (x < units) {
-      const int tok = x / upt, u = x % upt;
-      const float(&lo)[4] = *reinterpret_cast<const float(*)[4]>(v[q]);
-      const float(&hi)[4] = *reinterpret_cast<const float(*)[4]>(v[q] + 4);
-      const uint32_t c0 = codes4_f32<FMT>(lo, b), c1 = codes4_f32<FMT>(hi, b);
+    for (int half = 0; half < 2; ++half) {
+      uint32_t r[4] = {code[0][half], code[1][half], code[2][half], code[3][half]};
+      transpose4(r);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lds[(8 * u + e) * pitch + slot0 + tok] = (uint8_t)(c0 >> (8 * e));
-        lds[(8 * u + 4 + e) * pitch + slot0 + tok] = (uint8_t)(c1 >> (8 * e));
-      }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint32_t*>(lds + (8 * u_value + 4 * half + e) * pitch + slot_of(0)) = r[e];
     }
   }
   __syncthreads();
-  const int slot1 = slot0 + count;
-  if (count == 1) {
-    for (int d = t; d < D; d += nt) codes[d * BS + slot0] = lds[d * pitch + slot0];
-    return;
-  }
-  for (int x = t; x < D * (BS / 4); x += nt) {
-    const int d = x / (BS / 4), c = 4 * (x % (BS / 4));
+  const int words = BS / 4, shift = __builtin_ctz(words);  // of a dimension's row
+  for (int x = t; x < D * words; x += nt) {
+    const int d = x >> shift, c = 4 * (x & (words - 1));
     if (c >= slot0 && c + 4 <= slot1) {
       *reinterpret_cast<uint32_t*>(codes + d * BS + c) = *reinterpret_cast<const uint32_t*>(lds + d * pitch + c);
     } else {
@@ -248,77 +291,117 @@ struct ReadArgs {
   int blocks_per_seq;
 };
 
-// 8 codes (two dwords) at bias b -> out_dtype at o.
+// 8 codes (two words) times 2^-b -> out_dtype at o, each rounded once: by the
+// conversion itself where 2^-b and every result are normal numbers.
 template <int OT, int FMT>
-__device__ __forceinline__ void write8(void* p, int64_t i, uint32_t c0, uint32_t c1, int32_t b) {
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = __builtin_ldexpf(code_value<FMT>((c0 >> (8 * e)) & 0xFFu), -b);
-    v[4 + e] = __builtin_ldexpf(code_value<FMT>((c1 >> (8 * e)) & 0xFFu), -b);
-  }
+__device__ __forceinline__ void write8(void* p, int64_t i, uint32_t c0, uint32_t c1, int32_t b, float scale, bool hw) {
   if constexpr (OT == FP8_IN_FP32) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __builtin_ldexpf(code_value<FMT>((c0 >> (8 * e)) & 0xFFu), -b);
+      v[4 + e] = __builtin_ldexpf(code_value<FMT>((c1 >> (8 * e)) & 0xFFu), -b);
+    }
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
     o[0] = make_float4(v[0], v[1], v[2], v[3]);
     o[1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
-    const uint2 lo = bf16x4(v), hi = bf16x4(v + 4);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    uint4 o;
+    if (hw) {
+      hw_v2bf r[4];
+      if constexpr (FMT == FP8_E4M3) {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, scale, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c0, scale, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, scale, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, scale, true);
+      } else {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c0, scale, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c0, scale, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c1, scale, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c1, scale, true);
+      }
+      o = make_uint4(__builtin_bit_cast(uint32_t, r[0]), __builtin_bit_cast(uint32_t, r[1]),
+                     __builtin_bit_cast(uint32_t, r[2]), __builtin_bit_cast(uint32_t, r[3]));
+    } else {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __builtin_ldexpf(code_value<FMT>((c0 >> (8 * e)) & 0xFFu), -b);
+        v[4 + e] = __builtin_ldexpf(code_value<FMT>((c1 >> (8 * e)) & 0xFFu), -b);
+      }
+      const uint2 lo = bf16x4(v), hi = bf16x4(v + 4);
+      o = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = o;
   }
 }
 
-template <int OT, int FMT>
+// One workgroup per (sequence, block, head, keys | values).  A lane writes
+// eight dimensions of a token at a time; values come through LDS, words of four
+// tokens of a dimension, eight of which it transposes in registers.
+template <int OT, int FMT, int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
+  constexpr int kUpt = D / 8;
   extern __shared__ uint8_t lds[];
   const int t = threadIdx.x;
-  const int D = a.cache.head_dim, BS = a.cache.block_size, H = a.cache.heads;
-  int64_t g = blockIdx.x;
+  const int BS = a.cache.block_size, H = a.cache.heads;
+  uint32_t g = blockIdx.x;
   const bool values = g & 1;
   g >>= 1;
-  const int head = (int)(g % H);
+  const int head = g % H;
   g /= H;
-  const int nth_block = (int)(g % a.blocks_per_seq), i = (int)(g / a.blocks_per_seq);
+  const int nth_block = g % a.blocks_per_seq, i = g / a.blocks_per_seq;
   void* out = values ? a.v : a.k;
   if (!out) return;
   const KVSeq s = kv_seq_uniform(a.batch, BS, i);
   if (s.n == 0) return;
-  const int block_at = s.start / BS + nth_block;
+  const int block_at = (s.start >> __builtin_ctz(BS)) + nth_block;
   const int p0 = max(s.start, block_at * BS), p1 = min(s.start + s.n, block_at * BS + BS);
   if (p0 >= p1) return;
-  const int block = kv_block(a.cache, a.batch, i, block_at);
-  const int slot0 = p0 - block_at * BS, count = p1 - p0;
-  const int64_t row0 = s.first + (p0 - s.start);
-  const int upt = D / 8, units = count * upt;
+  const int block = __builtin_amdgcn_readfirstlane(kv_block(a.cache, a.batch, i, block_at));
+  const int slot0 = p0 - block_at * BS, slot1 = p1 - block_at * BS;
+  const int64_t row0 = s.first - s.start + (int64_t)block_at * BS;  // of slot 0
   const int64_t cell = (int64_t)max(block, 0) * H + head;
   const uint8_t* codes = (values ? a.cache.v : a.cache.k) + cell * BS * D;
   int32_t b = 0;
   if (block >= 0) b = (values ? a.cache.v_bias : a.cache.k_bias)[cell];
-  const int pitch = BS + 4;
-  if (values && block >= 0) {
-    for (int x = t; x < D * (BS / 16); x += 256) {
-      const int d = x / (BS / 16), c = 16 * (x % (BS / 16));
-      const uint4 w = *reinterpret_cast<const uint4*>(codes + d * BS + c);
-      uint32_t* o = reinterpret_cast<uint32_t*>(lds + d * pitch + c);
-      o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
+  const bool hw = b >= -100 && b <= 100;
+  const float scale = __builtin_ldexpf(1.0f, hw ? -b : 0);
+  auto at = [&](int slot, int u) { return ((row0 + slot) * H + head) * D + 8 * u; };
+  if (!values || block < 0) {
+    for (int x = t; x < (slot1 - slot0) * kUpt; x += 256) {
+      const int slot = slot0 + x / kUpt, u = x % kUpt;
+      uint2 w = make_uint2(0, 0);
+      if (block >= 0) w = *reinterpret_cast<const uint2*>(codes + slot * D + 8 * u);
+      write8<OT, FMT>(out, at(slot, u), w.x, w.y, b, scale, hw);
     }
-    __syncthreads();
+    return;
   }
-  for (int x = t; x < units; x += 256) {
-    const int tok = x / upt, u = x % upt;
-    uint32_t c0 = 0, c1 = 0;
-    if (block >= 0) {
-      if (values) {
+  const int pitch = BS + 4;
+  const int shift = __builtin_ctz(BS) - 4;  // 16-byte pieces of a dimension's row
+  for (int x = t; x < D << shift; x += 256) {
+    const int d = x >> shift, c = 16 * (x & ((1 << shift) - 1));
+    const uint4 w = *reinterpret_cast<const uint4*>(codes + d * BS + c);
+    uint32_t* o = reinterpret_cast<uint32_t*>(lds + d * pitch + c);
+    o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
+  }
+  __syncthreads();
+  for (int x = t; x < BS / 4 * kUpt; x += 256) {
+    const int quad = x / kUpt, u = x % kUpt;
+    if (4 * quad + 4 <= slot0 || 4 * quad >= slot1) continue;
+    uint32_t lo[4], hi[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c0 |= (uint32_t)lds[(8 * u + e) * pitch + slot0 + tok] << (8 * e);
-          c1 |= (uint32_t)lds[(8 * u + 4 + e) * pitch + slot0 + tok] << (8 * e);
-        }
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + (slot0 + tok) * D + 8 * u);
-        c0 = w.x, c1 = w.y;
-      }
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = *reinterpret_cast<const uint32_t*>(lds + (8 * u + e) * pitch + 4 * quad);
+      hi[e] = *reinterpret_cast<const uint32_t*>(lds + (8 * u + 4 + e) * pitch + 4 * quad);
     }
-    write8<OT, FMT>(out, ((row0 + tok) * H + head) * D + 8 * u, c0, c1, b);
+    transpose4(lo);
+    transpose4(hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int slot = 4 * quad + e;
+      if (slot >= slot0 && slot < slot1) write8<OT, FMT>(out, at(slot, u), lo[e], hi[e], b, scale, hw);
+    }
   }
 }
 
@@ -338,27 +421,53 @@ hipError_t launch_kv_append(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch
                             const void* v, int64_t v_stride, int dtype, const void* q, int64_t q_stride, int q_heads,
                             uint16_t* q_out, const float* cos, const float* sin, int rope_rows, int rope_pairs,
                             hipStream_t stream) {
-  AppendArgs a{c, batch, k, v, q, k_stride, v_stride, q_stride, q_heads, q_out, {cos, sin, rope_rows, rope_pairs}, 0, 0};
+  AppendArgs a{};
+  a.cache = c;
+  a.batch = batch;
+  a.k = k, a.v = v, a.q = q;
+  a.k_stride = k_stride, a.v_stride = v_stride, a.q_stride = q_stride;
+  a.q_heads = q_heads;
+  a.q_out = q_out;
+  a.rope = {cos, sin, rope_rows};
   // one new token touches one block; n tokens at most (n - 1) / block_size + 2
   a.blocks_per_seq = batch.max_new == 1 ? 1 : (batch.max_new - 1) / c.block_size + 2;
   a.kv_groups = (int64_t)batch.batch * a.blocks_per_seq * c.heads * 2;
-  const int64_t groups = a.kv_groups + (q ? (int64_t)batch.batch * batch.max_new : 0);
-  // lanes: a block's new tokens in kUnits units each
-  const int units = (batch.max_new < c.block_size ? batch.max_new : c.block_size) * (c.head_dim / 8);
-  int threads = (units + kUnits - 1) / kUnits;
-  threads = threads < 256 ? (q ? 256 : (threads + 63) / 64 * 64) : (threads + 63) / 64 * 64;
-  auto run = [&](auto dt, auto fmt) {
-    hipLaunchKernelGGL((kv_append_kernel<dt.value, fmt.value>), dim3((uint32_t)groups), dim3(threads), lds_bytes(c),
-                       stream, a);
-  };
-  using std::integral_constant;
-  if (dtype == FP8_IN_FP32) {
-    if (c.fmt == FP8_E4M3) run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, FP8_E4M3>{});
-    else run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, FP8_E5M2>{});
-  } else {
-    if (c.fmt == FP8_E4M3) run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, FP8_E4M3>{});
-    else run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, FP8_E5M2>{});
+  // queries: about 16384 elements a workgroup
+  int64_t groups = a.kv_groups;
+  if (q) {
+    const int64_t want = 16384 / ((int64_t)q_heads * c.head_dim);
+    a.q_tokens = (int)(want < 1 ? 1 : want < batch.max_new ? want : batch.max_new);
+    a.q_groups = (batch.max_new + a.q_tokens - 1) / a.q_tokens;
+    groups += (int64_t)batch.batch * a.q_groups;
   }
+  // lanes: a block's new tokens in kUnits units each (values: its quads of
+  // slots), a multiple of a token's units
+  const int upt = c.head_dim / 8;
+  const int quads = batch.max_new < c.block_size ? (batch.max_new + 2) / 4 + 1 : c.block_size / 4;
+  int threads = (quads < c.block_size / 4 ? quads : c.block_size / 4) * upt;
+  threads = (threads + 63) / 64 * 64;
+  if (q && threads < 256) threads = 256;
+  using std::integral_constant;
+  auto run = [&](auto dt, auto fmt, auto d, auto rope) {
+    hipLaunchKernelGGL((kv_append_kernel<dt.value, fmt.value, d.value, rope.value>), dim3((uint32_t)groups),
+                       dim3(threads), lds_bytes(c), stream, a);
+  };
+  auto with_rope = [&](auto dt, auto fmt, auto d) {
+    if (!cos) run(dt, fmt, d, integral_constant<int, kRopeNone>{});
+    else if (rope_pairs) run(dt, fmt, d, integral_constant<int, kRopePairs>{});
+    else run(dt, fmt, d, integral_constant<int, kRopeHalves>{});
+  };
+  auto with_dim = [&](auto dt, auto fmt) {
+    if (c.head_dim == 64) with_rope(dt, fmt, integral_constant<int, 64>{});
+    else if (c.head_dim == 128) with_rope(dt, fmt, integral_constant<int, 128>{});
+    else with_rope(dt, fmt, integral_constant<int, 256>{});
+  };
+  auto with_fmt = [&](auto dt) {
+    if (c.fmt == FP8_E4M3) with_dim(dt, integral_constant<int, FP8_E4M3>{});
+    else with_dim(dt, integral_constant<int, FP8_E5M2>{});
+  };
+  if (dtype == FP8_IN_FP32) with_fmt(integral_constant<int, FP8_IN_FP32>{});
+  else with_fmt(integral_constant<int, FP8_IN_BF16>{});
   return hipGetLastError();
 }
 
@@ -366,18 +475,22 @@ hipError_t launch_kv_read(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch, 
                           hipStream_t stream) {
   ReadArgs a{c, batch, k, v, (batch.max_new - 1) / c.block_size + 2};
   const int64_t groups = (int64_t)batch.batch * a.blocks_per_seq * c.heads * 2;
-  auto run = [&](auto dt, auto fmt) {
-    hipLaunchKernelGGL((kv_read_kernel<dt.value, fmt.value>), dim3((uint32_t)groups), dim3(256), lds_bytes(c), stream,
-                       a);
-  };
   using std::integral_constant;
-  if (out_dtype == FP8_IN_FP32) {
-    if (c.fmt == FP8_E4M3) run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, FP8_E4M3>{});
-    else run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, FP8_E5M2>{});
-  } else {
-    if (c.fmt == FP8_E4M3) run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, FP8_E4M3>{});
-    else run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, FP8_E5M2>{});
-  }
+  auto run = [&](auto dt, auto fmt, auto d) {
+    hipLaunchKernelGGL((kv_read_kernel<dt.value, fmt.value, d.value>), dim3((uint32_t)groups), dim3(256), lds_bytes(c),
+                       stream, a);
+  };
+  auto with_dim = [&](auto dt, auto fmt) {
+    if (c.head_dim == 64) run(dt, fmt, integral_constant<int, 64>{});
+    else if (c.head_dim == 128) run(dt, fmt, integral_constant<int, 128>{});
+    else run(dt, fmt, integral_constant<int, 256>{});
+  };
+  auto with_fmt = [&](auto dt) {
+    if (c.fmt == FP8_E4M3) with_dim(dt, integral_constant<int, FP8_E4M3>{});
+    else with_dim(dt, integral_constant<int, FP8_E5M2>{});
+  };
+  if (out_dtype == FP8_IN_FP32) with_fmt(integral_constant<int, FP8_IN_FP32>{});
+  else with_fmt(integral_constant<int, FP8_IN_BF16>{});
   return hipGetLastError();
 }
 

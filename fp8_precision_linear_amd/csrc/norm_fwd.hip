@@ -41,6 +41,7 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
   int parity = 0;
   int32_t bias = 0;
   if constexpr (OUT == kOutCodes) bias = *a.bias_in;
+  const Codes codes(a.fmt, bias);
   // the weight stays in registers over the workgroup's rows (where sixteen
   // waves leave enough), its loads in flight with the first row's
   constexpr bool kKeepW = W < 16;
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) m = max(m, __float_as_uint(h[u][e]) & 0x7FFFFFFFu);
         if constexpr (OUT == kOutBf16) store_as<FP8_IN_BF16, V>(a.y, base + j, h[u]);
-        if constexpr (OUT == kOutCodes) store_codes<V>(static_cast<uint8_t*>(a.y), base + j, h[u], a.fmt, bias);
+        if constexpr (OUT == kOutCodes) codes.store<V>(static_cast<uint8_t*>(a.y), base + j, h[u]);
       }
     }
     if constexpr (OUT == kOutStats) {
@@ -118,10 +119,11 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
           *a.amax = m;
           *a.bias_out = b;
         }
+        const Codes c(a.fmt, b);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int j = (u * kLanes + t) * V;
-          if (j < d) store_codes<V>(static_cast<uint8_t*>(a.y), base + j, h[u], a.fmt, b);
+          if (j < d) c.store<V>(static_cast<uint8_t*>(a.y), base + j, h[u]);
         }
       }
     } else {
@@ -185,6 +187,7 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
     *amax = m;
     *bias = b;
   }
+  const Codes codes(fmt, b);
   for (int64_t k = group; k < rows; k += (int64_t)kCastRows * groups) {
 #pragma unroll
     for (int q = 0; q < kCastRows; ++q) {
@@ -194,7 +197,7 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
         unpack<HT, V>(x[q], v);
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = v[e] * rs[q] * ww[e];
-        store_codes<V>(y, (rows - 1 - at) * d + j, v, fmt, b);
+        codes.store<V>(y, (rows - 1 - at) * d + j, v);
       }
     }
     fetch(k + (int64_t)kCastRows * groups);
@@ -208,7 +211,7 @@ void launch_fwd(const NormProblem& p, const FwdArgs& a, hipStream_t stream) {
   for_dtype(p.x_dtype, [&](auto xt) {
     if constexpr (xt.value != kNone) {
       for_dtype(p.r ? p.r_dtype : kNone, [&](auto rt) {
-        for_shape(a.d, [&](auto v, auto u, auto w) {
+        for_shape<false>(a.d, [&](auto v, auto u, auto w) {
           constexpr int W = w.value;
           const int64_t rows_per = kBlock<W> / (64 * W);
           const int64_t blocks = (a.rows + rows_per - 1) / rows_per;
