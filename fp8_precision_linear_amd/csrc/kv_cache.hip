@@ -283,6 +283,8 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
 }
 
 // ---------------------------------------------------------------- read
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
 struct ReadArgs {
   fp8_kv_cache_t cache;
   fp8_kv_batch_t batch;
@@ -332,7 +334,8 @@ __device__ __forceinline__ void write8(void* p, int64_t i, uint32_t c0, uint32_t
       const uint2 lo = bf16x4(v), hi = bf16x4(v + 4);
       o = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = o;
+    // streaming: 117 us over 8 x 16384 tokens of 8 heads, 126 through the caches
+    __builtin_nontemporal_store(u32x4{o.x, o.y, o.z, o.w}, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
   }
 }
 

@@ -197,7 +197,7 @@ hipError_t launch_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dt
     for_dtype(dy_dtype, [&](auto yt) {
       for_dtype(h_dtype, [&](auto ht) {
         if constexpr (yt.value != kNone && ht.value != kNone)
-          for_shape<true>((int)d, [&](auto v, auto u, auto w_) {
+          for_shape((int)d, [&](auto v, auto u, auto w_) {
             hipLaunchKernelGGL((norm_bwd_kernel<yt.value, ht.value, v.value, u.value, w_.value>),
                                dim3((uint32_t)parts), dim3(kBlock<w_.value>), 0, stream, a);
           });

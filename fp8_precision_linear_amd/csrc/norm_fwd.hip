@@ -204,18 +204,23 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
   }
 }
 
-constexpr int64_t kMaxBlocks = 2048;  // eight 256-lane workgroups per CU
+// Most workgroups: eight of 256 lanes per CU; three of 512 (8192 x 8192 in 91
+// us; 1024 workgroups 111, 2048 94), two of 1024.
+constexpr int64_t kMaxBlocks = 2048;
+// Of the second half, six per CU: not a power of two, which makes the rows in
+// flight meet in few memory channels (8192 x 8192 in 39 us; 1024: 49, 2048: 49).
+constexpr int64_t kCastBlocks = 1536;
 
 template <int OUT>
 void launch_fwd(const NormProblem& p, const FwdArgs& a, hipStream_t stream) {
   for_dtype(p.x_dtype, [&](auto xt) {
     if constexpr (xt.value != kNone) {
       for_dtype(p.r ? p.r_dtype : kNone, [&](auto rt) {
-        for_shape<false>(a.d, [&](auto v, auto u, auto w) {
+        for_shape(a.d, [&](auto v, auto u, auto w) {
           constexpr int W = w.value;
           const int64_t rows_per = kBlock<W> / (64 * W);
           const int64_t blocks = (a.rows + rows_per - 1) / rows_per;
-          const int64_t cap = W == 16 ? kMaxBlocks / 4 : kMaxBlocks;
+          const int64_t cap = W == 16 ? 512 : W == 8 ? 768 : kMaxBlocks;
           hipLaunchKernelGGL((norm_fwd_kernel<xt.value, rt.value, v.value, u.value, W, OUT>),
                              dim3((uint32_t)(blocks < cap ? blocks : cap)), dim3(kBlock<W>), 0, stream, a);
         });
@@ -276,10 +281,10 @@ hipError_t launch_norm_quantize(const NormProblem& p, int fmt, int32_t margin, u
   const int h_dtype = p.r ? p.r_dtype : p.x_dtype;
   const int V = p.d % 4 == 0 ? 4 : 1;
   const int col_blocks = (int)((p.d + 256 * V - 1) / (256 * V));
-  // rows shared out so that kMaxBlocks workgroups run, each with whole batches
-  // of kCastRows where there are rows enough
+  // rows shared out over kCastBlocks workgroups, each with whole batches of
+  // kCastRows where there are rows enough
   int64_t groups = (p.rows + kCastRows - 1) / kCastRows;
-  const int64_t most = kMaxBlocks / col_blocks > 0 ? kMaxBlocks / col_blocks : 1;
+  const int64_t most = kCastBlocks / col_blocks > 0 ? kCastBlocks / col_blocks : 1;
   groups = groups < most ? groups : most;
   if (groups == 0) groups = 1;
   auto run = [&](auto ht, auto v) {
