@@ -122,13 +122,14 @@ def _check(fn, status):
 
 
 # The current stream's handle without building a torch.cuda.Stream object
-# (2.7 us of host time a call), where this torch has the function.
+# (2.7 us of host time a call), where this torch has the functions.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream=None):
-    if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+    if stream is None and _raw_stream is not None and _raw_device is not None:
+        return _raw_stream(_raw_device())
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
