@@ -29,48 +29,53 @@ def _opt(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _here(t, name, dev):
+    """_need_place, its checks in line: a call per tensor is a fifth of a small
+    norm's host time."""
+    if not t.is_contiguous() or t.device != dev:
+        _need_place(t, name, dev)
+
+
 def _fwd_args(x, w, residual, eps, h, rstd, stream):
     """Checks; (rows, arguments up to rstd, h, rstd) of the forward calls.
     x and residual: [..., d]."""
-    for t, name in ((x, "x"), (w, "w"), (residual, "residual")):
-        if t is not None and not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-    shape = x.shape
-    if x.dim() < 1 or w.dim() != 1 or shape[-1] != w.shape[0]:
-        raise ValueError(f"x [..., d] and w [d] do not match: {tuple(shape)}, {tuple(w.shape)}")
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise ValueError(f"x and w must be tensors, got {type(x).__name__} and {type(w).__name__}")
+    shape, wshape = x.shape, w.shape
+    if not shape or len(wshape) != 1 or shape[-1] != wshape[0]:
+        raise ValueError(f"x [..., d] and w [d] do not match: {tuple(shape)}, {tuple(wshape)}")
     if not eps >= 0:
         raise ValueError(f"eps must not be negative, got {eps}")
     d = shape[-1]
     if not 1 <= d <= (MAX_D if d % 4 == 0 else MAX_ODD_D):
         raise ValueError(f"rows of {d} elements: 1 to {MAX_D}, or {MAX_ODD_D} where not a multiple of 4")
     rows = x.numel() // d
-    xt, wt = _dtype_code(x), _dtype_code(w)
-    rt = 0
+    xt, wt, rt, rptr, hptr = _dtype_code(x), _dtype_code(w), 0, 0, 0
+    dev = x.device
     if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.shape != shape:
+            raise ValueError(f"residual must be a tensor of shape {tuple(shape)}, got "
+                             f"{tuple(residual.shape) if isinstance(residual, torch.Tensor) else type(residual).__name__}")
         rt = _dtype_code(residual)
-        if residual.shape != shape:
-            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
-        if h is not None:
-            _need_kind(h, "h", residual.dtype, shape=shape)
     elif h is not None:
         raise ValueError("h is written only where there is a residual")
-    if rstd is not None:
-        _need_kind(rstd, "rstd", torch.float32, numel=rows)
-    dev = x.device
-    _need_place(x, "x", dev)
-    _need_place(w, "w", dev)
+    if not x.is_cuda:
+        _need_place(x, "x", dev)
+    _here(x, "x", dev)
+    _here(w, "w", dev)
+    out = x
     if residual is not None:
-        _need_place(residual, "residual", dev)
-    if h is not None:
-        _need_place(h, "h", dev)
-    elif residual is not None:
-        h = _like(residual, residual.dtype, stream)
+        _here(residual, "residual", dev)
+        if h is not None:
+            _need(h, "h", residual.dtype, dev, shape=shape)
+        else:
+            h = _like(residual, residual.dtype, stream)
+        out, rptr, hptr = h, residual.data_ptr(), h.data_ptr()
     if rstd is not None:
-        _need_place(rstd, "rstd", dev)
+        _need(rstd, "rstd", torch.float32, dev, numel=rows)
     else:
         rstd = _empty(rows, torch.float32, dev, stream)
-    args = (x.data_ptr(), xt, _opt(residual), rt, w.data_ptr(), wt, rows, d, eps, _opt(h), rstd.data_ptr())
-    return rows, args, (x if residual is None else h), rstd
+    return rows, (x.data_ptr(), xt, rptr, rt, w.data_ptr(), wt, rows, d, eps, hptr, rstd.data_ptr()), out, rstd
 
 
 def rmsnorm_fwd(x, w, residual=None, eps=1e-5, out=None, h=None, rstd=None, amax=None, stream=None):
@@ -159,9 +164,16 @@ def rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, amax=None, workspace=
     nbytes = rmsnorm_bwd_workspace_bytes(rows, d)
     _need_kind(rstd, "rstd", torch.float32, numel=rows)
     dev = h.device
-    _places(dev, (dy, "dy"), (h, "h"), (w, "w"), (rstd, "rstd"), (dh, "dh"), (workspace, "workspace"))
+    if not h.is_cuda:
+        _need_place(h, "h", dev)
+    _here(h, "h", dev)
+    _here(dy, "dy", dev)
+    _here(w, "w", dev)
+    _here(rstd, "rstd", dev)
     if dh is not None:
-        _need_kind(dh, "dh", h.dtype, shape=h.shape)
+        _need(dh, "dh", h.dtype, dev, shape=h.shape)
+    if workspace is not None:
+        _need_place(workspace, "workspace", dev)
     if amax is not None:
         _need(amax, "amax", torch.float32, dev, numel=1)
     if dx is not None:
