@@ -1,13 +1,15 @@
 // The paged FP8 cache of keys and values: written as tokens arrive, and read
 // back (include/fp8lin_block.h has the definitions).
 //
-// Append.  One workgroup per (sequence, touched block, head, keys | values)
-// holds that block's new tokens in registers between their largest magnitude
-// and the codes, so they are read once; the rotation is applied on the way.
-// Values change their order (tokens by dimensions -> dimensions by tokens) four
-// by four codes in registers, then through LDS.  Further workgroups of the same
-// launch rotate the queries.  HBM-bound for prompts; for single tokens the
-// launch is most of the time.
+// Append.  One workgroup per (sequence, touched block, head) holds that block's
+// new keys and values in registers between their largest magnitude and the
+// codes, so they are read once; the rotation is applied on the way.  Values
+// change their order (tokens by dimensions -> dimensions by tokens) four by four
+// codes in registers, then through LDS.  Further workgroups of the same launch
+// rotate the queries.  Single tokens are bound by three loads that wait for one
+// another (lengths, block number, tokens: the last two overlap); prompts by the
+// same chain under load, since a workgroup has only 64 KB to fetch: 3.7 TB/s
+// for keys and values, 5.1 for the queries.
 #include <type_traits>
 
 #include "fp8_code.h"
@@ -37,12 +39,12 @@ __device__ __forceinline__ uint2 bf16x4(const float* v) { return make_uint2(bf16
 // How keys and queries are rotated.
 constexpr int kRopeNone = 0, kRopeHalves = 1, kRopePairs = 2;
 
-// A unit of a head's dimensions: two groups of four.  Rotated halves: [4u, +4)
-// and [D/2 + 4u, +4); otherwise [8u, +8).
-template <int D, int ROPE>
-__device__ __forceinline__ int unit_lo(int u) { return ROPE == kRopeHalves ? 4 * u : 8 * u; }
-template <int D, int ROPE>
-__device__ __forceinline__ int unit_hi(int u) { return ROPE == kRopeHalves ? D / 2 + 4 * u : 8 * u + 4; }
+// A unit of a head's dimensions: [4u, +4) and [D/2 + 4u, +4), which the halves'
+// rotation pairs; the lanes of a load read consecutive bytes.
+template <int D>
+__device__ __forceinline__ int unit_lo(int u) { return 4 * u; }
+template <int D>
+__device__ __forceinline__ int unit_hi(int u) { return D / 2 + 4 * u; }
 
 struct Rope {
   const float* cos;
@@ -50,16 +52,33 @@ struct Rope {
   int rows;
 };
 
-// Rotates one unit of the token at `pos` in place.  Products and sums are
-// rounded separately, as the definition has them.
+// The cosines (angle[0..3]) and sines (angle[4..7]) of a unit of the token at
+// `pos`: loaded with the token itself.
 template <int D, int ROPE>
-__device__ __forceinline__ void rotate(float (&v)[8], int u, int pos, const Rope& r) {
-#pragma clang fp contract(off)
+__device__ __forceinline__ void load_angles(float (&angle)[8], int u, int pos, const Rope& r) {
   if constexpr (ROPE == kRopeNone) return;
   const int64_t row = (int64_t)min(pos, r.rows - 1) * (D / 2);
-  float c[4], s[4];
-  load4<FP8_IN_FP32>(r.cos, row + 4 * u, c);
-  load4<FP8_IN_FP32>(r.sin, row + 4 * u, s);
+  if constexpr (ROPE == kRopeHalves) {
+    load4<FP8_IN_FP32>(r.cos, row + 4 * u, angle);
+    load4<FP8_IN_FP32>(r.sin, row + 4 * u, angle + 4);
+  } else {
+    const float2 c0 = *reinterpret_cast<const float2*>(r.cos + row + 2 * u);
+    const float2 c1 = *reinterpret_cast<const float2*>(r.cos + row + D / 4 + 2 * u);
+    const float2 s0 = *reinterpret_cast<const float2*>(r.sin + row + 2 * u);
+    const float2 s1 = *reinterpret_cast<const float2*>(r.sin + row + D / 4 + 2 * u);
+    angle[0] = c0.x, angle[1] = c0.y, angle[2] = c1.x, angle[3] = c1.y;
+    angle[4] = s0.x, angle[5] = s0.y, angle[6] = s1.x, angle[7] = s1.y;
+  }
+}
+
+// Rotates one unit in place.  Products and sums are rounded separately, as the
+// definition has them.
+template <int ROPE>
+__device__ __forceinline__ void rotate(float (&v)[8], const float (&angle)[8]) {
+#pragma clang fp contract(off)
+  if constexpr (ROPE == kRopeNone) return;
+  const float* c = angle;
+  const float* s = angle + 4;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float& x = ROPE == kRopePairs ? v[2 * e] : v[e];
@@ -119,7 +138,7 @@ template <int DT, int FMT, int D, int ROPE>
 __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   constexpr int kUpt = D / 8;       // units of a token and head
   extern __shared__ uint8_t lds[];  // values' codes, [D][block_size + 4]
-  __shared__ uint32_t part[16];
+  __shared__ uint32_t part[2][16];
   const int nt = blockDim.x, t = threadIdx.x;
   const int BS = a.cache.block_size, H = a.cache.heads;
 
@@ -133,23 +152,25 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
     for (int tok = 0; tok < count; ++tok) {
       const int64_t row = s.first + nth + tok;
       for (int x0 = t; x0 < units; x0 += kUnits * nt) {
-        float v[kUnits][8];
+        float v[kUnits][8], angle[8];
+        // x % kUpt is the same for every q: nt is a multiple of kUpt
+        load_angles<D, ROPE>(angle, x0 % kUpt, s.start + nth + tok, a.rope);
 #pragma unroll
         for (int q = 0; q < kUnits; ++q) {
           const int x = x0 + q * nt, head = x / kUpt, u = x % kUpt;
           if (x < units) {
-            load4<DT>(a.q, row * a.q_stride + head * D + unit_lo<D, ROPE>(u), v[q]);
-            load4<DT>(a.q, row * a.q_stride + head * D + unit_hi<D, ROPE>(u), v[q] + 4);
+            load4<DT>(a.q, row * a.q_stride + head * D + unit_lo<D>(u), v[q]);
+            load4<DT>(a.q, row * a.q_stride + head * D + unit_hi<D>(u), v[q] + 4);
           }
         }
 #pragma unroll
         for (int q = 0; q < kUnits; ++q) {
           const int x = x0 + q * nt, head = x / kUpt, u = x % kUpt;
           if (x < units) {
-            rotate<D, ROPE>(v[q], u, s.start + nth + tok, a.rope);
+            rotate<ROPE>(v[q], angle);
             uint16_t* o = a.q_out + (row * a.q_heads + head) * D;
-            *reinterpret_cast<uint2*>(o + unit_lo<D, ROPE>(u)) = bf16x4(v[q]);
-            *reinterpret_cast<uint2*>(o + unit_hi<D, ROPE>(u)) = bf16x4(v[q] + 4);
+            *reinterpret_cast<uint2*>(o + unit_lo<D>(u)) = bf16x4(v[q]);
+            *reinterpret_cast<uint2*>(o + unit_hi<D>(u)) = bf16x4(v[q] + 4);
           }
         }
       }
@@ -158,115 +179,130 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   }
 
   uint32_t g = blockIdx.x;
-  const bool values = g & 1;
-  g >>= 1;
   const int head = g % H;
   g /= H;
   const int nth_block = g % a.blocks_per_seq, i = g / a.blocks_per_seq;
   const KVSeq s = kv_seq_uniform(a.batch, BS, i);
   if (s.n == 0) return;
-  const int block_at = (s.start >> __builtin_ctz(BS)) + nth_block;          // of the sequence
-  const int p0 = max(s.start, block_at * BS);             // first new position in the block
-  const int p1 = min(s.start + s.n, block_at * BS + BS);  // one past the last
+  const int block_at = (s.start >> __builtin_ctz(BS)) + nth_block;  // of the sequence
+  const int p0 = max(s.start, block_at * BS);                       // first new position in the block
+  const int p1 = min(s.start + s.n, block_at * BS + BS);            // one past the last
   if (p0 >= p1) return;
-  const int block = __builtin_amdgcn_readfirstlane(kv_block(a.cache, a.batch, i, block_at));
-  if (block < 0) return;
+  const int block_number = kv_block(a.cache, a.batch, i, block_at);  // needed after the tokens are in
   const int slot0 = p0 - block_at * BS, slot1 = p1 - block_at * BS;
 
   // This lane's units: keys, unit t + q * nt of the new tokens in order;
   // values, dimensions u of the four tokens of an aligned quad of slots, which
   // makes four codes of one dimension a word.
   const int64_t row0 = s.first - s.start + (int64_t)block_at * BS;  // of slot 0
-  const int first = values ? slot0 >> 2 : slot0;
-  auto slot_of = [&](int q) { return values ? 4 * (first + t / kUpt) + q : first + (t + q * nt) / kUpt; };
-  const int u_value = t % kUpt;  // nt is a multiple of kUpt
-  float v[kUnits][8];
-  uint32_t m = 0;
+  const int u = t % kUpt;                                           // nt is a multiple of kUpt
+  auto key_slot = [&](int q) { return slot0 + (t + q * nt) / kUpt; };
+  const int quad = 4 * ((slot0 >> 2) + t / kUpt);
+  float kv[kUnits][8], vv[kUnits][8], angle[kUnits][8];
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
-    const int slot = slot_of(q);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[q][e] = 0.0f;
-    if (slot >= slot0 && slot < slot1) {
-      if (values) {
-        const int64_t at = (row0 + slot) * a.v_stride + head * D + 8 * u_value;
-        load4<DT>(a.v, at, v[q]);
-        load4<DT>(a.v, at + 4, v[q] + 4);
-      } else {
-        const int64_t at = (row0 + slot) * a.k_stride + head * D;
-        load4<DT>(a.k, at + unit_lo<D, ROPE>(u_value), v[q]);
-        load4<DT>(a.k, at + unit_hi<D, ROPE>(u_value), v[q] + 4);
-      }
+    for (int e = 0; e < 8; ++e) kv[q][e] = vv[q][e] = angle[q][e] = 0.0f;
+    if (key_slot(q) < slot1) {
+      const int64_t at = (row0 + key_slot(q)) * a.k_stride + head * D;
+      load4<DT>(a.k, at + unit_lo<D>(u), kv[q]);
+      load4<DT>(a.k, at + unit_hi<D>(u), kv[q] + 4);
+      load_angles<D, ROPE>(angle[q], u, block_at * BS + key_slot(q), a.rope);
     }
   }
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
-    const int slot = slot_of(q);
-    if (!values && slot < slot1) rotate<D, ROPE>(v[q], u_value, block_at * BS + slot, a.rope);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, finite_mag(v[q][e]));
+    if (quad + q >= slot0 && quad + q < slot1) {
+      const int64_t at = (row0 + quad + q) * a.v_stride + head * D;
+      load4<DT>(a.v, at + unit_lo<D>(u), vv[q]);
+      load4<DT>(a.v, at + unit_hi<D>(u), vv[q] + 4);
+    }
   }
-  for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-  if ((t & 63) == 0) part[t >> 6] = m;
-  __syncthreads();
-  for (int w = 0; w < nt / 64; ++w) m = max(m, part[w]);
+  const int block = __builtin_amdgcn_readfirstlane(block_number);
+  if (block < 0) return;
+  const int64_t cell = (int64_t)block * H + head;
+  const int32_t old_k = a.cache.k_bias[cell], old_v = a.cache.v_bias[cell];
+  uint32_t mk = 0, mv = 0;
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    rotate<ROPE>(kv[q], angle[q]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mk = max(mk, finite_mag(kv[q][e]));
+      mv = max(mv, finite_mag(vv[q][e]));
+    }
+  }
+  for (int off = 32; off > 0; off >>= 1) {
+    mk = max(mk, (uint32_t)__shfl_xor((int)mk, off, 64));
+    mv = max(mv, (uint32_t)__shfl_xor((int)mv, off, 64));
+  }
+  if ((t & 63) == 0) {
+    part[0][t >> 6] = mk;
+    part[1][t >> 6] = mv;
+  }
+  __syncthreads();  // (and every lane has read the old biases)
+  for (int w = 0; w < nt / 64; ++w) {
+    mk = max(mk, part[0][w]);
+    mv = max(mv, part[1][w]);
+  }
 
-  int32_t* bias = (values ? a.cache.v_bias : a.cache.k_bias) + (int64_t)block * H + head;
-  uint8_t* codes = (values ? a.cache.v : a.cache.k) + ((int64_t)block * H + head) * BS * D;
-  int32_t b = m == 0 ? FP8_KV_MAX_BIAS : min(FP8_KV_MAX_BIAS, bias_from_amax_bits(m, FMT, 0));
-  if (slot0 > 0) {
-    const int32_t old = *bias;
-    b = min(b, old);
-    if (b < old) {  // the tokens that were there, at the new scale
-      const int32_t step = b < old - 300 ? -300 : b - old;
-      for (int x = t; x < slot0 * D; x += nt) {
-        uint8_t* c = codes + (values ? (x / slot0) * BS + x % slot0 : x);
-        const uint32_t old_code = *c;
-        if ((old_code & 0x7Fu) < (FMT == FP8_E4M3 ? 0x7Fu : 0x7Cu))  // NaN and infinity stay
-          *c = (uint8_t)fp8_code<FMT>(__float_as_uint(code_value<FMT>(old_code)), step);
+  // a block's bias; where it falls, the tokens that were there are coded again
+  uint8_t* k_codes = a.cache.k + cell * BS * D;
+  uint8_t* v_codes = a.cache.v + cell * BS * D;
+  auto settle = [&](uint32_t m, int32_t old, int32_t* bias, uint8_t* codes, bool values) {
+    int32_t b = m == 0 ? FP8_KV_MAX_BIAS : min(FP8_KV_MAX_BIAS, bias_from_amax_bits(m, FMT, 0));
+    if (slot0 > 0) {
+      b = min(b, old);
+      if (b < old) {
+        const int32_t step = b < old - 300 ? -300 : b - old;
+        for (int x = t; x < slot0 * D; x += nt) {
+          uint8_t* c = codes + (values ? (x / slot0) * BS + x % slot0 : x);
+          const uint32_t old_code = *c;
+          if ((old_code & 0x7Fu) < (FMT == FP8_E4M3 ? 0x7Fu : 0x7Cu))  // NaN and infinity stay
+            *c = (uint8_t)fp8_code<FMT>(__float_as_uint(code_value<FMT>(old_code)), step);
+        }
       }
     }
-    __syncthreads();  // every lane has read the old bias
+    if (t == 0) *bias = b;
+    return b;
+  };
+  const Coder<FMT> k_coder(settle(mk, old_k, a.cache.k_bias + cell, k_codes, false));
+  const Coder<FMT> v_coder(settle(mv, old_v, a.cache.v_bias + cell, v_codes, true));
+
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    if (key_slot(q) < slot1) {
+      uint8_t* o = k_codes + key_slot(q) * D;
+      *reinterpret_cast<uint32_t*>(o + unit_lo<D>(u)) = k_coder.four(*reinterpret_cast<const float(*)[4]>(kv[q]));
+      *reinterpret_cast<uint32_t*>(o + unit_hi<D>(u)) = k_coder.four(*reinterpret_cast<const float(*)[4]>(kv[q] + 4));
+    }
   }
-  if (t == 0) *bias = b;
-  const Coder<FMT> coder(b);
+
   uint32_t code[kUnits][2];
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
-    code[q][0] = coder.four(*reinterpret_cast<const float(*)[4]>(v[q]));
-    code[q][1] = coder.four(*reinterpret_cast<const float(*)[4]>(v[q] + 4));
-  }
-
-  if (!values) {
-#pragma unroll
-    for (int q = 0; q < kUnits; ++q) {
-      const int slot = slot_of(q);
-      if (slot < slot1) {
-        uint8_t* o = codes + slot * D;
-        *reinterpret_cast<uint32_t*>(o + unit_lo<D, ROPE>(u_value)) = code[q][0];
-        *reinterpret_cast<uint32_t*>(o + unit_hi<D, ROPE>(u_value)) = code[q][1];
-      }
-    }
-    return;
+    code[q][0] = v_coder.four(*reinterpret_cast<const float(*)[4]>(vv[q]));
+    code[q][1] = v_coder.four(*reinterpret_cast<const float(*)[4]>(vv[q] + 4));
   }
   if (slot1 - slot0 == 1) {  // one token: its codes go out byte by byte
 #pragma unroll
     for (int q = 0; q < kUnits; ++q)
-      if (slot_of(q) == slot0)
+      if (quad + q == slot0)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          codes[(8 * u_value + e) * BS + slot0] = (uint8_t)(code[q][e >> 2] >> (8 * (e & 3)));
+          v_codes[((e < 4 ? unit_lo<D>(u) : unit_hi<D>(u) - 4) + e) * BS + slot0] =
+              (uint8_t)(code[q][e >> 2] >> (8 * (e & 3)));
     return;
   }
   const int pitch = BS + 4;
-  if (slot_of(0) < slot1) {
+  if (quad < slot1) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t r[4] = {code[0][half], code[1][half], code[2][half], code[3][half]};
       transpose4(r);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint32_t*>(lds + (8 * u_value + 4 * half + e) * pitch + slot_of(0)) = r[e];
+        *reinterpret_cast<uint32_t*>(lds + ((half ? unit_hi<D>(u) : unit_lo<D>(u)) + e) * pitch + quad) = r[e];
     }
   }
   __syncthreads();
@@ -274,10 +310,10 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   for (int x = t; x < D * words; x += nt) {
     const int d = x >> shift, c = 4 * (x & (words - 1));
     if (c >= slot0 && c + 4 <= slot1) {
-      *reinterpret_cast<uint32_t*>(codes + d * BS + c) = *reinterpret_cast<const uint32_t*>(lds + d * pitch + c);
+      *reinterpret_cast<uint32_t*>(v_codes + d * BS + c) = *reinterpret_cast<const uint32_t*>(lds + d * pitch + c);
     } else {
       for (int e = 0; e < 4; ++e)
-        if (c + e >= slot0 && c + e < slot1) codes[d * BS + c + e] = lds[d * pitch + c + e];
+        if (c + e >= slot0 && c + e < slot1) v_codes[d * BS + c + e] = lds[d * pitch + c + e];
     }
   }
 }
@@ -434,7 +470,7 @@ hipError_t launch_kv_append(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch
   a.rope = {cos, sin, rope_rows};
   // one new token touches one block; n tokens at most (n - 1) / block_size + 2
   a.blocks_per_seq = batch.max_new == 1 ? 1 : (batch.max_new - 1) / c.block_size + 2;
-  a.kv_groups = (int64_t)batch.batch * a.blocks_per_seq * c.heads * 2;
+  a.kv_groups = (int64_t)batch.batch * a.blocks_per_seq * c.heads;
   // queries: about 16384 elements a workgroup
   int64_t groups = a.kv_groups;
   if (q) {
