@@ -4,9 +4,9 @@
 // MFMA- and VALU-bound.  A workgroup of four waves takes 128 rows (token, head
 // of the group) of one sequence and key head; each wave owns 32 of them on the
 // 32x32x16 MFMA and keeps its queries, logits and O in registers.  Tiles of 64
-// keys and values go through LDS by DMA, as codes, in two buffers: the next
-// tile lands while this one is consumed, one barrier a tile.  Each wave widens
-// the codes it reads (half the LDS bytes that widened tiles would cost).
+// keys and values go through LDS by DMA, as codes, in a ring of four, one
+// barrier a tile.  Each wave widens the codes it reads (half the LDS bytes that
+// widened tiles would cost).
 //
 // LDS, 16-byte chunks swizzled so that the 16 lanes of a read address 16
 // different bank groups (64 banks): keys [64][D], chunk c of row r at
@@ -19,6 +19,13 @@ namespace fp8lin {
 namespace {
 
 constexpr int kWaves = 4;
+// Tiles in LDS: three on their way while one is consumed.  (With one on its way
+// short prompts, whose workgroups have a CU to themselves, waited for every
+// tile: 740 tokens of 40 heads took 102 us.)
+constexpr int kRing = 4;
+// Tiles whose block numbers and biases are held in LDS at a time.  The main
+// loop then asks nothing of memory but tiles, whose arrival it counts.
+constexpr int kStretch = 64;
 // A lane's 32 probabilities of a tile may add up to this before its row's
 // reference moves: 32 keys level with the maximum that set it (2^kShift each)
 // stay below, and none can pass fp16's range.
@@ -50,7 +57,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   constexpr int J = D / 32;   // 32-dimension steps of the logits
   constexpr int DT = D / 32;  // 32-dimension tiles of the output
   constexpr int kTileBytes = kAttnTile * D;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][kTileBytes];  // [buffer][keys, values]
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kRing][2][kTileBytes];  // [buffer][keys, values]
+  __shared__ __attribute__((aligned(16))) int table[3][kStretch * NB];  // blocks, key biases, value biases
   __shared__ int found[kWaves];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -101,38 +109,36 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   float m = kNoRef, l = 0.0f;
   int bref = kNoBias;
 
-  // blocks and biases of a tile, the same in every lane; read a tile ahead, so
-  // that nothing waits for them before the tile's own wait does
+  // blocks and biases of a tile, scalars
   struct Blocks {
     int b[NB];
   };
   struct Biases {
     int k[NB], v[NB];
   };
-  auto blocks_of = [&](int T) {
-    Blocks r;
-#pragma unroll
-    for (int g = 0; g < NB; ++g) {
-      const int pos = T + 16 * g;
-      r.b[g] = pos < kend ? kv_block(a.cache, a.batch, at.seq, pos >> a.block_shift) : -1;
-    }
-    return r;
-  };
-  auto biases_of = [&](const Blocks& b) {
-    Biases r;
-#pragma unroll
-    for (int g = 0; g < NB; ++g) {
-      const int64_t c = (int64_t)max(b.b[g], 0) * H + at.head;
-      r.k[g] = a.cache.k_bias[c];
-      r.v[g] = a.cache.v_bias[c];
-    }
-    return r;
-  };
   auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
   // granule g's entry
   auto pick = [](const int (&v)[NB], int g) {
     if constexpr (ONE) return v[0];
     else return g < 2 ? (g == 0 ? v[0] : v[1]) : (g == 2 ? v[2] : v[3]);
+  };
+  const int tiles = (kend - kbeg + kAttnTile - 1) / kAttnTile;
+  auto fill = [&](int first) {  // the table for tiles [first, first + kStretch)
+    if ((int)threadIdx.x < kStretch * NB) {
+      const int pos = kbeg + first * kAttnTile + (int)threadIdx.x * (kAttnTile / NB);
+      const int block = pos < kend ? kv_block(a.cache, a.batch, at.seq, pos >> a.block_shift) : -1;
+      const int64_t c = (int64_t)max(block, 0) * H + at.head;
+      table[0][threadIdx.x] = block;
+      table[1][threadIdx.x] = a.cache.k_bias[c];
+      table[2][threadIdx.x] = a.cache.v_bias[c];
+    }
+  };
+  auto entry = [&](int (&to)[NB], int which, int t) {
+    int v[NB];
+#pragma unroll
+    for (int g = 0; g < NB; ++g) v[g] = table[which][t * NB + g];
+#pragma unroll
+    for (int g = 0; g < NB; ++g) to[g] = scalar(v[g]);
   };
   const uint32_t ring0 = lds_addr(ring);
   // This wave's quarter of a tile's keys (values), D / 64 KB: KB i holds key rows
@@ -352,39 +358,45 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
     __builtin_amdgcn_s_setprio(0);
   };
 
-  Blocks cur = blocks_of(kbeg);
-  Biases nbias = biases_of(cur);
+  static_assert(kStretch * 4 <= 64 * kWaves, "one table entry a lane");
+  constexpr int kLoads = 2 * (D / 64);  // this wave's DMA loads a tile
+  for (int first = 0; first < tiles; first += kStretch) {
+    if (first) __syncthreads();  // every wave is done with the table and the ring
+    fill(first);
+    __syncthreads();
+    const int n = min(kStretch, tiles - first), T0 = kbeg + first * kAttnTile;
+    Blocks ahead;
+    for (int t = 0; t < kRing - 1; ++t)
+      if (t < n) {
+        entry(ahead.b, 0, t);
+        issue_k(T0 + t * kAttnTile, ahead, t);
+        issue_v(T0 + t * kAttnTile, ahead, t);
+      }
+    for (int t = 0; t < n; ++t) {
+      const int T = T0 + t * kAttnTile, buf = t & (kRing - 1);
+      Blocks blocks;
+      Biases bias;
+      entry(blocks.b, 0, t);
+      entry(bias.k, 1, t);
+      entry(bias.v, 2, t);
+      const bool more = t + kRing - 1 < n;
+      if (more) entry(ahead.b, 0, t + kRing - 1);
+      wait_stages<kLoads>(min(kRing - 2, n - 1 - t));
+      bare_barrier();  // this tile is whole, and every wave is done with the one before
+      if (more) {
+        issue_k(T + (kRing - 1) * kAttnTile, ahead, (buf + kRing - 1) & (kRing - 1));
+        issue_v(T + (kRing - 1) * kAttnTile, ahead, (buf + kRing - 1) & (kRing - 1));
+      }
+      const uint32_t tile = ring0 + buf * 2 * kTileBytes;
+      bool there = true;
 #pragma unroll
-  for (int g = 0; g < NB; ++g) cur.b[g] = scalar(cur.b[g]);
-  issue_k(kbeg, cur, 0);
-  issue_v(kbeg, cur, 0);
-  Blocks nb = blocks_of(kbeg + kAttnTile);
-  int buf = 0;
-  for (int T = kbeg; T < kend; T += kAttnTile, buf ^= 1) {
-    wait_all();
-    bare_barrier();  // this tile is whole, and every wave is done with the other buffer
-    const Blocks blocks = cur;
-    Biases bias;
-#pragma unroll
-    for (int g = 0; g < NB; ++g) bias.k[g] = scalar(nbias.k[g]), bias.v[g] = scalar(nbias.v[g]);
-    if (T + kAttnTile < kend) {
-#pragma unroll
-      for (int g = 0; g < NB; ++g) cur.b[g] = scalar(nb.b[g]);
-      issue_k(T + kAttnTile, cur, buf ^ 1);
-      issue_v(T + kAttnTile, cur, buf ^ 1);
-      nbias = biases_of(cur);
-      nb = blocks_of(T + 2 * kAttnTile);
+      for (int g = 0; g < NB; ++g) there = there && blocks.b[g] >= 0;
+      if (!there || T + kAttnTile > all_hi || T < all_lo) clean(T, tile + kTileBytes, blocks);
+      if (T >= whi || T + kAttnTile <= wlo) continue;  // nothing for this wave's rows
+      const bool whole = there && T + kAttnTile <= hi && T >= lo;
+      consume(!__all(whole), T, tile, blocks, bias);
     }
-    const uint32_t tile = ring0 + buf * 2 * kTileBytes;
-    bool there = true;
-#pragma unroll
-    for (int g = 0; g < NB; ++g) there = there && blocks.b[g] >= 0;
-    if (!there || T + kAttnTile > all_hi || T < all_lo) clean(T, tile + kTileBytes, blocks);
-    if (T >= whi || T + kAttnTile <= wlo) continue;  // nothing for this wave's rows
-    const bool whole = there && T + kAttnTile <= hi && T >= lo;
-    consume(!__all(whole), T, tile, blocks, bias);
   }
-  wait_vmcnt<0>();
 
   l = swap32_sum(l);
   if (!stored) return;

@@ -62,15 +62,6 @@ __device__ __forceinline__ void wait_lgkm0() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
 }
 
-// Wait until at most `younger` stages of this wave's DMA (D instructions per
-// stage) are still in flight.
-template <int D>
-__device__ __forceinline__ void wait_stages(int younger) {
-  if (younger >= 2) wait_vmcnt<2 * D>();
-  else if (younger == 1) wait_vmcnt<D>();
-  else wait_vmcnt<0>();
-}
-
 // Chunk swizzles of the K-major and MN-major stage tiles.
 __device__ __forceinline__ int kswz(int r) { return (r >> 2) & 3; }
 template <int R>

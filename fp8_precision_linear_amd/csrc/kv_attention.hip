@@ -19,8 +19,10 @@ struct AttnPlan {
   int64_t most_splits;  // tile kernel, whatever the window
 };
 
-// Tile kernel: workgroups wanted in flight, two for each of 256 CUs.
-constexpr int64_t kWantTiles = 512;
+// Tile kernel: workgroups wanted in flight, two for each of 256 CUs, and the
+// fewest tiles of a chunk (shorter ones cost more in the join than they save:
+// 740 tokens of 40 heads over 15 tiles in two chunks 99 us, whole 40).
+constexpr int64_t kWantTiles = 512, kLeastTiles = 16;
 // Rows kernel: even shares where a segment may hold more tiles than this (a
 // join costs about as long as the tiles it takes off the longest workgroup).
 constexpr int64_t kWholeTiles = 24;
@@ -44,10 +46,10 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
   const int64_t tiles = span > 0 ? (span + kAttnTile - 1) / kAttnTile : 1;
   const int64_t want = (kWantTiles + p.base - 1) / p.base;
   int64_t per = (tiles + want - 1) / want;
-  per = (per + 3) / 4 * 4;  // no chunk below four tiles
+  per = per < kLeastTiles ? kLeastTiles : per;
   p.splits = (int)((tiles + per - 1) / per);
   p.chunk = (int)(per * kAttnTile);
-  const int64_t full = ((int64_t)b.max_len + 4 * kAttnTile - 1) / (4 * kAttnTile);
+  const int64_t least = kLeastTiles * kAttnTile, full = (b.max_len + least - 1) / least;
   p.most_splits = want < full ? want : (full > 0 ? full : 1);
   return p;
 }
@@ -57,22 +59,26 @@ int64_t part_rows(const AttnPlan& p, const fp8_kv_batch_t& b, int q_heads, int64
   return p.few ? 2 * (int64_t)p.shares * p.tile_rows : splits * b.tokens * q_heads;
 }
 
-// One workgroup per (new token, query head) whose keys were split joins its
-// parts (chunks, or shares): out = sum_c 2^(lse_c - L) out_c, L = log2 sum_c 2^lse_c.  The parts
-// are dealt to groups of lanes, which meet in LDS in order; a part
+// The join of a (new token, query head) whose keys were split into parts
+// (chunks, or shares): out = sum_c 2^(lse_c - L) out_c, L = log2 sum_c 2^lse_c.
+// A row of D / 4 lanes joins `few` parts alone, several rows a workgroup; many
+// parts are dealt to all rows of a workgroup, which meet in LDS in order.  A part
 // without visible keys has lse = -inf and adds nothing.
 constexpr int kJoin = 256;
-__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows) {
+constexpr int kFewParts = 16;
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows, bool few) {
   __shared__ v4f so[kJoin];
   __shared__ float ss[kJoin], st[kJoin];
-  uint32_t x = blockIdx.x;
-  const int head = x % a.q_heads;
-  x /= a.q_heads;
+  const int D = a.cache.head_dim, lanes = D / 4, t = threadIdx.x;
+  const int64_t index = few ? (int64_t)blockIdx.x * (kJoin / lanes) + t / lanes : blockIdx.x;
+  const int head = index % a.q_heads;
+  const uint32_t x = index / a.q_heads;
   const int i = x % a.batch.batch, nth = x / a.batch.batch;
+  if (nth >= a.batch.max_new) return;
   const int row = nth * a.group + head % a.group, tile = row / tile_rows;
   int2 w{0, 0};
   if (a.shares) w = a.segments[((int64_t)i * a.row_tiles + tile) * a.cache.heads + head / a.group];
-  const KVSeq s = kv_seq_uniform(a.batch, a.cache.block_size, i);
+  const KVSeq s = kv_seq(a.batch, a.cache.block_size, i);
   if (nth >= s.n) return;
   const int64_t at = (int64_t)(s.first + nth) * a.q_heads + head;
   // part c's row of part_o and part_lse: first for c = 0, then from `base` by step
@@ -87,8 +93,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
     chunks = attn_span(a, s, tile * tile_rows, tile_rows).chunks;
   }
   if (chunks <= 1) return;
-  const int D = a.cache.head_dim, lanes = D / 4, t = threadIdx.x;
-  const int share = t / lanes, shares = kJoin / lanes, d = 4 * (t % lanes);
+  const int share = few ? 0 : t / lanes, shares = few ? 1 : kJoin / lanes, d = 4 * (t % lanes);
   // four parts at a time, their results and sums loaded together
   constexpr int kAhead = 4;
   float top = -INFINITY, total = 0.0f;
@@ -117,24 +122,26 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
       if (f != 0.0f) sum += v[u] * f;
     }
   }
-  so[t] = sum;
-  ss[t] = total;
-  st[t] = top;
-  __syncthreads();
-  if (t >= lanes) return;
-  for (int k = 0; k < shares; ++k) top = fmaxf(top, st[k * lanes + t]);
-  sum = v4f{0, 0, 0, 0};
-  total = 0.0f;
-  for (int k = 0; k < shares; ++k) {
-    const float part = st[k * lanes + t];
-    const float f = part == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(part - top);
-    if (f != 0.0f) sum += so[k * lanes + t] * f;
-    total += ss[k * lanes + t] * f;
+  if (!few) {
+    so[t] = sum;
+    ss[t] = total;
+    st[t] = top;
+    __syncthreads();
+    if (t >= lanes) return;
+    for (int k = 0; k < shares; ++k) top = fmaxf(top, st[k * lanes + t]);
+    sum = v4f{0, 0, 0, 0};
+    total = 0.0f;
+    for (int k = 0; k < shares; ++k) {
+      const float part = st[k * lanes + t];
+      const float f = part == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(part - top);
+      if (f != 0.0f) sum += so[k * lanes + t] * f;
+      total += ss[k * lanes + t] * f;
+    }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   *reinterpret_cast<uint2*>(a.out + at * D + d) =
       make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
-  if (t == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
+  if (d == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
 }
 
 }  // namespace
@@ -180,7 +187,12 @@ hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stre
                        : launch_attn_tile(a, groups, stream);
   if (e != hipSuccess || (p.splits == 1 && p.shares == 0)) return e;
   const int64_t joins = (int64_t)pr.batch.batch * pr.batch.max_new * pr.q_heads;
-  hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)joins), dim3(kJoin), 0, stream, a, p.tile_rows);
+  // shares: a segment's parts are about its tiles over a share's
+  const int64_t parts_most = p.shares ? (p.base < p.shares ? (p.shares + p.base - 1) / p.base + 1 : 3) : p.splits;
+  const bool few = parts_most <= kFewParts;
+  const int per = few ? kJoin / (pr.cache.head_dim / 4) : 1;
+  hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)((joins + per - 1) / per)), dim3(kJoin), 0, stream, a,
+                     p.tile_rows, few);
   return hipGetLastError();
 }
 

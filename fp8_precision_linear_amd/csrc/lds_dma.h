@@ -14,9 +14,14 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// s_waitcnt vmcnt(0) lgkmcnt(0): everything this wave has asked of memory or LDS
-// has come back.
-__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(7 << 4); }
+// Wait until at most `younger` stages of this wave's DMA (D instructions per
+// stage) are still in flight.
+template <int D>
+__device__ __forceinline__ void wait_stages(int younger) {
+  if (younger >= 2) wait_vmcnt<2 * D>();
+  else if (younger == 1) wait_vmcnt<D>();
+  else wait_vmcnt<0>();
+}
 
 // A bare barrier: no memory access may move across it (asm "memory" clobber),
 // and it waits for nothing the explicit waits did not.
