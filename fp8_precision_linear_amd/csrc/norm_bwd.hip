@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kDwCols* kDwShares) void norm_dw_kernel(const float
 
 // Workgroups (and rows of partial sums) of the backward pass.
 int bwd_parts(int64_t rows, int64_t d) {
-  const int64_t rows_per = d % 4 == 0 && d <= 2048 ? 4 : 1;
+  const int64_t rows_per = d % 4 == 0 && d <= 1024 ? 4 : 1;
   const int64_t blocks = (rows + rows_per - 1) / rows_per;
   return (int)(blocks < 512 ? blocks : 512);
 }

@@ -190,8 +190,11 @@ __global__ void clear_kernel(uint32_t* p) { *p = 0u; }
 
 // The shapes a row length runs in: V elements per unit (4 where rows start on
 // 16-byte boundaries whatever their type), W waves per row, U units per lane.
-// (Eight waves instead of four for rows of 4100 to 8192: 94 us against 100 over
-// 8192 x 8192 forward, 53 against 56 over 4095 x 5120 backward.)
+// Fewer units a lane and more waves a row are faster as long as the row's sum
+// does not dominate: rows of 1028 to 2048 on four waves instead of one, 28 us
+// against 33 over 8000 x 2048 forward and 25 against 27 over 4095 x 2048
+// backward; rows of 4100 to 8192 on eight instead of four, 94 against 100 over
+// 8192 x 8192 and 53 against 56 over 4095 x 5120.
 template <typename F>
 void for_shape(int d, F&& f) {
   using std::integral_constant;
@@ -199,7 +202,7 @@ void for_shape(int d, F&& f) {
   f(integral_constant<int, V>{}, integral_constant<int, U>{}, integral_constant<int, W>{})
   if (d % 4 == 0) {
     if (d <= 1024) FP8LIN_SHAPE(4, 4, 1);
-    else if (d <= 2048) FP8LIN_SHAPE(4, 8, 1);
+    else if (d <= 2048) FP8LIN_SHAPE(4, 2, 4);
     else if (d <= 4096) FP8LIN_SHAPE(4, 4, 4);
     else if (d <= 8192) FP8LIN_SHAPE(4, 4, 8);
     else if (d <= 16384) FP8LIN_SHAPE(4, 4, 16);
