@@ -20,9 +20,12 @@ struct AttnPlan {
 };
 
 // Tile kernel: workgroups wanted in flight, two for each of 256 CUs, and the
-// fewest tiles of a chunk (shorter ones cost more in the join than they save:
-// 740 tokens of 40 heads over 15 tiles in two chunks 99 us, whole 40).
-constexpr int64_t kWantTiles = 512, kLeastTiles = 16;
+// fewest tiles of a chunk.  Where whole row tiles leave CUs without work, short
+// chunks pay (247 tokens of 16 heads of 256 on 808 cached: chunks of 4 tiles 33
+// us, of 6 38, of 10 47); where they do not, the join costs more than a second
+// workgroup a CU saves (740 tokens of 40 heads, 15 tiles: two chunks 99 us,
+// whole 40).
+constexpr int64_t kWantTiles = 512, kCUs = 256, kLeastTiles = 4, kLeastTilesFull = 32;
 // Rows kernel: even shares where a segment may hold more tiles than this (a
 // join costs about as long as the tiles it takes off the longest workgroup).
 constexpr int64_t kWholeTiles = 24;
@@ -46,10 +49,11 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
   const int64_t tiles = span > 0 ? (span + kAttnTile - 1) / kAttnTile : 1;
   const int64_t want = (kWantTiles + p.base - 1) / p.base;
   int64_t per = (tiles + want - 1) / want;
-  per = per < kLeastTiles ? kLeastTiles : per;
+  const int64_t fewest = p.base < kCUs ? kLeastTiles : kLeastTilesFull;
+  per = per < fewest ? fewest : per;
   p.splits = (int)((tiles + per - 1) / per);
   p.chunk = (int)(per * kAttnTile);
-  const int64_t least = kLeastTiles * kAttnTile, full = (b.max_len + least - 1) / least;
+  const int64_t least = fewest * kAttnTile, full = (b.max_len + least - 1) / least;
   p.most_splits = want < full ? want : (full > 0 ? full : 1);
   return p;
 }
