@@ -23,8 +23,8 @@ struct AttnPlan {
 // fewest tiles of a chunk.  Where whole row tiles leave CUs without work, short
 // chunks pay (247 tokens of 16 heads of 256 on 808 cached: chunks of 4 tiles 33
 // us, of 6 38, of 10 47); where they do not, the join costs more than a second
-// workgroup a CU saves (740 tokens of 40 heads, 15 tiles: two chunks 99 us,
-// whole 40).
+// workgroup a CU saves (two prompts of up to 1303 tokens, 32 heads of 64 on 8:
+// two chunks 42 us, whole 27).
 constexpr int64_t kWantTiles = 512, kCUs = 256, kLeastTiles = 4, kLeastTilesFull = 32;
 // Rows kernel: even shares where a segment may hold more tiles than this (a
 // join costs about as long as the tiles it takes off the longest workgroup).

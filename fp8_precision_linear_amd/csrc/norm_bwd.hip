@@ -21,7 +21,7 @@ struct BwdArgs {
 // Each workgroup walks rows blockIdx.x, + gridDim.x, ...; this lane's share of
 // dw stays in registers, and the weight where they suffice.  dw leaves as one row of `partial` per
 // workgroup, added in a fixed order by norm_dw_kernel.
-template <int YT, int HT, int V, int U, int W>
+template <int YT, int HT, bool WHOLE, int U, int W>
 __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
   constexpr int kLanes = 64 * W;
   constexpr int kRows = kBlock<W> / kLanes;
@@ -31,16 +31,16 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
   const int d = a.d;
   // sixteen waves leave 128 registers a lane, too few to keep w as well
   constexpr bool kKeepW = W < 16;
-  float w[kKeepW ? U : 1][V], dw[U][V];
+  float w[kKeepW ? U : 1][4], dw[U][4];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int j = (u * kLanes + t) * V;
+    const int j = (u * kLanes + t) * 4;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[u][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) dw[u][e] = 0.0f;
     if constexpr (kKeepW) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[u][e] = 0.0f;
-      if (j < d) load_cached<V>(a.w, a.w_dtype, j, w[u]);
+      for (int e = 0; e < 4; ++e) w[u][e] = 0.0f;
+      if (j < d) load_weight<WHOLE>(a.w, a.w_dtype, j, d - j, w[u]);
     }
   }
   uint32_t top = 0;
@@ -48,8 +48,8 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
   // a row's inputs, loaded one row ahead (the sixteen-wave shape has no
   // registers for that: its loads stand where they are used)
   constexpr bool kAhead = W < 16;
-  Raw<YT, V> ry[U];
-  Raw<HT, V> rh[U], rd[U];
+  Raw<YT> ry[U];
+  Raw<HT> rh[U], rd[U];
   float rs_next = 0.0f;
   auto fetch = [&](int64_t row) {
     if (row >= a.rows) return;
@@ -57,11 +57,11 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
     rs_next = a.rstd[row];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
       if (j < d) {
-        ry[u] = load_raw<YT, V>(a.dy, base + j);
-        rh[u] = load_raw<HT, V>(a.h, base + j);
-        if (kAhead && a.dh) rd[u] = load_raw<HT, V>(a.dh, base + j);
+        ry[u] = load_raw<YT, WHOLE, true>(a.dy, base + j, d - j);
+        rh[u] = load_raw<HT, WHOLE, true>(a.h, base + j, d - j);
+        if (kAhead && a.dh) rd[u] = load_raw<HT, WHOLE, true>(a.dh, base + j, d - j);
       }
     }
   };
@@ -72,16 +72,16 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
     if constexpr (!kAhead) fetch(row);
     const int64_t base = row * d;
     const float rs = rs_next;
-    float g[U][V], xh[U][V];
-    Raw<HT, V> rd_now[kAhead ? U : 1];
+    float g[U][4], xh[U][4];
+    Raw<HT> rd_now[kAhead ? U : 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
 #pragma unroll
-      for (int e = 0; e < V; ++e) g[u][e] = xh[u][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) g[u][e] = xh[u][e] = 0.0f;
       if (j < d) {
-        unpack<YT, V>(ry[u], g[u]);
-        unpack<HT, V>(rh[u], xh[u]);
+        unpack<YT>(ry[u], g[u]);
+        unpack<HT>(rh[u], xh[u]);
         if constexpr (kAhead) rd_now[u] = rd[u];
       }
     }
@@ -91,15 +91,15 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
     for (int u = 0; u < U; ++u) {
       float* wu = w[kKeepW ? u : 0];
       if constexpr (!kKeepW) {
-        int j = (u * kLanes + t) * V;
+        int j = (u * kLanes + t) * 4;
         asm volatile("" : "+v"(j));  // or the loads leave the loop, into registers again
-        float ww[V] = {};
-        if (j < d) load_cached<V>(a.w, a.w_dtype, j, ww);
+        float ww[4] = {};
+        if (j < d) load_weight<WHOLE>(a.w, a.w_dtype, j, d - j, ww);
 #pragma unroll
-        for (int e = 0; e < V; ++e) wu[e] = ww[e];
+        for (int e = 0; e < 4; ++e) wu[e] = ww[e];
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
+      for (int e = 0; e < 4; ++e) {
         xh[u][e] *= rs;
         dw[u][e] = fmaf(g[u][e], xh[u][e], dw[u][e]);
         g[u][e] *= wu[e];
@@ -110,48 +110,47 @@ __global__ __launch_bounds__(kBlock<W>) void norm_bwd_kernel(BwdArgs a) {
     parity ^= 1;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
       if (j < d) {
-        float o[V];
+        float o[4];
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = rs * (g[u][e] - xh[u][e] * c);
+        for (int e = 0; e < 4; ++e) o[e] = rs * (g[u][e] - xh[u][e] * c);
         if (a.dh) {
-          float past[V];
-          if constexpr (kAhead) unpack<HT, V>(rd_now[u], past);
-          else load_stream<HT, V>(a.dh, base + j, past);
+          float past[4];
+          if constexpr (kAhead) unpack<HT>(rd_now[u], past);
+          else load_stream<HT, WHOLE>(a.dh, base + j, d - j, past);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += past[e];
+          for (int e = 0; e < 4; ++e) o[e] += past[e];
         }
-        round_to<HT, V>(o);
-        store_as<HT, V>(a.dx, base + j, o);
-#pragma unroll
-        for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(o[e]) & 0x7FFFFFFFu);
+        round_to<HT>(o);
+        store_as<HT, WHOLE>(a.dx, base + j, d - j, o);
+        top = unit_max<WHOLE>(top, d - j, o);
       }
     }
   }
   if (a.amax) fold_amax_wave(top, a.amax);
   // a workgroup of four one-wave rows adds its waves' shares in wave order
   if constexpr (kRows > 1) {
-    __shared__ float acc[kRows - 1][U * V][64];
+    __shared__ float acc[kRows - 1][U * 4][64];
     if (sub > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[sub - 1][u * V + e][t] = dw[u][e];
+        for (int e = 0; e < 4; ++e) acc[sub - 1][u * 4 + e][t] = dw[u][e];
     }
     __syncthreads();
     if (sub > 0) return;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < V; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int s = 0; s < kRows - 1; ++s) dw[u][e] += acc[s][u * V + e][t];
+        for (int s = 0; s < kRows - 1; ++s) dw[u][e] += acc[s][u * 4 + e][t];
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int j = (u * kLanes + t) * V;
-    if (j < d) store_as<FP8_IN_FP32, V>(a.partial, (int64_t)blockIdx.x * d + j, dw[u]);
+    const int j = (u * kLanes + t) * 4;
+    if (j < d) store_as<FP8_IN_FP32, WHOLE>(a.partial, (int64_t)blockIdx.x * d + j, d - j, dw[u]);
   }
 }
 
@@ -178,7 +177,7 @@ __global__ __launch_bounds__(kDwCols* kDwShares) void norm_dw_kernel(const float
 
 // Workgroups (and rows of partial sums) of the backward pass.
 int bwd_parts(int64_t rows, int64_t d) {
-  const int64_t rows_per = d % 4 == 0 && d <= 1024 ? 4 : 1;
+  const int64_t rows_per = d <= 1024 ? 4 : 1;
   const int64_t blocks = (rows + rows_per - 1) / rows_per;
   return (int)(blocks < 512 ? blocks : 512);
 }
@@ -197,8 +196,8 @@ hipError_t launch_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dt
     for_dtype(dy_dtype, [&](auto yt) {
       for_dtype(h_dtype, [&](auto ht) {
         if constexpr (yt.value != kNone && ht.value != kNone)
-          for_shape((int)d, [&](auto v, auto u, auto w_) {
-            hipLaunchKernelGGL((norm_bwd_kernel<yt.value, ht.value, v.value, u.value, w_.value>),
+          for_shape((int)d, [&](auto whole, auto u, auto w_) {
+            hipLaunchKernelGGL((norm_bwd_kernel<yt.value, ht.value, whole.value, u.value, w_.value>),
                                dim3((uint32_t)parts), dim3(kBlock<w_.value>), 0, stream, a);
           });
       });

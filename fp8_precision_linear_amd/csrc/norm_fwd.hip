@@ -29,7 +29,7 @@ struct FwdArgs {
   int32_t* bias_out;       // kOutStats, one row
 };
 
-template <int XT, int RT, int V, int U, int W, int OUT>
+template <int XT, int RT, bool WHOLE, int U, int W, int OUT>
 __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
   constexpr int kLanes = 64 * W;                 // lanes per row
   constexpr int kRows = kBlock<W> / kLanes;      // rows per workgroup
@@ -45,40 +45,40 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
   // the weight stays in registers over the workgroup's rows (where sixteen
   // waves leave enough), its loads in flight with the first row's
   constexpr bool kKeepW = W < 16;
-  float w[kKeepW ? U : 1][V];
+  float w[kKeepW ? U : 1][4];
   if constexpr (kKeepW) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[u][e] = 0.0f;
-      if (j < d) load_cached<V>(a.w, a.w_dtype, j, w[u]);
+      for (int e = 0; e < 4; ++e) w[u][e] = 0.0f;
+      if (j < d) load_weight<WHOLE>(a.w, a.w_dtype, j, d - j, w[u]);
     }
   }
   for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.rows; row += (int64_t)gridDim.x * kRows) {
     const int64_t base = row * d;
-    float h[U][V];
+    float h[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
       if (j < d) {
-        load_stream<XT, V>(a.x, base + j, h[u]);
+        load_stream<XT, WHOLE>(a.x, base + j, d - j, h[u]);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[u][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) h[u][e] = 0.0f;
       }
     }
     if constexpr (RT != kNone) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int j = (u * kLanes + t) * V;
+        const int j = (u * kLanes + t) * 4;
         if (j < d) {
-          float r[V];
-          load_stream<RT, V>(a.r, base + j, r);
+          float r[4];
+          load_stream<RT, WHOLE>(a.r, base + j, d - j, r);
 #pragma unroll
-          for (int e = 0; e < V; ++e) h[u][e] += r[e];
-          round_to<RT, V>(h[u]);
-          store_as<RT, V>(a.h, base + j, h[u]);
+          for (int e = 0; e < 4; ++e) h[u][e] += r[e];
+          round_to<RT>(h[u]);
+          store_as<RT, WHOLE>(a.h, base + j, d - j, h[u]);
         }
       }
     }
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(h[u][e], h[u][e], ss);
+      for (int e = 0; e < 4; ++e) ss = fmaf(h[u][e], h[u][e], ss);
     // two sets of words: a wave may reach the next row's sum while another
     // still reads this one's
     ss = row_sum<W>(ss, part[parity]);
@@ -96,17 +96,16 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
     uint32_t m = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = (u * kLanes + t) * V;
+      const int j = (u * kLanes + t) * 4;
       if (j < d) {
         float* wu = w[kKeepW ? u : 0];
-        if constexpr (!kKeepW) load_cached<V>(a.w, a.w_dtype, j, w[0]);
+        if constexpr (!kKeepW) load_weight<WHOLE>(a.w, a.w_dtype, j, d - j, w[0]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[u][e] = h[u][e] * rstd * wu[e];
-        if constexpr (OUT == kOutBf16) round_to<FP8_IN_BF16, V>(h[u]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) m = max(m, __float_as_uint(h[u][e]) & 0x7FFFFFFFu);
-        if constexpr (OUT == kOutBf16) store_as<FP8_IN_BF16, V>(a.y, base + j, h[u]);
-        if constexpr (OUT == kOutCodes) codes.store<V>(static_cast<uint8_t*>(a.y), base + j, h[u]);
+        for (int e = 0; e < 4; ++e) h[u][e] = h[u][e] * rstd * wu[e];
+        if constexpr (OUT == kOutBf16) round_to<FP8_IN_BF16>(h[u]);
+        m = unit_max<WHOLE>(m, d - j, h[u]);
+        if constexpr (OUT == kOutBf16) store_as<FP8_IN_BF16, WHOLE>(a.y, base + j, d - j, h[u]);
+        if constexpr (OUT == kOutCodes) codes.store<WHOLE>(static_cast<uint8_t*>(a.y), base + j, d - j, h[u]);
       }
     }
     if constexpr (OUT == kOutStats) {
@@ -122,8 +121,8 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
         const Codes c(a.fmt, b);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int j = (u * kLanes + t) * V;
-          if (j < d) c.store<V>(static_cast<uint8_t*>(a.y), base + j, h[u]);
+          const int j = (u * kLanes + t) * 4;
+          if (j < d) c.store<WHOLE>(static_cast<uint8_t*>(a.y), base + j, d - j, h[u]);
         }
       }
     } else {
@@ -136,25 +135,25 @@ __global__ __launch_bounds__(kBlock<W>) void norm_fwd_kernel(FwdArgs a) {
 
 // The second half of fp8_rmsnorm_quantize: the tensor's amax from every row's,
 // the bias from it, and the codes of y formed again from h.  A workgroup takes
-// 256 V columns, whose weights its lanes keep, of every `groups`-th row, four
+// 1024 columns, whose weights its lanes keep, of every `groups`-th row, four
 // rows in flight; the first ones' loads stand before the amax.  Rows are walked
 // from the last one: what the first half wrote last is still cached.
 constexpr int kCastRows = 4;
-template <int HT, int V>
+template <int HT, bool WHOLE>
 __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const float* rstd, const void* w, int w_dtype,
                                                         int64_t rows, int d, int col_blocks, int groups,
                                                         const uint32_t* row_amax, int fmt, int32_t margin, uint8_t* y,
                                                         uint32_t* amax, int32_t* bias) {
   __shared__ uint32_t part[4];
   const int t = threadIdx.x;
-  const int j = ((int)(blockIdx.x % col_blocks) * 256 + t) * V;
+  const int j = ((int)(blockIdx.x % col_blocks) * 256 + t) * 4;
   const int64_t group = blockIdx.x / col_blocks;
   const bool live = j < d;
-  float ww[V];
+  float ww[4];
 #pragma unroll
-  for (int e = 0; e < V; ++e) ww[e] = 0.0f;
-  if (live) load_cached<V>(w, w_dtype, j, ww);
-  Raw<HT, V> x[kCastRows];
+  for (int e = 0; e < 4; ++e) ww[e] = 0.0f;
+  if (live) load_weight<WHOLE>(w, w_dtype, j, d - j, ww);
+  Raw<HT> x[kCastRows];
   float rs[kCastRows];
   auto fetch = [&](int64_t k) {
 #pragma unroll
@@ -163,8 +162,7 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
       if (live && at < rows) {
         const int64_t row = rows - 1 - at;
         rs[q] = rstd[row];
-        using E = std::conditional_t<HT == FP8_IN_FP32, float, uint16_t>;
-        x[q] = *reinterpret_cast<const Raw<HT, V>*>(static_cast<const E*>(h) + row * d + j);
+        x[q] = load_raw<HT, WHOLE, false>(h, row * d + j, d - j);
       }
     }
   };
@@ -193,11 +191,11 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
     for (int q = 0; q < kCastRows; ++q) {
       const int64_t at = k + (int64_t)q * groups;
       if (live && at < rows) {
-        float v[V];
-        unpack<HT, V>(x[q], v);
+        float v[4];
+        unpack<HT>(x[q], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = v[e] * rs[q] * ww[e];
-        codes.store<V>(y, (rows - 1 - at) * d + j, v);
+        for (int e = 0; e < 4; ++e) v[e] = v[e] * rs[q] * ww[e];
+        codes.store<WHOLE>(y, (rows - 1 - at) * d + j, d - j, v);
       }
     }
     fetch(k + (int64_t)kCastRows * groups);
@@ -216,12 +214,12 @@ void launch_fwd(const NormProblem& p, const FwdArgs& a, hipStream_t stream) {
   for_dtype(p.x_dtype, [&](auto xt) {
     if constexpr (xt.value != kNone) {
       for_dtype(p.r ? p.r_dtype : kNone, [&](auto rt) {
-        for_shape(a.d, [&](auto v, auto u, auto w) {
+        for_shape(a.d, [&](auto whole, auto u, auto w) {
           constexpr int W = w.value;
           const int64_t rows_per = kBlock<W> / (64 * W);
           const int64_t blocks = (a.rows + rows_per - 1) / rows_per;
           const int64_t cap = W == 16 ? 512 : W == 8 ? 768 : kMaxBlocks;
-          hipLaunchKernelGGL((norm_fwd_kernel<xt.value, rt.value, v.value, u.value, W, OUT>),
+          hipLaunchKernelGGL((norm_fwd_kernel<xt.value, rt.value, whole.value, u.value, W, OUT>),
                              dim3((uint32_t)(blocks < cap ? blocks : cap)), dim3(kBlock<W>), 0, stream, a);
         });
       });
@@ -279,27 +277,24 @@ hipError_t launch_norm_quantize(const NormProblem& p, int fmt, int32_t margin, u
   if (p.rows == 1) return hipGetLastError();
   const void* h = p.r ? p.h : p.x;
   const int h_dtype = p.r ? p.r_dtype : p.x_dtype;
-  const int V = p.d % 4 == 0 ? 4 : 1;
-  const int col_blocks = (int)((p.d + 256 * V - 1) / (256 * V));
+  const int col_blocks = (int)((p.d + 1023) / 1024);
   // rows shared out over kCastBlocks workgroups, each with whole batches of
   // kCastRows where there are rows enough
   int64_t groups = (p.rows + kCastRows - 1) / kCastRows;
   const int64_t most = kCastBlocks / col_blocks > 0 ? kCastBlocks / col_blocks : 1;
   groups = groups < most ? groups : most;
   if (groups == 0) groups = 1;
-  auto run = [&](auto ht, auto v) {
-    hipLaunchKernelGGL((norm_cast_kernel<ht.value, v.value>), dim3((uint32_t)(groups * col_blocks)), dim3(256), 0,
+  auto run = [&](auto ht, auto whole) {
+    hipLaunchKernelGGL((norm_cast_kernel<ht.value, whole.value>), dim3((uint32_t)(groups * col_blocks)), dim3(256), 0,
                        stream, h, p.rstd, p.w, p.w_dtype, p.rows, (int)p.d, col_blocks, (int)groups, row_amax, fmt,
                        margin, y, amax, bias);
   };
-  using std::integral_constant;
-  if (h_dtype == FP8_IN_FP32) {
-    if (V == 4) run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, 4>{});
-    else run(integral_constant<int, FP8_IN_FP32>{}, integral_constant<int, 1>{});
-  } else {
-    if (V == 4) run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, 4>{});
-    else run(integral_constant<int, FP8_IN_BF16>{}, integral_constant<int, 1>{});
-  }
+  for_dtype(h_dtype, [&](auto ht) {
+    if constexpr (ht.value != kNone) {
+      if (p.d % 4 == 0) run(ht, std::bool_constant<true>{});
+      else run(ht, std::bool_constant<false>{});
+    }
+  });
   return hipGetLastError();
 }
 

@@ -11,10 +11,11 @@
 // stored h, differentiates exactly the function the forward computed.  Sums,
 // rstd and y are fp32.
 //
-// HBM-bound: a row (d <= 32768; 16384 where d is not a multiple of 4) stays in registers between the sum of squares
-// and the output, so every input is read once and every output written once.
-// One wave, four or sixteen take a row, 16 bytes per fp32 load and 4 or 8
-// units in flight per lane; sums go through wave shuffles and LDS.
+// HBM-bound: a row (d <= 32768; 16384 where d is not a multiple of 4) stays in
+// registers between the sum of squares and the output, so every input is read
+// once and every output written once.  One, four, eight or sixteen waves take a
+// row, in units of four elements (16 bytes of fp32), two to eight of them in
+// flight per lane; sums go through wave shuffles and LDS.
 #pragma once
 
 #include <type_traits>
@@ -30,111 +31,118 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNone = -1;  // "no residual" as a type
 
-// V consecutive elements of type DT (FP8_IN_BF16 or FP8_IN_FP32) as they lie in
-// memory, loaded past the caches (each input is read once), and as fp32.
-template <int DT, int V>
-using Raw = std::conditional_t<DT == FP8_IN_FP32, std::conditional_t<V == 4, f32x4, float>,
-                               std::conditional_t<V == 4, u32x2, uint16_t>>;
-template <int DT, int V>
-__device__ __forceinline__ Raw<DT, V> load_raw(const void* p, int64_t i) {
+// A unit is four consecutive elements.  WHOLE: d is a multiple of 4, so every
+// row starts on 16-byte boundaries (8 of bf16, 4 of codes) and has whole units
+// only.  Otherwise a unit lies at any element -- still one load or store, which
+// the hardware takes at any address (8000 x 4099 in 76 us, element by element
+// 144; 4000 x 3001 backward in 43, element by element 70) -- and a row's last one may hold fewer: `left`
+// elements of the row lie at and after a unit's first.
+typedef f32x4 f32x4_loose __attribute__((aligned(4)));
+typedef u32x2 u32x2_loose __attribute__((aligned(2)));
+typedef uint32_t u32_loose __attribute__((aligned(1)));
+
+// A unit of type DT (FP8_IN_BF16 or FP8_IN_FP32) as it lies in memory, loaded
+// past the caches if STREAM (each input is read once), and as fp32.  Elements
+// past the row are zeros.
+template <int DT>
+using Raw = std::conditional_t<DT == FP8_IN_FP32, f32x4, u32x2>;
+template <int DT, bool WHOLE, bool STREAM>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p, int64_t i, int left) {
   using E = std::conditional_t<DT == FP8_IN_FP32, float, uint16_t>;
-  return __builtin_nontemporal_load(reinterpret_cast<const Raw<DT, V>*>(static_cast<const E*>(p) + i));
+  using Loose = std::conditional_t<DT == FP8_IN_FP32, f32x4_loose, u32x2_loose>;
+  using At = std::conditional_t<WHOLE, Raw<DT>, Loose>;
+  const E* q = static_cast<const E*>(p) + i;
+  if (WHOLE || left >= 4) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const At*>(q));
+    else return *reinterpret_cast<const At*>(q);
+  }
+  Raw<DT> r{};
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    if (e < left) {
+      if constexpr (DT == FP8_IN_FP32) r[e] = q[e];
+      else r[e >> 1] |= (uint32_t)q[e] << (16 * (e & 1));
+    }
+  }
+  return r;
 }
-template <int DT, int V>
-__device__ __forceinline__ void unpack(const Raw<DT, V>& r, float (&v)[V]) {
-  if constexpr (DT == FP8_IN_FP32 && V == 4) {
+template <int DT>
+__device__ __forceinline__ void unpack(const Raw<DT>& r, float (&v)[4]) {
+  if constexpr (DT == FP8_IN_FP32) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = r[e];
-  } else if constexpr (DT == FP8_IN_FP32) {
-    v[0] = r;
-  } else if constexpr (V == 4) {
+  } else {
     v[0] = __uint_as_float(r[0] << 16);
     v[1] = __uint_as_float(r[0] & 0xFFFF0000u);
     v[2] = __uint_as_float(r[1] << 16);
     v[3] = __uint_as_float(r[1] & 0xFFFF0000u);
-  } else {
-    v[0] = __uint_as_float((uint32_t)r << 16);
   }
 }
-template <int DT, int V>
-__device__ __forceinline__ void load_stream(const void* p, int64_t i, float (&v)[V]) {
-  unpack<DT, V>(load_raw<DT, V>(p, i), v);
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void load_stream(const void* p, int64_t i, int left, float (&v)[4]) {
+  unpack<DT>(load_raw<DT, WHOLE, true>(p, i, left), v);
 }
 
-// Ordinary loads, the type chosen at run time (the weight, and h on its second
-// reading: both come from a cache).
-template <int V>
-__device__ __forceinline__ void load_cached(const void* p, int dt, int64_t i, float (&v)[V]) {
-  if (dt == FP8_IN_FP32) {
-    const float* q = static_cast<const float*>(p) + i;
-    if constexpr (V == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(q);
-      v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-    } else {
-      v[0] = *q;
-    }
-  } else {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-    if constexpr (V == 4) {
-      const uint2 t = *reinterpret_cast<const uint2*>(q);
-      v[0] = __uint_as_float(t.x << 16);
-      v[1] = __uint_as_float(t.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(t.y << 16);
-      v[3] = __uint_as_float(t.y & 0xFFFF0000u);
-    } else {
-      v[0] = __uint_as_float((uint32_t)*q << 16);
-    }
+// The weight, its type chosen at run time; it comes from a cache.
+template <bool WHOLE>
+__device__ __forceinline__ void load_weight(const void* p, int dt, int64_t i, int left, float (&v)[4]) {
+  if (dt == FP8_IN_FP32) unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(p, i, left), v);
+  else unpack<FP8_IN_BF16>(load_raw<FP8_IN_BF16, WHOLE, false>(p, i, left), v);
+}
+
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void store_as(void* p, int64_t i, int left, const float (&v)[4]) {
+  using E = std::conditional_t<DT == FP8_IN_FP32, float, uint16_t>;
+  using Loose = std::conditional_t<DT == FP8_IN_FP32, f32x4_loose, u32x2_loose>;
+  using At = std::conditional_t<WHOLE, Raw<DT>, Loose>;
+  E* q = static_cast<E*>(p) + i;
+  Raw<DT> r;
+  if constexpr (DT == FP8_IN_FP32) r = f32x4{v[0], v[1], v[2], v[3]};
+  else r = u32x2{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+  if (WHOLE || left >= 4) {
+    *reinterpret_cast<At*>(q) = r;
+    return;
   }
-}
-
-template <int DT, int V>
-__device__ __forceinline__ void store_as(void* p, int64_t i, const float (&v)[V]) {
-  if constexpr (DT == FP8_IN_FP32) {
-    float* q = static_cast<float*>(p) + i;
-    if constexpr (V == 4)
-      *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *q = v[0];
-  } else {
-    uint16_t* q = static_cast<uint16_t*>(p) + i;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(q) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-    else
-      *q = (uint16_t)bf16x2(v[0], 0.0f);
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    if (e < left) {
+      if constexpr (DT == FP8_IN_FP32) q[e] = r[e];
+      else q[e] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
+    }
   }
 }
 
 // Rounds v to type DT in place.
-template <int DT, int V>
-__device__ __forceinline__ void round_to(float (&v)[V]) {
-  if constexpr (DT == FP8_IN_BF16) {
-    if constexpr (V == 4) {
-      const uint32_t a = bf16x2(v[0], v[1]), b = bf16x2(v[2], v[3]);
-      v[0] = __uint_as_float(a << 16);
-      v[1] = __uint_as_float(a & 0xFFFF0000u);
-      v[2] = __uint_as_float(b << 16);
-      v[3] = __uint_as_float(b & 0xFFFF0000u);
-    } else {
-      v[0] = __uint_as_float(bf16x2(v[0], 0.0f) << 16);
-    }
-  }
+template <int DT>
+__device__ __forceinline__ void round_to(float (&v)[4]) {
+  if constexpr (DT == FP8_IN_BF16) unpack<FP8_IN_BF16>(u32x2{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])}, v);
+}
+
+// The largest magnitude (fp32 bits) of m and a unit's elements.
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t unit_max(uint32_t m, int left, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (WHOLE || e < left) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  return m;
 }
 
 // The codes of v * 2^b (E4M3 or E5M2).
 struct Codes {
   int fmt;
-  int32_t b;
   Coder<FP8_E4M3> e4;
   Coder<FP8_E5M2> e5;
-  __device__ __forceinline__ Codes(int fmt_, int32_t b_) : fmt(fmt_), b(b_), e4(b_), e5(b_) {}
-  template <int V>
-  __device__ __forceinline__ void store(uint8_t* y, int64_t i, const float (&v)[V]) const {
-    if constexpr (V == 4) {
-      *reinterpret_cast<uint32_t*>(y + i) = fmt == FP8_E4M3 ? e4.four(v) : e5.four(v);
-    } else {
-      const uint32_t u = __float_as_uint(v[0]);
-      y[i] = (uint8_t)(fmt == FP8_E4M3 ? fp8_code<FP8_E4M3>(u, b) : fp8_code<FP8_E5M2>(u, b));
+  __device__ __forceinline__ Codes(int fmt_, int32_t b) : fmt(fmt_), e4(b), e5(b) {}
+  template <bool WHOLE>
+  __device__ __forceinline__ void store(uint8_t* y, int64_t i, int left, const float (&v)[4]) const {
+    const uint32_t c = fmt == FP8_E4M3 ? e4.four(v) : e5.four(v);
+    if (WHOLE || left >= 4) {
+      *reinterpret_cast<std::conditional_t<WHOLE, uint32_t, u32_loose>*>(y + i) = c;
+      return;
     }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < left) y[i + e] = (uint8_t)(c >> (8 * e));
   }
 };
 
@@ -188,30 +196,27 @@ __device__ __forceinline__ void fold_amax_wave(uint32_t m, uint32_t* amax) {
 
 __global__ void clear_kernel(uint32_t* p) { *p = 0u; }
 
-// The shapes a row length runs in: V elements per unit (4 where rows start on
-// 16-byte boundaries whatever their type), W waves per row, U units per lane.
-// Fewer units a lane and more waves a row are faster as long as the row's sum
-// does not dominate: rows of 1028 to 2048 on four waves instead of one, 28 us
-// against 33 over 8000 x 2048 forward and 25 against 27 over 4095 x 2048
-// backward; rows of 4100 to 8192 on eight instead of four, 94 against 100 over
-// 8192 x 8192 and 53 against 56 over 4095 x 5120.
+// The shapes a row length runs in: whole units or not, U units per lane, W
+// waves per row.  Fewer units a lane and more waves a row are faster as long as
+// the row's sum does not dominate: rows of 1028 to 2048 on four waves instead of
+// one, 28 us against 33 over 8000 x 2048 forward and 25 against 27 over 4095 x
+// 2048 backward; rows of 4100 to 8192 on eight instead of four, 94 against 100
+// over 8192 x 8192 and 53 against 56 over 4095 x 5120.
 template <typename F>
 void for_shape(int d, F&& f) {
+  using std::bool_constant;
   using std::integral_constant;
-#define FP8LIN_SHAPE(V, U, W) \
-  f(integral_constant<int, V>{}, integral_constant<int, U>{}, integral_constant<int, W>{})
-  if (d % 4 == 0) {
-    if (d <= 1024) FP8LIN_SHAPE(4, 4, 1);
-    else if (d <= 2048) FP8LIN_SHAPE(4, 2, 4);
-    else if (d <= 4096) FP8LIN_SHAPE(4, 4, 4);
-    else if (d <= 8192) FP8LIN_SHAPE(4, 4, 8);
-    else if (d <= 16384) FP8LIN_SHAPE(4, 4, 16);
-    else FP8LIN_SHAPE(4, 8, 16);
-  } else {
-    if (d <= 2048) FP8LIN_SHAPE(1, 8, 4);
-    else FP8LIN_SHAPE(1, 16, 16);
-  }
-#undef FP8LIN_SHAPE
+  auto units = [&](auto whole) {
+    auto go = [&](auto u, auto w) { f(whole, u, w); };
+    if (d <= 1024) go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    else if (d <= 2048) go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    else if (d <= 4096) go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    else if (d <= 8192) go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    else if (d <= 16384) go(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+    else if constexpr (decltype(whole)::value) go(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+  };
+  if (d % 4 == 0) units(bool_constant<true>{});
+  else units(bool_constant<false>{});
 }
 
 template <typename F>

@@ -19,7 +19,8 @@ E = 2.0 ** -18
 EPS = 1e-5
 BF, F32 = torch.bfloat16, torch.float32
 SHAPES = [(1, 1), (1, 8192), (3, 4), (5, 7), (2, 64), (130, 768), (17, 1000), (9, 1026), (4, 2048), (33, 2052),
-          (6, 4096), (3, 4099), (7, 5120), (2, 8191), (2, 8196), (3, 16384), (2, 16383), (2, 32768)]
+          (6, 4096), (3, 4099), (7, 5120), (2, 8191), (2, 8196), (3, 16384), (2, 16383), (2, 32768),
+          (9, 1021), (6, 2047), (5, 4097), (3, 8190), (2, 2), (3, 3)]
 
 
 @pytest.fixture(scope="module")
