@@ -27,6 +27,11 @@
 // down to 2^-22 of the largest, against bf16's 8 bits.  The reference follows
 // the row maximum lazily: it moves only when a logit exceeds it by
 // kShift - 1, so that most tiles rescale nothing and p stays below 2^15.
+//
+// Where logits are huge, s * kscale is rounded before the reference is
+// subtracted, as it was for the maximum that set the reference: fused into one
+// operation its rounding error alone, 2^-24 of the logit, would drive the
+// largest p out of fp16's range from 2^26 on.
 #pragma once
 
 #include <type_traits>
@@ -71,7 +76,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 constexpr int kAttnTile = 64;          // keys per step
 constexpr float kShift = 8.0f;
 constexpr float kLazy = 15.0f;         // rescale when t > m + kLazy (m includes the shift)
-constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
+constexpr float kNoRef = -0x1.fffffep127f;  // reference of a row that has seen nothing
 constexpr int kNoBias = 1 << 20;       // value bias before the first block
 template <int FMT>
 constexpr int kHead = FMT == FP8_E4M3 ? 7 : 0;  // 448 * 2^7 and 57344 both fit fp16
@@ -124,6 +129,12 @@ __device__ __forceinline__ float pow2_scale(int e) {
 // logit of -inf times it stays -inf.
 __device__ __forceinline__ float key_scale(float scale_log2, int kb) {
   return fmaxf(scale_log2 * pow2_scale(-kb), 0x1p-126f);
+}
+
+// A product that is not fused with what follows.
+__device__ __forceinline__ float rounded(float s, float kscale) {
+#pragma clang fp contract(off)
+  return s * kscale;
 }
 
 // 8 codes -> 8 bf16, exactly.

@@ -2,12 +2,19 @@
 // FP8 cache: attn_common.h has the mathematics.
 //
 // HBM-bound: every cached byte of the (sequence, key head) is read once and
-// serves the group's query rows, 16 per MFMA tile.  One workgroup of four
-// waves per chunk of keys; the waves take the chunk's tiles of 64 keys in
-// turn, each with its own running maximum, sum and O, and meet in LDS at the
-// end.  Keys and values go from memory straight to registers: a load
-// instruction covers whole 64-byte runs, and the next tile's keys are in
-// flight during this tile's softmax, its values during the next one's logits.
+// serves the group's query rows, 16 per MFMA tile.  Workgroups of four waves
+// take the keys of one segment, or an even share of all of them; the waves take
+// its tiles of 64 keys in turn, each with its own running maximum, sum and O,
+// and meet in LDS at the end.  Keys and values go from memory straight to
+// registers: a load instruction covers whole 64-byte runs, and the next tile's
+// keys are in flight during this tile's softmax, its values during the next
+// one's logits.
+//
+// 131071 tokens of 8 heads of 128: 268 MB in 52-54 us (5.1 TB/s), and 6 us of
+// join; 32 sequences of 1000 to 8191 tokens: 302 MB in 67-69 us (4.5 TB/s: the
+// start, the walk to a share's first segment and the meeting in LDS cost some
+// 10 us of it), and 5 us of join.  One workgroup per segment instead of even
+// shares took 107 us over the 32.
 #include "attn_common.h"
 
 namespace fp8lin {
@@ -159,256 +166,257 @@ __global__ __launch_bounds__(64 * kWaves, (kOcc<D, RB>)) void attn_rows_kernel(A
   }
 
   for (;;) {
-  seg.last = (int)min((int64_t)pair.tiles, seg.first + (end - at));
-  const int sequence = a.row_tiles == 1 ? seg.pair : seg.pair / a.row_tiles;
-  const int row0 = (seg.pair - sequence * a.row_tiles) * kRows, head = seg.head;
-  const KVSeq s = pair.s;
-  const int rows = s.n * G;
-  const AttnSpan span = attn_span(a, s, row0, kRows);
-  const int kbeg = span.lo + seg.first * kAttnTile, kend = min(span.hi, span.lo + seg.last * kAttnTile);
+    seg.last = (int)min((int64_t)pair.tiles, seg.first + (end - at));
+    const int sequence = a.row_tiles == 1 ? seg.pair : seg.pair / a.row_tiles;
+    const int row0 = (seg.pair - sequence * a.row_tiles) * kRows, head = seg.head;
+    const KVSeq s = pair.s;
+    const int rows = s.n * G;
+    const AttnSpan span = attn_span(a, s, row0, kRows);
+    const int kbeg = span.lo + seg.first * kAttnTile, kend = min(span.hi, span.lo + seg.last * kAttnTile);
 
-  // Operand roles.  Logits: row r16 of sub-tile `sub` is the key
-  // 16 (r16 / 4) + 4 sub + r16 % 4 of the tile; then S^T's four results of
-  // sub-tile `sub` in lane (r16, g) are the keys 16 g + 4 sub + 0..3.
-  // ONE: blocks hold whole tiles, so a tile has one block, the same in every
-  // lane; otherwise each granule of 16 keys has its own.
-  const int gk = r16 >> 2;
-  auto block_of = [&](int pos) {
-    return pos < kend ? kv_block(a.cache, a.batch, sequence, pos >> a.block_shift) : -1;
-  };
-  auto cell = [&](int block) { return (int64_t)max(block, 0) * H + head; };
-  const uint32_t k_lane = ((ONE ? 16 * gk : 0) + (r16 & 3)) * D + 16 * g, v_lane = r16 * BS + (ONE ? 16 * g : 0);
-  uint4 kreg[4][J], vreg[DT];
-  auto load_k = [&](int T, int block) {
-    const uint8_t* p = a.cache.k + cell(block) * BS * D + ((T + (ONE ? 0 : 16 * gk)) & (BS - 1)) * D;
+    // Operand roles.  Logits: row r16 of sub-tile `sub` is the key
+    // 16 (r16 / 4) + 4 sub + r16 % 4 of the tile; then S^T's four results of
+    // sub-tile `sub` in lane (r16, g) are the keys 16 g + 4 sub + 0..3.
+    // ONE: blocks hold whole tiles, so a tile has one block, the same in every
+    // lane; otherwise each granule of 16 keys has its own.
+    const int gk = r16 >> 2;
+    auto block_of = [&](int pos) {
+      return pos < kend ? kv_block(a.cache, a.batch, sequence, pos >> a.block_shift) : -1;
+    };
+    auto cell = [&](int block) { return (int64_t)max(block, 0) * H + head; };
+    const uint32_t k_lane = ((ONE ? 16 * gk : 0) + (r16 & 3)) * D + 16 * g, v_lane = r16 * BS + (ONE ? 16 * g : 0);
+    uint4 kreg[4][J], vreg[DT];
+    auto load_k = [&](int T, int block) {
+      const uint8_t* p = a.cache.k + cell(block) * BS * D + ((T + (ONE ? 0 : 16 * gk)) & (BS - 1)) * D;
 #pragma unroll
-    for (int sub = 0; sub < 4; ++sub)
+      for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-      for (int j = 0; j < J; ++j) kreg[sub][j] = *reinterpret_cast<const uint4*>((p + 4 * sub * D + 64 * j) + k_lane);
-  };
-  auto load_v = [&](int T, int block) {
-    const uint8_t* p = a.cache.v + cell(block) * BS * D + ((T + (ONE ? 0 : 16 * g)) & (BS - 1));
+        for (int j = 0; j < J; ++j) kreg[sub][j] = *reinterpret_cast<const uint4*>((p + 4 * sub * D + 64 * j) + k_lane);
+    };
+    auto load_v = [&](int T, int block) {
+      const uint8_t* p = a.cache.v + cell(block) * BS * D + ((T + (ONE ? 0 : 16 * g)) & (BS - 1));
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vreg[d] = *reinterpret_cast<const uint4*>((p + 16 * d * BS) + v_lane);
-  };
-  auto uniform = [](int v) { return ONE ? __builtin_amdgcn_readfirstlane(v) : v; };
+      for (int d = 0; d < DT; ++d) vreg[d] = *reinterpret_cast<const uint4*>((p + 16 * d * BS) + v_lane);
+    };
+    auto uniform = [](int v) { return ONE ? __builtin_amdgcn_readfirstlane(v) : v; };
 
-  constexpr int kStep = kWaves * kAttnTile;
-  int T = kbeg + wave * kAttnTile;
-  int bk = -1, bv = -1, kb = 0, vb = 0;
-  auto ids = [&](int T, int& k, int& v) {
-    v = block_of(ONE ? T : T + 16 * g);
-    k = ONE ? v : block_of(T + 16 * gk);
-  };
-  int nbk, nbv;
-  if (T < kend) ids(T, bk, bv);
-  ids(T + kStep, nbk, nbv);
-  if (T < kend) {
-    bk = uniform(bk), bv = uniform(bv);
-    load_k(T, bk);
-    load_v(T, bv);
-    kb = a.cache.k_bias[cell(bv)];
-    vb = a.cache.v_bias[cell(bv)];
-  }
-
-  // this lane's rows: queries and visible keys [lo, hi)
-  v8b q[RB][J][2];
-  int lo[RB], hi[RB];
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    const int row = row0 + 16 * rb + r16;
-    lo[rb] = -0x7FFFFFFF, hi[rb] = 0x7FFFFFFF;  // past the last row: anything, not stored
-#pragma unroll
-    for (int j = 0; j < J; ++j) q[rb][j][0] = q[rb][j][1] = v8b{};
-    if (row < rows) {
-      const int pos = s.start + row / G;
-      hi[rb] = a.causal ? min(pos + 1, s.len) : s.len;
-      if (a.window) lo[rb] = pos - a.window + 1;
-      const uint16_t* qp = a.q + (int64_t)(s.first + row / G) * a.q_stride + (head * G + row % G) * D + 16 * g;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          q[rb][j][c] = __builtin_bit_cast(
-              v8b, sign_queries(*reinterpret_cast<const uint4*>(qp + 64 * j + 8 * c), a.scale));
+    constexpr int kStep = kWaves * kAttnTile;
+    int T = kbeg + wave * kAttnTile;
+    int bk = -1, bv = -1, kb = 0, vb = 0;
+    auto ids = [&](int T, int& k, int& v) {
+      v = block_of(ONE ? T : T + 16 * g);
+      k = ONE ? v : block_of(T + 16 * gk);
+    };
+    int nbk, nbv;
+    if (T < kend) ids(T, bk, bv);
+    ids(T + kStep, nbk, nbv);
+    if (T < kend) {
+      bk = uniform(bk), bv = uniform(bv);
+      load_k(T, bk);
+      load_v(T, bv);
+      kb = a.cache.k_bias[cell(bv)];
+      vb = a.cache.v_bias[cell(bv)];
     }
-  }
 
-  v4f o[RB][DT];
-  float m[RB], l[RB];
-  int bref = kNoBias;
+    // this lane's rows: queries and visible keys [lo, hi)
+    v8b q[RB][J][2];
+    int lo[RB], hi[RB];
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    m[rb] = kNoRef, l[rb] = 0.0f;
+    for (int rb = 0; rb < RB; ++rb) {
+      const int row = row0 + 16 * rb + r16;
+      lo[rb] = -0x7FFFFFFF, hi[rb] = 0x7FFFFFFF;  // past the last row: anything, not stored
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[rb][d] = v4f{0, 0, 0, 0};
-  }
+      for (int j = 0; j < J; ++j) q[rb][j][0] = q[rb][j][1] = v8b{};
+      if (row < rows) {
+        const int pos = s.start + row / G;
+        hi[rb] = a.causal ? min(pos + 1, s.len) : s.len;
+        if (a.window) lo[rb] = pos - a.window + 1;
+        const uint16_t* qp = a.q + (int64_t)(s.first + row / G) * a.q_stride + (head * G + row % G) * D + 16 * g;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            q[rb][j][c] = __builtin_bit_cast(
+                v8b, sign_queries(*reinterpret_cast<const uint4*>(qp + 64 * j + 8 * c), a.scale));
+      }
+    }
 
-  for (; T < kend; T += kStep) {
-    // logits
-    v4f sacc[RB][4];
+    v4f o[RB][DT];
+    float m[RB], l[RB];
+    int bref = kNoBias;
 #pragma unroll
-    for (int sub = 0; sub < 4; ++sub) {
-      __builtin_amdgcn_sched_barrier(0);  // widen a sub-tile at a time: registers
+    for (int rb = 0; rb < RB; ++rb) {
+      m[rb] = kNoRef, l[rb] = 0.0f;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) sacc[rb][sub] = v4f{0, 0, 0, 0};
+      for (int d = 0; d < DT; ++d) o[rb][d] = v4f{0, 0, 0, 0};
+    }
+
+    for (; T < kend; T += kStep) {
+      // logits
+      v4f sacc[RB][4];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint4 w = kreg[sub][j];
-        const v8b k0 = widen_bf16<FMT>(w.x, w.y), k1 = widen_bf16<FMT>(w.z, w.w);
+      for (int sub = 0; sub < 4; ++sub) {
+        __builtin_amdgcn_sched_barrier(0);  // widen a sub-tile at a time: registers
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) sacc[rb][sub] = v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint4 w = kreg[sub][j];
+          const v8b k0 = widen_bf16<FMT>(w.x, w.y), k1 = widen_bf16<FMT>(w.z, w.w);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            sacc[rb][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rb][j][0], sacc[rb][sub], 0, 0, 0);
+            sacc[rb][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rb][j][1], sacc[rb][sub], 0, 0, 0);
+          }
+        }
+      }
+      const int block = bv;
+      const float kscale = key_scale(a.scale_log2, kb);
+      const int vbias = block >= 0 ? vb : kNoBias;
+      // the next tile's keys, and the block numbers of the one after
+      const bool more = T + kStep < kend;
+      if (more) {
+        bk = uniform(nbk), bv = uniform(nbv);
+        load_k(T + kStep, bk);
+        kb = a.cache.k_bias[cell(bv)];
+        vb = a.cache.v_bias[cell(bv)];
+        ids(T + 2 * kStep, nbk, nbv);
+      }
+
+      bool inside = block >= 0;
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) inside = inside && T + kAttnTile <= hi[rb] && T >= lo[rb];
+      const bool masked = !__all(inside);
+      v8h p[RB][2];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        if (masked) {
+          const int first = T + 16 * g;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (block < 0 || first + e < lo[rb] || first + e >= hi[rb]) sacc[rb][e >> 2][e & 3] = -INFINITY;
+        }
+        float top = sacc[rb][0][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = raw_max(top, sacc[rb][e >> 2][e & 3]);
+        top = swap16_max(swap32_max(top * kscale));
+        const bool move = top > m[rb] + kLazy;
+        if (__any(move)) {
+          const float to = move ? top - kShift : m[rb];
+          const float f = __builtin_amdgcn_exp2f(m[rb] - to);
+          m[rb] = to;
+          l[rb] *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[rb][d] *= f;
+        }
+        float t[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          t[e] = __builtin_amdgcn_exp2f(rounded(sacc[rb][e >> 2][e & 3], kscale) - m[rb]);
+          l[rb] += t[e];
+        }
+        p[rb][0] = pack_f16(t);
+        p[rb][1] = pack_f16(t + 8);
+      }
+
+      // values, at the scale of the smallest bias so far
+      const int low = __builtin_amdgcn_readfirstlane(ONE ? vbias : swap16_min(swap32_min(vbias)));
+      if (low < bref) {
+        if (bref != kNoBias) {
+          const float f = pow2_scale(low - bref);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[rb][d] *= f;
+        }
+        bref = low;
+      }
+      const float vscale = pow2_scale(min(bref, 1000) - min(vbias, 1000) + kHead<FMT>);
+      if (masked) clean_values<FMT, RB, DT>(vreg, o, [&](int rb, int e) {
+        return !(block < 0 || T + 16 * g + e < lo[rb] || T + 16 * g + e >= hi[rb]);
+      });
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+        const uint4 w = vreg[d];
+        const v8h v0 = widen_f16<FMT>(w.x, w.y, vscale), v1 = widen_f16<FMT>(w.z, w.w, vscale);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-          sacc[rb][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rb][j][0], sacc[rb][sub], 0, 0, 0);
-          sacc[rb][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rb][j][1], sacc[rb][sub], 0, 0, 0);
+          o[rb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[rb][0], o[rb][d], 0, 0, 0);
+          o[rb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[rb][1], o[rb][d], 0, 0, 0);
+        }
+      }
+      if (more) load_v(T + kStep, bv);
+    }
+
+    // the waves' results meet: row r of the workgroup, four waves in order
+    const bool whole = seg.first == 0 && seg.last == pair.tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.first == 0);  // of a partial result
+    if (a.shares && seg.first == 0 && threadIdx.x == 0)
+      a.segments[(int64_t)seg.pair * H + head] =
+          make_int2(blockIdx.x, (int)min((int64_t)a.shares - 1, (at + pair.tiles - 1) / share));
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      l[rb] = swap16_sum(swap32_sum(l[rb]));
+      if (g == 0) {
+        sm[wave][16 * rb + r16] = m[rb];
+        sl[wave][16 * rb + r16] = l[rb];
+      }
+    }
+    if (lane == 0) sb[wave] = bref;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      if (rb > 0) __syncthreads();
+#pragma unroll
+      for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&so[wave][r16][16 * d + 4 * g]) = o[rb][d];
+      __syncthreads();
+      int low = sb[0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) low = min(low, sb[w]);
+      for (int x = threadIdx.x; x < 16 * (D / 4); x += 64 * kWaves) {
+        const int r = x / (D / 4), d = 4 * (x % (D / 4));
+        const int row = row0 + 16 * rb + r;
+        if (row >= rows) continue;
+        float top = sm[0][16 * rb + r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][16 * rb + r]);
+        float total = 0.0f;
+        v4f sum{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(sm[w][16 * rb + r] - top);
+          total += sl[w][16 * rb + r] * f;
+          sum += *reinterpret_cast<const v4f*>(&so[w][r][d]) * (sb[w] == kNoBias ? 0.0f : f * pow2_scale(low - sb[w]));
+        }
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = total == 0.0f ? 0.0f : __builtin_ldexpf(sum[e] * inv, -(low + kHead<FMT>));
+        const float lse2 = total == 0.0f ? -INFINITY : top + log2f(total);
+        if (whole) {
+          const int64_t to = (int64_t)(s.first + row / G) * a.q_heads + head * G + row % G;
+          *reinterpret_cast<uint2*>(a.out + to * D + d) =
+              make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
+          if (d == 0 && a.lse) a.lse[to] = lse2 * 0.693147180559945309f;
+        } else {
+          const int64_t to = slot * kRows + 16 * rb + r;
+          *reinterpret_cast<v4f*>(a.part_o + to * D + d) = sum;
+          if (d == 0) a.part_lse[to] = lse2;
         }
       }
     }
-    const int block = bv;
-    const float kscale = key_scale(a.scale_log2, kb);
-    const int vbias = block >= 0 ? vb : kNoBias;
-    // the next tile's keys, and the block numbers of the one after
-    const bool more = T + kStep < kend;
-    if (more) {
-      bk = uniform(nbk), bv = uniform(nbv);
-      load_k(T + kStep, bk);
-      kb = a.cache.k_bias[cell(bv)];
-      vb = a.cache.v_bias[cell(bv)];
-      ids(T + 2 * kStep, nbk, nbv);
-    }
 
-    bool inside = block >= 0;
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) inside = inside && T + kAttnTile <= hi[rb] && T >= lo[rb];
-    const bool masked = !__all(inside);
-    v8h p[RB][2];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      if (masked) {
-        const int first = T + 16 * g;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (block < 0 || first + e < lo[rb] || first + e >= hi[rb]) sacc[rb][e >> 2][e & 3] = -INFINITY;
-      }
-      float top = sacc[rb][0][0];
-#pragma unroll
-      for (int e = 1; e < 16; ++e) top = raw_max(top, sacc[rb][e >> 2][e & 3]);
-      top = swap16_max(swap32_max(top * kscale));
-      const bool move = top > m[rb] + kLazy;
-      if (__any(move)) {
-        const float to = move ? top - kShift : m[rb];
-        const float f = __builtin_amdgcn_exp2f(m[rb] - to);
-        m[rb] = to;
-        l[rb] *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[rb][d] *= f;
-      }
-      float t[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        t[e] = __builtin_amdgcn_exp2f(fmaf(sacc[rb][e >> 2][e & 3], kscale, -m[rb]));
-        l[rb] += t[e];
-      }
-      p[rb][0] = pack_f16(t);
-      p[rb][1] = pack_f16(t + 8);
+    // the next segment of the share
+    at += seg.last - seg.first;
+    if (at >= end) return;
+    __syncthreads();  // LDS is free again
+    seg.first = 0;
+    if (++seg.head == H) {
+      seg.head = 0;
+      do {
+        if (++seg.pair >= a.batch.batch * a.row_tiles) return;
+        pair = pair_from(pair_of<kRows>(a, seg.pair), 0);
+      } while (pair.tiles == 0);
     }
-
-    // values, at the scale of the smallest bias so far
-    const int low = __builtin_amdgcn_readfirstlane(ONE ? vbias : swap16_min(swap32_min(vbias)));
-    if (low < bref) {
-      if (bref != kNoBias) {
-        const float f = pow2_scale(low - bref);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[rb][d] *= f;
-      }
-      bref = low;
-    }
-    const float vscale = pow2_scale(min(bref, 1000) - min(vbias, 1000) + kHead<FMT>);
-    if (masked) clean_values<FMT, RB, DT>(vreg, o, [&](int rb, int e) {
-      return !(block < 0 || T + 16 * g + e < lo[rb] || T + 16 * g + e >= hi[rb]);
-    });
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-      const uint4 w = vreg[d];
-      const v8h v0 = widen_f16<FMT>(w.x, w.y, vscale), v1 = widen_f16<FMT>(w.z, w.w, vscale);
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        o[rb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[rb][0], o[rb][d], 0, 0, 0);
-        o[rb][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[rb][1], o[rb][d], 0, 0, 0);
-      }
-    }
-    if (more) load_v(T + kStep, bv);
-  }
-
-  // the waves' results meet: row r of the workgroup, four waves in order
-  const bool whole = seg.first == 0 && seg.last == pair.tiles;
-  const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.first == 0);  // of a partial result
-  if (a.shares && seg.first == 0 && threadIdx.x == 0)
-    a.segments[(int64_t)seg.pair * H + head] = make_int2(blockIdx.x, (int)min((int64_t)a.shares - 1, (at + pair.tiles - 1) / share));
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    l[rb] = swap16_sum(swap32_sum(l[rb]));
-    if (g == 0) {
-      sm[wave][16 * rb + r16] = m[rb];
-      sl[wave][16 * rb + r16] = l[rb];
-    }
-  }
-  if (lane == 0) sb[wave] = bref;
-#pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    if (rb > 0) __syncthreads();
-#pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&so[wave][r16][16 * d + 4 * g]) = o[rb][d];
-    __syncthreads();
-    int low = sb[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) low = min(low, sb[w]);
-    for (int x = threadIdx.x; x < 16 * (D / 4); x += 64 * kWaves) {
-      const int r = x / (D / 4), d = 4 * (x % (D / 4));
-      const int row = row0 + 16 * rb + r;
-      if (row >= rows) continue;
-      float top = sm[0][16 * rb + r];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][16 * rb + r]);
-      float total = 0.0f;
-      v4f sum{0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm[w][16 * rb + r] - top);
-        total += sl[w][16 * rb + r] * f;
-        sum += *reinterpret_cast<const v4f*>(&so[w][r][d]) * (sb[w] == kNoBias ? 0.0f : f * pow2_scale(low - sb[w]));
-      }
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = total == 0.0f ? 0.0f : __builtin_ldexpf(sum[e] * inv, -(low + kHead<FMT>));
-      const float lse2 = total == 0.0f ? -INFINITY : top + log2f(total);
-      if (whole) {
-        const int64_t to = (int64_t)(s.first + row / G) * a.q_heads + head * G + row % G;
-        *reinterpret_cast<uint2*>(a.out + to * D + d) =
-            make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
-        if (d == 0 && a.lse) a.lse[to] = lse2 * 0.693147180559945309f;
-      } else {
-        const int64_t to = slot * kRows + 16 * rb + r;
-        *reinterpret_cast<v4f*>(a.part_o + to * D + d) = sum;
-        if (d == 0) a.part_lse[to] = lse2;
-      }
-    }
-  }
-
-  // the next segment of the share
-  at += seg.last - seg.first;
-  if (at >= end) return;
-  __syncthreads();  // LDS is free again
-  seg.first = 0;
-  if (++seg.head == H) {
-    seg.head = 0;
-    do {
-      if (++seg.pair >= a.batch.batch * a.row_tiles) return;
-      pair = pair_from(pair_of<kRows>(a, seg.pair), 0);
-    } while (pair.tiles == 0);
-  }
   }
 }
 

@@ -1,7 +1,13 @@
 // Attention of many query rows (prompts, chunks of them) over the paged FP8
 // cache: attn_common.h has the mathematics.
 //
-// MFMA- and VALU-bound.  A workgroup of four waves takes 128 rows (token, head
+// MFMA- and VALU-bound: two prompts of 1777 to 2048 tokens on 1500 to 2048
+// cached, 64 heads of 128 on 8: 312 GFLOP in 337-357 us, 875-925 TFLOP/s, where
+// a large bf16 product of a library reaches 1205 and converts nothing.  Heads of
+// 256 leave one wave a SIMD (the output alone takes 128 registers), which then
+// waits out what two would overlap.
+//
+// A workgroup of four waves takes 128 rows (token, head
 // of the group) of one sequence and key head; each wave owns 32 of them on the
 // 32x32x16 MFMA and keeps its queries, logits and O in registers.  Tiles of 64
 // keys and values go through LDS by DMA, as codes, in a ring of four, one
@@ -30,6 +36,8 @@ constexpr int kStretch = 64;
 // reference moves: 32 keys level with the maximum that set it (2^kShift each)
 // stay below, and none can pass fp16's range.
 constexpr float kMostPart = 32768.0f;
+// References from here on have their logits rounded (attn_common.h).
+constexpr float kHuge = 0x1p22f;
 
 // Bits of a key row that tell apart the rows 16 lanes of a fragment read
 // ({0..7, 16..23} or {8..15, 24..31} of 32) and share a bank window.
@@ -107,6 +115,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
   float m = kNoRef, l = 0.0f;
+  bool huge = false;  // some row's reference passes kHuge
   int bref = kNoBias;
 
   // blocks and biases of a tile, scalars
@@ -306,6 +315,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
       // (a missing granule's bias is block 0's: anything)
       vscale[sub] = pow2_scale(min(0, bref - (h ? pick(bias.v, 2 * sub + 1) : pick(bias.v, 2 * sub))) + kHead<FMT>);
     }
+    // (as a branch of its own: rounding every product costs 5% of the kernel)
+    auto round_logits = [&] {
+      asm volatile("");
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sacc[sub][e] = rounded(sacc[sub][e], kscale[sub]);
+        kscale[sub] = 1.0f;
+      }
+    };
+    if (huge) round_logits();
     // Probabilities against the reference as it is; their sum tells whether a
     // logit has outgrown it (it always has in a row's first tile), and only
     // then are the maxima taken and the tile done again.
@@ -341,6 +361,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
       const float f = __builtin_amdgcn_exp2f(m - to);
       m = to;
       rescale(f, bref);
+      if (__any(fabsf(m) > kHuge && m != kNoRef)) {
+        huge = true;
+        round_logits();
+      }
       probabilities();
     }
     l += part;

@@ -9,7 +9,11 @@
 // rotate the queries.  Single tokens are bound by three loads that wait for one
 // another (lengths, block number, tokens: the last two overlap); prompts by the
 // same chain under load, since a workgroup has only 64 KB to fetch: 3.7 TB/s
-// for keys and values, 5.1 for the queries.
+// for keys and values, 5.1 for the queries; 617 MB of four prompts of 700 to
+// 4000 tokens, 32 heads of 128, in 152-154 us.
+//
+// Read.  HBM-bound: 629 MB of eight sequences of 9000 to 16384 tokens, 8 heads
+// of 128, in 116-117 us, 5.4 TB/s.
 #include <type_traits>
 
 #include "fp8_code.h"
@@ -19,7 +23,7 @@
 namespace fp8lin {
 namespace {
 
-// 8 elements at p (16-byte aligned) as fp32.
+// 4 elements at p + i as fp32.
 template <int DT>
 __device__ __forceinline__ void load4(const void* p, int64_t i, float* v) {
   if constexpr (DT == FP8_IN_FP32) {

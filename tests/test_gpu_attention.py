@@ -266,3 +266,29 @@ def test_other_stream_workspace_and_graph(fa):
         torch.cuda.synchronize()
         want, wl = fa.kv_attention(cache, batch, q, return_lse=True)
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("n,H,Hq", [(3, 2, 4), (90, 1, 2)])
+def test_one_visible_key_takes_all_whatever_its_logit(fa, n, H, Hq):
+    """A window of one: out is the token's own value, also where the only logit
+    is some -1e33.  Bound: the probability is 1, so the value's bf16 rounding and
+    the few fp32 steps are all that is left."""
+    D, bs, fmt = 64, 32, E4M3
+    rng = np.random.default_rng(n)
+    cache, tables, k, v, kb, vb = build(fa, rng, [n], H, D, bs, fmt)
+    q = torch.from_numpy(rng.standard_normal((n, Hq, D)).astype(np.float32) * 2.0 ** 110).to(torch.bfloat16).cuda()
+    say("one key", n, H, Hq)
+    out, lse = fa.kv_attention(cache, fa.KVBatch.from_lists([n], [n], tables), q, window=1, scale=1.0, return_lse=True)
+    own = ref.gather(v, vb, tables[0], n, bs, fmt, True)
+    keys = ref.gather(k, kb, tables[0], n, bs, fmt, False)
+    qd, got, lse = q.cpu().double().numpy(), out.cpu().double().numpy(), lse.cpu().double().numpy()
+    low = 0
+    for h in range(Hq):
+        g = h * H // Hq
+        want = own[:, g] if own.shape[0] == n else own[g]
+        key = keys[:, g] if keys.shape[0] == n else keys[g]
+        assert np.all(np.abs(got[:, h] - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -18)), h
+        s = (qd[:, h] * key).sum(-1)
+        assert np.all(np.abs(lse[:, h] - s) <= 2.0 ** -17 * np.abs(qd[:, h] * key).sum(-1)), h
+        low += int((s < -1e32).sum())
+    assert low > 0
