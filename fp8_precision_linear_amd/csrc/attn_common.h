@@ -25,13 +25,16 @@
 // at the top of fp16's range, so a value loses bits only 2^30 below them.
 // Probabilities are fp16 scaled by 2^kShift relative to the reference: 11 bits
 // down to 2^-22 of the largest, against bf16's 8 bits.  The reference follows
-// the row maximum lazily: it moves only when a logit exceeds it by
-// kShift - 1, so that most tiles rescale nothing and p stays below 2^15.
+// the row maximum lazily: it moves only when a logit exceeds it by more than
+// kLazy, so that most tiles rescale nothing and p, at most 2^15, stays in range.
 //
 // Where logits are huge, s * kscale is rounded before the reference is
 // subtracted, as it was for the maximum that set the reference: fused into one
 // operation its rounding error alone, 2^-24 of the logit, would drive the
-// largest p out of fp16's range from 2^26 on.
+// largest p out of fp16's range from 2^26 on.  The reference itself is a number
+// of the logits' size, in steps of 16 from 2^27 on: logits are compared with it
+// by their difference, which is exact, and it lies at most kShift below the
+// maximum (reference_for).
 #pragma once
 
 #include <type_traits>
@@ -75,7 +78,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 constexpr int kAttnTile = 64;          // keys per step
 constexpr float kShift = 8.0f;
-constexpr float kLazy = 15.0f;         // rescale when t > m + kLazy (m includes the shift)
+constexpr float kLazy = 15.0f;         // rescale when t - m > kLazy (m includes the shift)
 constexpr float kNoRef = -0x1.fffffep127f;  // reference of a row that has seen nothing
 constexpr int kNoBias = 1 << 20;       // value bias before the first block
 template <int FMT>
@@ -135,6 +138,13 @@ __device__ __forceinline__ float key_scale(float scale_log2, int kb) {
 __device__ __forceinline__ float rounded(float s, float kscale) {
 #pragma clang fp contract(off)
   return s * kscale;
+}
+
+// The reference of a row whose largest logit is top: kShift below it, or top
+// itself where rounding would take it further down.
+__device__ __forceinline__ float reference_for(float top) {
+  const float to = top - kShift;
+  return top - to > kShift ? top : to;
 }
 
 // 8 codes -> 8 bf16, exactly.

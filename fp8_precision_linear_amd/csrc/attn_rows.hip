@@ -300,9 +300,9 @@ __global__ __launch_bounds__(64 * kWaves, (kOcc<D, RB>)) void attn_rows_kernel(A
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = raw_max(top, sacc[rb][e >> 2][e & 3]);
         top = swap16_max(swap32_max(top * kscale));
-        const bool move = top > m[rb] + kLazy;
+        const bool move = top - m[rb] > kLazy;
         if (__any(move)) {
-          const float to = move ? top - kShift : m[rb];
+          const float to = move ? reference_for(top) : m[rb];
           const float f = __builtin_amdgcn_exp2f(m[rb] - to);
           m[rb] = to;
           l[rb] *= f;
