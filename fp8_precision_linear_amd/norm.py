@@ -212,7 +212,9 @@ class RMSNormFunction(torch.autograd.Function):
 
 
 class FP8NormLinearFunction(torch.autograd.Function):
-    """(y, h): h = x + residual, y = fp8_linear(norm(h) w_norm, w)."""
+    """(y, h): h = x + residual, y = fp8_linear(norm(h) w_norm, w).  What the
+    backward pass reads is held by autograd: h (an output, or the input x) and
+    w_norm may not change in between, and everything goes with the graph."""
 
     @staticmethod
     def forward(ctx, x, residual, w_norm, w, state, eps):
@@ -225,14 +227,15 @@ class FP8NormLinearFunction(torch.autograd.Function):
         n8 = n8.reshape(-1, n8.shape[-1])
         w8, bw = state.quantise("w", w.contiguous())
         y = scaled_gemm_auto(OP_FWD, n8, E4M3, bn, w8, E4M3, bw, math=state.math)
-        ctx.saved = (n8, bn, w8, bw, h, rstd)
-        ctx.state, ctx.weight, ctx.w_norm, ctx.has_residual = state, w, w_norm, residual is not None
+        ctx.save_for_backward(n8, bn, w8, bw, h, rstd, w_norm)
+        # the weight itself is only asked for its .grad; its codes are w8
+        ctx.state, ctx.weight, ctx.has_residual = state, w, residual is not None
         y = y.reshape(*x.shape[:-1], w.shape[0])
         return (y, h) if residual is not None else y
 
     @staticmethod
     def backward(ctx, dy, dh=None):
-        n8, bn, w8, bw, h, rstd = ctx.saved
+        n8, bn, w8, bw, h, rstd, w_norm = ctx.saved_tensors
         state, w = ctx.state, ctx.weight
         dy8, bdy = state.quantise("dy", dy.contiguous().reshape(-1, dy.shape[-1]))
         dn = scaled_gemm_auto(OP_DGRAD, dy8, E5M2, bdy, w8, E4M3, bw, math=state.math)
@@ -241,10 +244,9 @@ class FP8NormLinearFunction(torch.autograd.Function):
             dw = None
         else:
             dw = scaled_gemm_auto(OP_WGRAD, dy8, E5M2, bdy, n8, E4M3, bn, math=state.math)
-        dx, dwn = rmsnorm_bwd(dn.reshape(h.shape), h, ctx.w_norm.contiguous(), rstd,
+        dx, dwn = rmsnorm_bwd(dn.reshape(h.shape), h, w_norm.contiguous(), rstd,
                               dh=None if dh is None else dh.contiguous())
-        ctx.saved = ctx.weight = None
-        return dx, (dx if ctx.has_residual else None), dwn.to(ctx.w_norm.dtype), dw, None, None
+        return dx, (dx if ctx.has_residual else None), dwn.to(w_norm.dtype), dw, None, None
 
 
 class FP8NormLinear(torch.nn.Module):
