@@ -10,6 +10,7 @@ the norm and the FP8-AMAX linear layer behind it as one autograd module: the
 codes go straight into the product.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (E4M3, E5M2, OP_DGRAD, OP_FWD, OP_WGRAD, Fp8Error, _check, _dtype_code, _empty, _need, _need_kind,
                _need_place, _places, _ptr, _stream, lib, scaled_gemm_accumulate, scaled_gemm_auto)
@@ -204,6 +205,7 @@ class RMSNormFunction(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, w, rstd = ctx.saved_tensors
         dx, dw = rmsnorm_bwd(dy.contiguous(), h.contiguous(), w.contiguous(), rstd,
@@ -234,6 +236,7 @@ class FP8NormLinearFunction(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         n8, bn, w8, bw, h, rstd, w_norm = ctx.saved_tensors
         state, w = ctx.state, ctx.weight
