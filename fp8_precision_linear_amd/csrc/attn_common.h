@@ -57,7 +57,7 @@ struct AttnArgs {
   uint16_t* out;
   float* lse;
   float* part_o;    // [splits][tokens][q_heads][D], normalised
-  float* part_lse;  // [splits][tokens][q_heads], base 2
+  float2* part_sum;  // [splits][tokens][q_heads], reference and sum
   int chunk;        // tile kernel: keys per split, a multiple of kAttnTile
   int splits;       // tile kernel: most chunks of any row tile
   int row_tiles;    // most row tiles of any sequence

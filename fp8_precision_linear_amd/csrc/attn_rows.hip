@@ -391,16 +391,16 @@ __global__ __launch_bounds__(64 * kWaves, (kOcc<D, RB>)) void attn_rows_kernel(A
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] = total == 0.0f ? 0.0f : __builtin_ldexpf(sum[e] * inv, -(low + kHead<FMT>));
-        const float lse2 = total == 0.0f ? -INFINITY : top + log2f(total);
         if (whole) {
           const int64_t to = (int64_t)(s.first + row / G) * a.q_heads + head * G + row % G;
           *reinterpret_cast<uint2*>(a.out + to * D + d) =
               make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
-          if (d == 0 && a.lse) a.lse[to] = lse2 * 0.693147180559945309f;
+          if (d == 0 && a.lse)
+            a.lse[to] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
         } else {
           const int64_t to = slot * kRows + 16 * rb + r;
           *reinterpret_cast<v4f*>(a.part_o + to * D + d) = sum;
-          if (d == 0) a.part_lse[to] = lse2;
+          if (d == 0) a.part_sum[to] = make_float2(top, total);
         }
       }
     }

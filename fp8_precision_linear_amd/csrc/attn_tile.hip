@@ -425,7 +425,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   l = swap32_sum(l);
   if (!stored) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
   const int64_t cell = (int64_t)(s.first + row / G) * a.q_heads + at.head * G + row % G;
   const int64_t slot = (int64_t)at.split * a.batch.tokens * a.q_heads + cell;
   // result v of a lane is dimension 32 d + 8 (v / 4) + 4 h + v % 4
@@ -444,8 +443,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
         *reinterpret_cast<v4f*>(a.part_o + slot * D + at_d) = v4f{v[0], v[1], v[2], v[3]};
     }
   if (h == 0) {
-    if (span.chunks > 1) a.part_lse[slot] = lse2;
-    else if (a.lse) a.lse[cell] = lse2 * 0.693147180559945309f;
+    if (span.chunks > 1) a.part_sum[slot] = make_float2(m, l);
+    else if (a.lse) a.lse[cell] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
   }
 }
 

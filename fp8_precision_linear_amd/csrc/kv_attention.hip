@@ -64,10 +64,13 @@ int64_t part_rows(const AttnPlan& p, const fp8_kv_batch_t& b, int q_heads, int64
 }
 
 // The join of a (new token, query head) whose keys were split into parts
-// (chunks, or shares): out = sum_c 2^(lse_c - L) out_c, L = log2 sum_c 2^lse_c.
+// (chunks, or shares): out = sum_c w_c out_c / sum_c w_c, w_c = l_c 2^(m_c - M),
+// with M the largest reference of a part that sees keys (one that sees none has
+// l = 0 and adds nothing).  The parts' references and sums stay apart until here:
+// added to a large reference a sum would be rounded away.  out is kept divided by
+// the weights' sum throughout, since a value times a sum could pass fp32's range.
 // A row of D / 4 lanes joins `few` parts alone, several rows a workgroup; many
-// parts are dealt to all rows of a workgroup, which meet in LDS in order.  A part
-// without visible keys has lse = -inf and adds nothing.
+// parts are dealt to all rows of a workgroup, which meet in LDS in order.
 constexpr int kJoin = 256;
 constexpr int kFewParts = 16;
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows, bool few) {
@@ -85,7 +88,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
   const KVSeq s = kv_seq(a.batch, a.cache.block_size, i);
   if (nth >= s.n) return;
   const int64_t at = (int64_t)(s.first + nth) * a.q_heads + head;
-  // part c's row of part_o and part_lse: first for c = 0, then from `base` by step
+  // part c's row of part_o and part_sum: first for c = 0, then from `base` by step
   int64_t first = at, base = at, step = (int64_t)a.batch.tokens * a.q_heads;
   int chunks;
   if (a.shares) {
@@ -103,28 +106,33 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
   float top = -INFINITY, total = 0.0f;
   v4f sum{0, 0, 0, 0};
   for (int c0 = share; c0 < chunks; c0 += kAhead * shares) {
-    float lse[kAhead];
+    float2 ml[kAhead];
     v4f v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int c = c0 + u * shares;
-      const int64_t p = c == 0 ? first : base + (c < chunks ? c : c0) * step;
-      lse[u] = c < chunks ? a.part_lse[p] : -INFINITY;
-      v[u] = *reinterpret_cast<const v4f*>(a.part_o + (c0 == 0 && c >= chunks ? first : p) * D + d);
+      const int real = c < chunks ? c : c0;
+      const int64_t p = real == 0 ? first : base + real * step;
+      ml[u] = a.part_sum[p];
+      if (c >= chunks) ml[u].y = 0.0f;
+      v[u] = *reinterpret_cast<const v4f*>(a.part_o + p * D + d);
     }
     float up = top;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) up = fmaxf(up, lse[u]);
-    const float f0 = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - up);
-    sum *= f0;
-    total *= f0;
-    top = up;
+    for (int u = 0; u < kAhead; ++u) up = ml[u].y == 0.0f ? up : fmaxf(up, ml[u].x);
+    const float before = total == 0.0f ? 0.0f : total * __builtin_amdgcn_exp2f(top - up);
+    float w[kAhead];
+    top = up, total = before;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const float f = lse[u] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lse[u] - top);
-      total += f;
-      if (f != 0.0f) sum += v[u] * f;
+      w[u] = ml[u].y == 0.0f ? 0.0f : ml[u].y * __builtin_amdgcn_exp2f(ml[u].x - top);
+      total += w[u];
     }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    sum *= before * inv;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (w[u] != 0.0f) sum += v[u] * (w[u] * inv);
   }
   if (!few) {
     so[t] = sum;
@@ -132,19 +140,23 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
     st[t] = top;
     __syncthreads();
     if (t >= lanes) return;
-    for (int k = 0; k < shares; ++k) top = fmaxf(top, st[k * lanes + t]);
+    float most = total;  // what the weights may add up to
+    for (int k = 1; k < shares; ++k) {
+      top = fmaxf(top, st[k * lanes + t]);
+      most += ss[k * lanes + t];
+    }
+    const float down = most == 0.0f ? 0.0f : 1.0f / most;
     sum = v4f{0, 0, 0, 0};
     total = 0.0f;
     for (int k = 0; k < shares; ++k) {
       const float part = st[k * lanes + t];
-      const float f = part == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(part - top);
-      if (f != 0.0f) sum += so[k * lanes + t] * f;
-      total += ss[k * lanes + t] * f;
+      const float f = part == -INFINITY ? 0.0f : ss[k * lanes + t] * __builtin_amdgcn_exp2f(part - top);
+      if (f != 0.0f) sum += so[k * lanes + t] * (f * down);
+      total += f;
     }
+    sum *= total == 0.0f ? 0.0f : most / total;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  *reinterpret_cast<uint2*>(a.out + at * D + d) =
-      make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+  *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
   if (d == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
 }
 
@@ -159,7 +171,7 @@ int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch
   if (p.shares == 0 && p.most_splits == 1) return 0;
   // the join's workgroups
   if ((int64_t)b.batch * b.max_new > 0x7FFFFFFF / q_heads) return FP8_ERR_SIZE;
-  return part_rows(p, b, q_heads, p.most_splits) * (c.head_dim + 1) * 4 + (p.shares ? p.base * 8 : 0);
+  return part_rows(p, b, q_heads, p.most_splits) * (c.head_dim + 2) * 4 + (p.shares ? p.base * 8 : 0);
 }
 
 hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stream) {
@@ -180,8 +192,8 @@ hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stre
   a.lse = pr.lse;
   a.part_o = static_cast<float*>(ws);
   const int64_t parts = part_rows(p, pr.batch, pr.q_heads, p.splits);
-  a.part_lse = a.part_o + parts * pr.cache.head_dim;
-  a.segments = reinterpret_cast<int2*>(a.part_lse + parts);
+  a.part_sum = reinterpret_cast<float2*>(a.part_o + parts * pr.cache.head_dim);
+  a.segments = reinterpret_cast<int2*>(a.part_sum + parts);
   a.shares = p.shares;
   a.chunk = p.chunk;
   a.splits = p.splits;
