@@ -66,7 +66,7 @@ int64_t part_rows(const AttnPlan& p, const fp8_kv_batch_t& b, int q_heads, int64
 // The join of a (new token, query head) whose keys were split into parts
 // (chunks, or shares): out = sum_c w_c out_c / sum_c w_c, w_c = l_c 2^(m_c - M),
 // with M the largest reference of a part that sees keys (one that sees none has
-// l = 0 and adds nothing).  The parts' references and sums stay apart until here:
+// l = 0 and out = 0; a weight that underflows still carries a NaN on).  The parts' references and sums stay apart until here:
 // added to a large reference a sum would be rounded away.  out is kept divided by
 // the weights' sum throughout, since a value times a sum could pass fp32's range.
 // A row of D / 4 lanes joins `few` parts alone, several rows a workgroup; many
@@ -131,8 +131,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     sum *= before * inv;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (w[u] != 0.0f) sum += v[u] * (w[u] * inv);
+    for (int u = 0; u < kAhead; ++u) sum += v[u] * (w[u] * inv);
   }
   if (!few) {
     so[t] = sum;
@@ -151,7 +150,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
     for (int k = 0; k < shares; ++k) {
       const float part = st[k * lanes + t];
       const float f = part == -INFINITY ? 0.0f : ss[k * lanes + t] * __builtin_amdgcn_exp2f(part - top);
-      if (f != 0.0f) sum += so[k * lanes + t] * (f * down);
+      sum += so[k * lanes + t] * (f * down);
       total += f;
     }
     sum *= total == 0.0f ? 0.0f : most / total;
