@@ -216,6 +216,30 @@ __device__ __forceinline__ v8h ones_f16(uint32_t m0, uint32_t m1) {
 // compiler cannot prove quiet); a NaN loses to any number.
 __device__ __forceinline__ float raw_max(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
 
+// ln sum_j exp(s_j) of a row: m + log2(l) in base e.  In 64 bits until the last
+// rounding: m carries kShift, which the logarithm takes off again (three keys with
+// logits of zero: ln 3 = (log2 768 - 8) ln 2 came out 4 units in the last place
+// off in fp32).  l = f 2^e with f in [2/3, 4/3): ln l = e ln 2 + 2 atanh(s),
+// s = (f - 1) / (f + 1), |s| <= 1/5, by the series up to s^13 / 13 (the rest is
+// below 2^-37).  The library's logarithm in its place cost 128 decoded sequences
+// of 2000 tokens 92 us instead of 90.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  if (!(l > 0.0f && l < INFINITY)) return l == 0.0f ? -INFINITY : l + m;  // NaN
+  const int e = __builtin_amdgcn_frexp_expf(l * 0.75f);
+  const double f = (double)__builtin_ldexpf(l, -e), up = f + 1.0;
+  double r = (double)__builtin_amdgcn_rcpf((float)up);
+  r = r * (2.0 - up * r);
+  const double s = (f - 1.0) * r, s2 = s * s;
+  double p = 2.0 / 13;
+  p = fma(p, s2, 2.0 / 11);
+  p = fma(p, s2, 2.0 / 9);
+  p = fma(p, s2, 2.0 / 7);
+  p = fma(p, s2, 2.0 / 5);
+  p = fma(p, s2, 2.0 / 3);
+  p = fma(p, s2, 2.0);
+  return (float)fma((double)m + e, 0.693147180559945309417, p * s);
+}
+
 // Reductions over the lanes that share a query row: l ^ 32, and l ^ 16.
 __device__ __forceinline__ float swap32_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -395,8 +395,7 @@ __global__ __launch_bounds__(64 * kWaves, (kOcc<D, RB>)) void attn_rows_kernel(A
           const int64_t to = (int64_t)(s.first + row / G) * a.q_heads + head * G + row % G;
           *reinterpret_cast<uint2*>(a.out + to * D + d) =
               make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
-          if (d == 0 && a.lse)
-            a.lse[to] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
+          if (d == 0 && a.lse) a.lse[to] = row_lse(top, total);
         } else {
           const int64_t to = slot * kRows + 16 * rb + r;
           *reinterpret_cast<v4f*>(a.part_o + to * D + d) = sum;

@@ -444,7 +444,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
     }
   if (h == 0) {
     if (span.chunks > 1) a.part_sum[slot] = make_float2(m, l);
-    else if (a.lse) a.lse[cell] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+    else if (a.lse) a.lse[cell] = row_lse(m, l);
   }
 }
 

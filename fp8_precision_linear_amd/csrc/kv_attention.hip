@@ -156,7 +156,7 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
     sum *= total == 0.0f ? 0.0f : most / total;
   }
   *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
-  if (d == 0 && a.lse) a.lse[at] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.693147180559945309f;
+  if (d == 0 && a.lse) a.lse[at] = row_lse(top, total);
 }
 
 }  // namespace
