@@ -201,6 +201,15 @@ __device__ __forceinline__ uint32_t bad_bytes(uint32_t w) {
   return top * 0xFFu;
 }
 
+// A finite sum of weighted values, or NaN.  An infinite sum means an infinity
+// code (no sum of finite codes comes near fp32's range); its sign and whether it
+// met a weight of zero would depend on where the keys were split and masked.
+template <int FMT>
+__device__ __forceinline__ float nan_if_infinite(float o) {
+  if constexpr (FMT == FP8_E5M2) return o + (o - o);
+  return o;
+}
+
 // 1.0 where the byte is set, as fp16.
 __device__ __forceinline__ v8h ones_f16(uint32_t m0, uint32_t m1) {
   v8h r;

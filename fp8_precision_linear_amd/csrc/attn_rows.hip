@@ -390,7 +390,8 @@ __global__ __launch_bounds__(64 * kWaves, (kOcc<D, RB>)) void attn_rows_kernel(A
         }
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = total == 0.0f ? 0.0f : __builtin_ldexpf(sum[e] * inv, -(low + kHead<FMT>));
+        for (int e = 0; e < 4; ++e)
+          sum[e] = total == 0.0f ? 0.0f : __builtin_ldexpf(nan_if_infinite<FMT>(sum[e]) * inv, -(low + kHead<FMT>));
         if (whole) {
           const int64_t to = (int64_t)(s.first + row / G) * a.q_heads + head * G + row % G;
           *reinterpret_cast<uint2*>(a.out + to * D + d) =

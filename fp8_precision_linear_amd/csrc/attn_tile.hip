@@ -435,7 +435,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        v[e] = l == 0.0f ? 0.0f : __builtin_ldexpf(o[d][4 * u + e] * inv, -(bref + kHead<FMT>));
+        v[e] = l == 0.0f ? 0.0f : __builtin_ldexpf(nan_if_infinite<FMT>(o[d][4 * u + e]) * inv, -(bref + kHead<FMT>));
       const int at_d = 32 * d + 8 * u + 4 * h;
       if (span.chunks == 1)
         *reinterpret_cast<uint2*>(a.out + cell * D + at_d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));

@@ -202,7 +202,9 @@ int fp8_kv_read(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, fp8_dt
  *   out = sum_j softmax(s)_j v_j      lse = ln sum_j exp(s_j)
  * Visible: j < lens[i]; causal != 0: j <= p; window > 0: j > p - window
  * (needs causal).  A query that sees nothing gets out = 0 and lse = -inf;
- * what lies in invisible slots -- NaN codes among it -- has no influence.
+ * what lies in invisible slots -- NaN codes among it -- has no influence.  A
+ * visible value whose code is NaN or (E5M2) an infinity makes that dimension of
+ * the output NaN, whatever its weight; NaN and +infinity as a logit, every one.
  *   q     device, tokens rows of q_heads x head_dim bf16 words, q_stride
  *         elements apart (rows multiples of 16 bytes)
  *   out   device, tokens x q_heads x head_dim bf16 words, written
