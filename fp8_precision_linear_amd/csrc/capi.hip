@@ -134,7 +134,16 @@ int rows_checks(const void* p, int64_t stride, int64_t heads, int64_t head_dim, 
   return FP8_OK;
 }
 
-bool kv_empty(const fp8_kv_batch_t* b) { return b->batch == 0 || b->tokens == 0 || b->max_new == 0; }
+// The batch with max_new held to what tokens and max_len allow: grids, splits
+// and workspaces go by it, and a caller's bound may be loose.
+fp8_kv_batch_t bounded(const fp8_kv_batch_t* b) {
+  fp8_kv_batch_t r = *b;
+  if (r.max_new > r.tokens) r.max_new = r.tokens;
+  if (r.max_new > r.max_len) r.max_new = r.max_len;
+  return r;
+}
+
+bool kv_empty(const fp8_kv_batch_t& b) { return b.batch == 0 || b.tokens == 0 || b.max_new == 0; }
 
 }  // namespace
 
@@ -602,7 +611,8 @@ int fp8_kv_append(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, cons
   if (q && q_heads < 1) return FP8_ERR_SIZE;
   if (!cos != !sin) return FP8_ERR_NULL;
   if (cos && rope_rows < batch->max_len) return FP8_ERR_SIZE;
-  if (kv_empty(batch)) return FP8_OK;
+  const fp8_kv_batch_t b = bounded(batch);
+  if (kv_empty(b)) return FP8_OK;
   const int bytes = dtype == FP8_IN_FP32 ? 4 : 2;
   if ((st = rows_checks(k, k_stride, cache->heads, cache->head_dim, bytes)) != FP8_OK) return st;
   if ((st = rows_checks(v, v_stride, cache->heads, cache->head_dim, bytes)) != FP8_OK) return st;
@@ -612,9 +622,9 @@ int fp8_kv_append(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, cons
     if (misaligned(q_out)) return FP8_ERR_ALIGN;
   }
   if (misaligned(cos) || misaligned(sin)) return FP8_ERR_ALIGN;
-  if (fp8lin::kv_append_groups(*cache, *batch, q != nullptr) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  if (fp8lin::kv_append_groups(*cache, b, q != nullptr) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
   if ((st = device_ok()) != FP8_OK) return st;
-  return hip_status(fp8lin::launch_kv_append(*cache, *batch, k, k_stride, v, v_stride, dtype, q, q_stride, q_heads,
+  return hip_status(fp8lin::launch_kv_append(*cache, b, k, k_stride, v, v_stride, dtype, q, q_stride, q_heads,
                                              q_out, cos, sin, rope_rows, rope_pairs, (hipStream_t)stream));
 }
 
@@ -624,18 +634,20 @@ int fp8_kv_read(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, fp8_dt
   if (st != FP8_OK) return st;
   if (bad_dtype(out_dtype)) return FP8_ERR_DTYPE;
   if (misaligned(k_out) || misaligned(v_out)) return FP8_ERR_ALIGN;
-  if (kv_empty(batch) || (!k_out && !v_out)) return FP8_OK;
-  if (fp8lin::kv_append_groups(*cache, *batch, false) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  const fp8_kv_batch_t b = bounded(batch);
+  if (kv_empty(b) || (!k_out && !v_out)) return FP8_OK;
+  if (fp8lin::kv_append_groups(*cache, b, false) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
   if ((st = device_ok()) != FP8_OK) return st;
-  return hip_status(fp8lin::launch_kv_read(*cache, *batch, out_dtype, k_out, v_out, (hipStream_t)stream));
+  return hip_status(fp8lin::launch_kv_read(*cache, b, out_dtype, k_out, v_out, (hipStream_t)stream));
 }
 
 int64_t fp8_kv_attention_workspace_bytes(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, int32_t q_heads) {
   const int st = kv_checks(cache, batch);
   if (st != FP8_OK) return st;
   if (q_heads < 1 || q_heads % cache->heads != 0) return FP8_ERR_SIZE;
-  if (kv_empty(batch)) return 0;
-  return fp8lin::kv_attention_workspace_bytes(*cache, *batch, q_heads);
+  const fp8_kv_batch_t b = bounded(batch);
+  if (kv_empty(b)) return 0;
+  return fp8lin::kv_attention_workspace_bytes(*cache, b, q_heads);
 }
 
 int fp8_kv_attention(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, const uint16_t* q, int64_t q_stride,
@@ -644,14 +656,15 @@ int fp8_kv_attention(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, c
   const int64_t need = fp8_kv_attention_workspace_bytes(cache, batch, q_heads);
   if (need < 0) return (int)need;
   if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
-  if (kv_empty(batch)) return FP8_OK;
+  const fp8_kv_batch_t b = bounded(batch);
+  if (kv_empty(b)) return FP8_OK;
   int st = rows_checks(q, q_stride, q_heads, cache->head_dim, 2);
   if (st != FP8_OK) return st;
   if (!out || (need > 0 && !ws)) return FP8_ERR_NULL;
   if (misaligned(out) || misaligned_word(lse) || misaligned(ws)) return FP8_ERR_ALIGN;
   if (ws_bytes < need) return FP8_ERR_SIZE;
   if ((st = device_ok()) != FP8_OK) return st;
-  const fp8lin::AttnProblem p{*cache, *batch, q, q_stride, q_heads, scale, causal, window, out, lse};
+  const fp8lin::AttnProblem p{*cache, b, q, q_stride, q_heads, scale, causal, window, out, lse};
   return hip_status(fp8lin::launch_kv_attention(p, ws, (hipStream_t)stream));
 }
 

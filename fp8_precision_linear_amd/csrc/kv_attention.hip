@@ -162,6 +162,8 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
 }  // namespace
 
 int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads) {
+  // the kernels number a key head's rows in 32 bits, up to the end of a tile
+  if ((int64_t)b.max_new * (q_heads / c.heads) > 0x7FFFFFFF - kAttnTileRows) return FP8_ERR_SIZE;
   // the window may shorten the span and so raise the split, up to most_splits
   const AttnPlan p = plan_of(c, b, q_heads, 0);
   if (p.base > 0x7FFFFFFF / p.most_splits) return FP8_ERR_SIZE;

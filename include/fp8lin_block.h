@@ -133,7 +133,8 @@ typedef struct {
  *   lens         device, batch int32
  *   block_table  device, batch x table_width int32
  *   tokens       rows of the packed tensors
- *   max_new      at least every n_i;  max_len  at least every lens[i], at most
+ *   max_new      at least every n_i (a looser bound costs nothing past `tokens`
+ *                and max_len);  max_len  at least every lens[i], at most
  *                table_width * block_size and 2^30 (FP8_ERR_SIZE otherwise)
  * The device arrays are read by the kernels only.  They stay within the
  * buffers whatever the arrays hold: a table entry outside 0 .. num_blocks - 1
@@ -217,7 +218,8 @@ int fp8_kv_read(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, fp8_dt
  * scales relative to the smallest bias met so far in the sequence: a value
  * keeps at least 11 bits unless it is 2^30 below the largest); probabilities
  * are fp16 relative to a running maximum; sums, maxima and the join are fp32.
- * q_heads: a positive multiple of heads (FP8_ERR_SIZE otherwise).
+ * q_heads: a positive multiple of heads (FP8_ERR_SIZE otherwise, and where
+ * max_new * q_heads / heads passes 2^31 - 129).
  */
 int64_t fp8_kv_attention_workspace_bytes(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch,
                                          int32_t q_heads);
