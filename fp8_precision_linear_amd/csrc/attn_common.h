@@ -61,6 +61,7 @@ struct AttnArgs {
   int chunk;        // tile kernel: keys per split, a multiple of kAttnTile
   int splits;       // tile kernel: most chunks of any row tile
   int row_tiles;    // most row tiles of any sequence
+  uint32_t first;   // this launch's first workgroup
   int shares;       // rows kernel: workgroups that share all keys evenly, or 0
   int2* segments;   // rows kernel, shares > 0: [batch][row_tiles][heads], the
                     // first and last workgroup of a segment
@@ -76,6 +77,8 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
+constexpr int kAttnWaves = 4;          // of a workgroup
+constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnTile = 64;          // keys per step
 constexpr float kShift = 8.0f;
 constexpr float kLazy = 15.0f;         // rescale when t - m > kLazy (m includes the shift)
@@ -92,7 +95,7 @@ struct AttnPlace {
 };
 __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a) {
   AttnPlace p;
-  uint32_t x = blockIdx.x;
+  uint32_t x = a.first + blockIdx.x;
   p.head = x % a.cache.heads;
   x /= a.cache.heads;
   p.split = x % a.splits;

@@ -20,7 +20,7 @@
 namespace fp8lin {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kAttnWaves;
 
 // Waves of one SIMD (registers allow that many).
 template <int D, int RB>

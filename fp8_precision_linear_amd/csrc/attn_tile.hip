@@ -24,7 +24,7 @@
 namespace fp8lin {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kAttnWaves;
 // Tiles in LDS: three on their way while one is consumed.  (With one on its way
 // short prompts, whose workgroups have a CU to themselves, waited for every
 // tile: 740 tokens of 40 heads took 102 us.)

@@ -82,6 +82,17 @@ hipError_t launch_norm_bwd(const void* dy, int dy_dtype, const void* h, int h_dt
                            const float* rstd, const void* dh, int64_t rows, int64_t d, void* dx, float* dw,
                            uint32_t* amax, float* ws, hipStream_t stream);
 
+// Launches of `groups` workgroups of `threads` lanes that one launch may not
+// hold: a grid counts its lanes in 32 bits, and one that passes them is cut off
+// without an error.  launch(first, count) for stretches of them in turn; a
+// kernel adds `first` to its workgroup number.
+template <typename F>
+void in_stretches(int64_t groups, int threads, F&& launch) {
+  const int64_t most = 0xFFFFFFFF / threads;
+  for (int64_t first = 0; first < groups; first += most)
+    launch((uint32_t)first, (uint32_t)(groups - first < most ? groups - first : most));
+}
+
 // The paged FP8 cache (kv_cache.hip).  Workgroups an append or read of the
 // batch launches, or 2^31 for too many.
 int64_t kv_append_groups(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, bool queries);

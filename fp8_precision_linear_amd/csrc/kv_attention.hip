@@ -199,9 +199,12 @@ hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stre
   a.chunk = p.chunk;
   a.splits = p.splits;
   a.row_tiles = p.row_tiles;
-  const uint32_t groups = p.shares ? (uint32_t)p.shares : (uint32_t)(p.base * p.splits);
-  hipError_t e = p.few ? launch_attn_rows(a, p.row_blocks, groups, stream)
-                       : launch_attn_tile(a, groups, stream);
+  hipError_t e = hipSuccess;
+  in_stretches(p.shares ? p.shares : p.base * p.splits, kAttnThreads, [&](uint32_t first, uint32_t count) {
+    if (e != hipSuccess) return;
+    a.first = first;
+    e = p.few ? launch_attn_rows(a, p.row_blocks, count, stream) : launch_attn_tile(a, count, stream);
+  });
   if (e != hipSuccess || (p.splits == 1 && p.shares == 0)) return e;
   const int64_t joins = (int64_t)pr.batch.batch * pr.batch.max_new * pr.q_heads;
   // shares: a segment's parts are about its tiles over a share's

@@ -132,6 +132,7 @@ struct AppendArgs {
   Rope rope;
   int blocks_per_seq;   // most blocks a sequence's new tokens touch
   int64_t kv_groups;    // workgroups of the keys and values; the others are the queries'
+  uint32_t first;       // this launch's first workgroup
   int q_tokens;         // tokens of one of the queries' workgroups
   int q_groups;         // of them per sequence
 };
@@ -146,8 +147,9 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
   const int nt = blockDim.x, t = threadIdx.x;
   const int BS = a.cache.block_size, H = a.cache.heads;
 
-  if ((int64_t)blockIdx.x >= a.kv_groups) {  // some tokens' queries
-    const uint32_t g = (uint32_t)((int64_t)blockIdx.x - a.kv_groups);
+  uint32_t g = a.first + blockIdx.x;
+  if ((int64_t)g >= a.kv_groups) {  // some tokens' queries
+    g -= (uint32_t)a.kv_groups;
     const int i = g / a.q_groups, nth = (g % a.q_groups) * a.q_tokens;
     const KVSeq s = kv_seq_uniform(a.batch, BS, i);
     const int count = min(a.q_tokens, s.n - nth);
@@ -182,7 +184,6 @@ __global__ __launch_bounds__(1024) void kv_append_kernel(AppendArgs a) {
     return;
   }
 
-  uint32_t g = blockIdx.x;
   const int head = g % H;
   g /= H;
   const int nth_block = g % a.blocks_per_seq, i = g / a.blocks_per_seq;
@@ -331,6 +332,7 @@ struct ReadArgs {
   void* k;
   void* v;
   int blocks_per_seq;
+  uint32_t first;  // this launch's first workgroup
 };
 
 // 8 codes (two words) times 2^-b -> out_dtype at o, each rounded once: by the
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
   extern __shared__ uint8_t lds[];
   const int t = threadIdx.x;
   const int BS = a.cache.block_size, H = a.cache.heads;
-  uint32_t g = blockIdx.x;
+  uint32_t g = a.first + blockIdx.x;
   const bool values = g & 1;
   g >>= 1;
   const int head = g % H;
@@ -492,8 +494,11 @@ hipError_t launch_kv_append(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch
   if (q && threads < 256) threads = 256;
   using std::integral_constant;
   auto run = [&](auto dt, auto fmt, auto d, auto rope) {
-    hipLaunchKernelGGL((kv_append_kernel<dt.value, fmt.value, d.value, rope.value>), dim3((uint32_t)groups),
-                       dim3(threads), lds_bytes(c), stream, a);
+    in_stretches(groups, threads, [&](uint32_t first, uint32_t count) {
+      a.first = first;
+      hipLaunchKernelGGL((kv_append_kernel<dt.value, fmt.value, d.value, rope.value>), dim3(count), dim3(threads),
+                         lds_bytes(c), stream, a);
+    });
   };
   auto with_rope = [&](auto dt, auto fmt, auto d) {
     if (!cos) run(dt, fmt, d, integral_constant<int, kRopeNone>{});
@@ -516,12 +521,15 @@ hipError_t launch_kv_append(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch
 
 hipError_t launch_kv_read(const fp8_kv_cache_t& c, const fp8_kv_batch_t& batch, int out_dtype, void* k, void* v,
                           hipStream_t stream) {
-  ReadArgs a{c, batch, k, v, (batch.max_new - 1) / c.block_size + 2};
+  ReadArgs a{c, batch, k, v, (batch.max_new - 1) / c.block_size + 2, 0};
   const int64_t groups = (int64_t)batch.batch * a.blocks_per_seq * c.heads * 2;
   using std::integral_constant;
   auto run = [&](auto dt, auto fmt, auto d) {
-    hipLaunchKernelGGL((kv_read_kernel<dt.value, fmt.value, d.value>), dim3((uint32_t)groups), dim3(256), lds_bytes(c),
-                       stream, a);
+    in_stretches(groups, 256, [&](uint32_t first, uint32_t count) {
+      a.first = first;
+      hipLaunchKernelGGL((kv_read_kernel<dt.value, fmt.value, d.value>), dim3(count), dim3(256), lds_bytes(c), stream,
+                         a);
+    });
   };
   auto with_dim = [&](auto dt, auto fmt) {
     if (c.head_dim == 64) run(dt, fmt, integral_constant<int, 64>{});
