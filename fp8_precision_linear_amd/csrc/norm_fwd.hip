@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256) void norm_cast_kernel(const void* h, const flo
   const int t = threadIdx.x;
   const int j = ((int)(blockIdx.x % col_blocks) * 256 + t) * 4;
   const int64_t group = blockIdx.x / col_blocks;
-  const bool live = j < d;
+  const bool live = j < d && rows > 0;  // without rows w need not be there
   float ww[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) ww[e] = 0.0f;
