@@ -242,6 +242,7 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, l
     qs = _head_rows(q, "q", T, heads, D, dev, torch.bfloat16)
     if window < 0 or (window and not causal):
         raise ValueError("a window is positive and needs causal")
+    window = min(int(window), 0x7FFFFFFF)   # past every position, and what the library's 32 bits hold
     if out is not None:
         _need_kind(out, "out", torch.bfloat16, shape=(T, heads, D))
         _need_place(out, "out", dev)
@@ -259,6 +260,6 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, l
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("fp8_kv_attention",
            lib.fp8_kv_attention(cache._ref, batch._ref, q.data_ptr(), qs, heads,
-                                float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window), out.data_ptr(),
+                                float(D ** -0.5 if scale is None else scale), int(bool(causal)), window, out.data_ptr(),
                                 _opt(lse), _opt(workspace), nbytes, _stream(stream)))
     return (out, lse) if return_lse else out
