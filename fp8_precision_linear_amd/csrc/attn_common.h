@@ -144,11 +144,9 @@ __device__ __forceinline__ float rounded(float s, float kscale) {
 }
 
 // The reference of a row whose largest logit is top: kShift below it, or top
-// itself where rounding would take it further down.
-__device__ __forceinline__ float reference_for(float top) {
-  const float to = top - kShift;
-  return top - to > kShift ? top : to;
-}
+// itself from 2^24 on, where rounding the difference could take it further down
+// (and logits lie 2 and more apart).
+__device__ __forceinline__ float reference_for(float top) { return fabsf(top) < 0x1p24f ? top - kShift : top; }
 
 // 8 codes -> 8 bf16, exactly.
 template <int FMT>

@@ -357,7 +357,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
         top = fmaxf(top, s * kscale[sub]);
       }
       top = swap32_max(top);
-      const float to = fmaxf(reference_for(top), m);
+      const float up = reference_for(top), to = up > m ? up : m;
       const float f = __builtin_amdgcn_exp2f(m - to);
       m = to;
       rescale(f, bref);
