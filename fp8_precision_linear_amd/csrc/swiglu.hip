@@ -87,15 +87,16 @@ __device__ __forceinline__ void fold_amax(uint32_t m, uint32_t* amax) {
   }
 }
 
-// Block b covers units [part * kUnitsPerBlock, (part + 1) * kUnitsPerBlock) of
+// Block b = first + blockIdx.x covers units [part * kUnitsPerBlock, (part + 1) * kUnitsPerBlock) of
 // row b / bpr; a unit is V consecutive columns (V = 4 when f % 4 == 0).
 template <int V>
 __global__ __launch_bounds__(kThreads) void swiglu_fwd_kernel(const float* __restrict__ h,
                                                               int64_t f, int64_t upr, int bpr,
                                                               uint16_t* __restrict__ a,
-                                                              uint32_t* __restrict__ amax) {
-  const int64_t row = blockIdx.x / bpr;
-  const int64_t j0 = (int64_t)(blockIdx.x - row * bpr) * kUnitsPerBlock + threadIdx.x;
+                                                              uint32_t* __restrict__ amax, uint32_t first) {
+  const uint32_t block = first + blockIdx.x;
+  const int64_t row = block / bpr;
+  const int64_t j0 = (int64_t)(block - row * bpr) * kUnitsPerBlock + threadIdx.x;
   const float* hg = h + row * 2 * f;
   const float* hu = hg + f;
   uint16_t* ar = a + row * f;
@@ -132,9 +133,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(const float* __res
                                                               const float* __restrict__ da,
                                                               int64_t f, int64_t upr, int bpr,
                                                               uint16_t* __restrict__ dh,
-                                                              uint32_t* __restrict__ amax) {
-  const int64_t row = blockIdx.x / bpr;
-  const int64_t j0 = (int64_t)(blockIdx.x - row * bpr) * kUnitsPerBlock + threadIdx.x;
+                                                              uint32_t* __restrict__ amax, uint32_t first) {
+  const uint32_t block = first + blockIdx.x;
+  const int64_t row = block / bpr;
+  const int64_t j0 = (int64_t)(block - row * bpr) * kUnitsPerBlock + threadIdx.x;
   const float* hg = h + row * 2 * f;
   const float* hu = hg + f;
   const float* dar = da + row * f;
@@ -199,12 +201,12 @@ hipError_t launch_swiglu_fwd(const float* h, int64_t rows, int64_t f, uint16_t* 
   if (amax) hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, stream, amax);
   if (rows > 0 && f > 0) {
     const Grid g = grid_of(rows, f);
-    if (g.vec)
-      hipLaunchKernelGGL(swiglu_fwd_kernel<4>, dim3((uint32_t)g.blocks), dim3(kThreads), 0, stream,
-                         h, f, g.upr, g.bpr, a, amax);
-    else
-      hipLaunchKernelGGL(swiglu_fwd_kernel<1>, dim3((uint32_t)g.blocks), dim3(kThreads), 0, stream,
-                         h, f, g.upr, g.bpr, a, amax);
+    in_stretches(g.blocks, kThreads, [&](uint32_t first, uint32_t count) {
+      if (g.vec)
+        hipLaunchKernelGGL(swiglu_fwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax, first);
+      else
+        hipLaunchKernelGGL(swiglu_fwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax, first);
+    });
   }
   return hipGetLastError();
 }
@@ -214,12 +216,12 @@ hipError_t launch_swiglu_bwd(const float* h, const float* da, int64_t rows, int6
   if (amax) hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, stream, amax);
   if (rows > 0 && f > 0) {
     const Grid g = grid_of(rows, f);
-    if (g.vec)
-      hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3((uint32_t)g.blocks), dim3(kThreads), 0, stream,
-                         h, da, f, g.upr, g.bpr, dh, amax);
-    else
-      hipLaunchKernelGGL(swiglu_bwd_kernel<1>, dim3((uint32_t)g.blocks), dim3(kThreads), 0, stream,
-                         h, da, f, g.upr, g.bpr, dh, amax);
+    in_stretches(g.blocks, kThreads, [&](uint32_t first, uint32_t count) {
+      if (g.vec)
+        hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax, first);
+      else
+        hipLaunchKernelGGL(swiglu_bwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax, first);
+    });
   }
   return hipGetLastError();
 }
