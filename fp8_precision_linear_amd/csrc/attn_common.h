@@ -22,7 +22,7 @@
 // sums of the 16-bit MFMA are fp32.  Values widen to fp16, scaled by
 // 2^(bref - vb + kHead) in the conversion itself, where bref is the smallest
 // value bias met so far (O is rescaled when it drops): the largest values sit
-// at the top of fp16's range, so a value loses bits only 2^30 below them.
+// at the top of fp16's range, so a value loses only what lies 2^40 below them.
 // Probabilities are fp16 scaled by 2^kShift relative to the reference: 11 bits
 // down to 2^-22 of the largest, against bf16's 8 bits.  The reference follows
 // the row maximum lazily: it moves only when a logit exceeds it by more than

@@ -26,8 +26,11 @@ struct AttnPlan {
 // workgroup a CU saves (two prompts of up to 1303 tokens, 32 heads of 64 on 8:
 // two chunks 42 us, whole 27).
 constexpr int64_t kWantTiles = 512, kCUs = 256, kLeastTiles = 4, kLeastTilesFull = 32;
-// Rows kernel: even shares where a segment may hold more tiles than this (a
-// join costs about as long as the tiles it takes off the longest workgroup).
+// Rows kernel: even shares where a segment may hold more tiles than this.  The
+// join costs some 8 us, and a segment's tiles 2 to 3 us for every four: one
+// sequence of 1000 tokens, 8 heads of 128, whole 13.6 us and in shares 12.5, of
+// 1500 17.2 and 12.7, of 2500 23.7 and 12.8; 32 sequences of 500 to 1000 tokens
+// 17.2 and 23.1, of 750 to 1500 21.8 and 25.5, of 1250 to 2500 29.6 and 32.2.
 constexpr int64_t kWholeTiles = 24;
 
 AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int window) {

@@ -139,7 +139,8 @@ typedef struct {
  * The device arrays are read by the kernels only.  They stay within the
  * buffers whatever the arrays hold: a table entry outside 0 .. num_blocks - 1
  * is a block that is neither written nor seen, tokens past max_new, max_len or
- * `tokens` do not exist.
+ * `tokens` do not exist, and rows of outputs that belong to no token of a
+ * sequence stay as they are.
  */
 typedef struct {
   const int32_t* cu_tokens;
@@ -214,10 +215,12 @@ int fp8_kv_read(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, fp8_dt
  *         (0: none needed): partial results of long sequences, split so that a
  *         few queries fill the chip; joined in a fixed order (same inputs,
  *         same bits).  Calls in flight at the same time need separate ones.
- * Keys and values are widened exactly (keys to bf16, values to fp16, their
- * scales relative to the smallest bias met so far in the sequence: a value
- * keeps at least 11 bits unless it is 2^30 below the largest); probabilities
- * are fp16 relative to a running maximum; sums, maxima and the join are fp32.
+ * Keys widen exactly to bf16; values to fp16, scaled by the smallest bias met so
+ * far among the blocks that a workgroup's queries read, seen or not: exactly,
+ * but for what lies below 2^-40 of the largest value of that bias (E4M3 blocks
+ * within 22 of it are exact, E5M2 ones within 8, their larger codes within
+ * 30).  Probabilities are fp16 relative to a running maximum; logits, sums,
+ * maxima and the join are fp32, lse's last step 64 bits.
  * q_heads: a positive multiple of heads (FP8_ERR_SIZE otherwise, and where
  * max_new * q_heads / heads passes 2^31 - 129).
  */
