@@ -62,6 +62,7 @@ struct AttnArgs {
   int splits;       // tile kernel: most chunks of any row tile
   int row_tiles;    // most row tiles of any sequence
   uint32_t first;   // this launch's first workgroup
+  int least, most;  // rows of a key head that a sequence has to have to be served
   int shares;       // rows kernel: workgroups that share all keys evenly, or 0
   int2* segments;   // rows kernel, shares > 0: [batch][row_tiles][heads], the
                     // first and last workgroup of a segment
@@ -103,6 +104,12 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a) {
   p.seq = x % a.batch.batch;
   p.row_tile = a.row_tiles - 1 - (int)(x / a.batch.batch);
   return p;
+}
+
+// Whether sequence s is this launch's (a mixed batch is two launches').
+__device__ __forceinline__ bool attn_serves(const AttnArgs& a, const KVSeq& s) {
+  const int rows = s.n * a.group;
+  return rows >= a.least && rows <= a.most;
 }
 
 // The logits' factor scale * log2(e) is positive in the kernels: a negative

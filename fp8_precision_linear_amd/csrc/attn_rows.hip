@@ -49,7 +49,7 @@ __device__ __forceinline__ Pair pair_of(const AttnArgs& a, int p) {
   const int i = a.row_tiles == 1 ? p : p / a.row_tiles;
   r.s = kv_seq(a.batch, a.cache.block_size, i);
   const int row0 = (p - i * a.row_tiles) * ROWS;
-  if (row0 >= r.s.n * a.group) return r;
+  if (row0 >= r.s.n * a.group || !attn_serves(a, r.s)) return r;
   const AttnSpan span = attn_span(a, r.s, row0, ROWS);
   r.tiles = max(1, (span.hi - span.lo + kAttnTile - 1) / kAttnTile);
   return r;

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void attn_tile_kerne
   const int BS = a.cache.block_size, H = a.cache.heads, G = a.group;
   const KVSeq s = kv_seq_uniform(a.batch, BS, at.seq);
   const int rows = s.n * G, row0 = at.row_tile * kAttnTileRows;
-  if (row0 >= rows) return;
+  if (row0 >= rows || !attn_serves(a, s)) return;
   const AttnSpan span = attn_span(a, s, row0, kAttnTileRows);
   if (at.split >= span.chunks) return;
   const int kbeg = span.lo + at.split * a.chunk, kend = min(span.hi, kbeg + a.chunk);

@@ -1,6 +1,7 @@
 // Attention over the paged FP8 cache: which kernel takes a batch, how its keys
 // are split, and the join of split results (attn_common.h, attn_rows.hip,
 // attn_tile.hip).
+#include <climits>
 #include <cmath>
 
 #include "attn_common.h"
@@ -9,6 +10,7 @@ namespace fp8lin {
 namespace {
 
 struct AttnPlan {
+  int max_new;          // most new tokens of a sequence that is served
   bool few;             // the rows kernel
   int row_blocks;       // of 16, rows kernel
   int tile_rows;        // rows per row tile
@@ -33,10 +35,14 @@ constexpr int64_t kWantTiles = 512, kCUs = 256, kLeastTiles = 4, kLeastTilesFull
 // 17.2 and 23.1, of 750 to 1500 21.8 and 25.5, of 1250 to 2500 29.6 and 32.2.
 constexpr int64_t kWholeTiles = 24;
 
-AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int window) {
+// Rows of a key head up to which a sequence is the rows kernel's.
+constexpr int kFewRows = 32;
+// max_new: most new tokens of the sequences that the plan is for.
+AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int window, int max_new) {
   AttnPlan p{};
-  const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-  p.few = rows <= 32;
+  const int64_t rows = (int64_t)max_new * (q_heads / c.heads);
+  p.max_new = max_new;
+  p.few = rows <= kFewRows;
   p.row_blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
   p.tile_rows = p.few ? 16 * p.row_blocks : kAttnTileRows;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
@@ -48,7 +54,7 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
     return p;
   }
   int64_t span = b.max_len;  // most keys of a row tile
-  if (window > 0) span = span < (int64_t)window + b.max_new + kAttnTile ? span : (int64_t)window + b.max_new + kAttnTile;
+  if (window > 0) span = span < (int64_t)window + max_new + kAttnTile ? span : (int64_t)window + max_new + kAttnTile;
   const int64_t tiles = span > 0 ? (span + kAttnTile - 1) / kAttnTile : 1;
   const int64_t want = (kWantTiles + p.base - 1) / p.base;
   int64_t per = (tiles + want - 1) / want;
@@ -61,22 +67,56 @@ AttnPlan plan_of(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, 
   return p;
 }
 
+// Mixed batches: sequences of few rows beside some of many get the rows kernel, in
+// launches of their own, where a workgroup of the tile kernel would walk their
+// keys for longer than that takes: a tile of 64 keys costs it about 1 us, the
+// launches 30 us and the caches' reading at 5 TB/s.  Half as much again is asked,
+// since the walk may hide behind the longer sequences' work.  A prompt of 512
+// tokens beside one token on 131071, 64 heads on 8 of 128: one kernel 2370 us, two
+// 91, on 8000 154 and 43, on 2000 47 and 39 (left to one); a prompt of 2000 beside
+// one token on 3000, 32 heads: one kernel 82 us, two 96, on 8000 170 and 100.
+//
+// Returns the most new tokens of a sequence that the rows kernel takes, or 0
+// where the rule says no or the batch's bounds leave no room for such a sequence.
+int mixed_new(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int window) {
+  const int n = kFewRows / (q_heads / c.heads);
+  if (n == 0 || b.max_new <= n || (int64_t)b.tokens > (int64_t)(b.batch - 1) * b.max_new + n) return 0;
+  auto pays = [&](int w) {
+    const double keys = w > 0 && w < b.max_len ? w : b.max_len;
+    const double apart = 30.0 + keys * b.batch * c.heads * c.head_dim * 2 / 5e6;  // us
+    const double walk = plan_of(c, b, q_heads, w, b.max_new).chunk / kAttnTile;
+    return walk > 1.5 * apart;
+  };
+  // (a workspace is made without knowing the window)
+  return pays(0) && (window == 0 || pays(window)) ? n : 0;
+}
+
 // Rows of partial results.
 int64_t part_rows(const AttnPlan& p, const fp8_kv_batch_t& b, int q_heads, int64_t splits) {
   return p.few ? 2 * (int64_t)p.shares * p.tile_rows : splits * b.tokens * q_heads;
 }
 
+// Workspace of a plan whose batch is cut into up to `splits` chunks: partial
+// outputs, references and sums, and for even shares the segments' workgroups.  A
+// multiple of 16.
+int64_t plan_bytes(const AttnPlan& p, const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads, int64_t splits) {
+  if (p.shares == 0 && splits == 1) return 0;
+  const int64_t n = part_rows(p, b, q_heads, splits) * (c.head_dim + 2) * 4 + (p.shares ? p.base * 8 : 0);
+  return (n + 15) / 16 * 16;
+}
+
 // The join of a (new token, query head) whose keys were split into parts
 // (chunks, or shares): out = sum_c w_c out_c / sum_c w_c, w_c = l_c 2^(m_c - M),
 // with M the largest reference of a part that sees keys (one that sees none has
-// l = 0 and out = 0; a weight that underflows still carries a NaN on).  The parts' references and sums stay apart until here:
-// added to a large reference a sum would be rounded away.  out is kept divided by
-// the weights' sum throughout, since a value times a sum could pass fp32's range.
+// l = 0 and out = 0; a weight that underflows still carries a NaN on).  The
+// parts' references and sums stay apart until here: added to a large reference a
+// sum would be rounded away.  out is kept divided by the weights' sum throughout,
+// since a value times a sum could pass fp32's range.
 // A row of D / 4 lanes joins `few` parts alone, several rows a workgroup; many
 // parts are dealt to all rows of a workgroup, which meet in LDS in order.
 constexpr int kJoin = 256;
 constexpr int kFewParts = 16;
-__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows, bool few) {
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_rows, bool few, int max_new) {
   __shared__ v4f so[kJoin];
   __shared__ float ss[kJoin], st[kJoin];
   const int D = a.cache.head_dim, lanes = D / 4, t = threadIdx.x;
@@ -84,12 +124,12 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
   const int head = index % a.q_heads;
   const uint32_t x = index / a.q_heads;
   const int i = x % a.batch.batch, nth = x / a.batch.batch;
-  if (nth >= a.batch.max_new) return;
+  if (nth >= max_new) return;
   const int row = nth * a.group + head % a.group, tile = row / tile_rows;
   int2 w{0, 0};
   if (a.shares) w = a.segments[((int64_t)i * a.row_tiles + tile) * a.cache.heads + head / a.group];
   const KVSeq s = kv_seq(a.batch, a.cache.block_size, i);
-  if (nth >= s.n) return;
+  if (nth >= s.n || !attn_serves(a, s)) return;
   const int64_t at = (int64_t)(s.first + nth) * a.q_heads + head;
   // part c's row of part_o and part_sum: first for c = 0, then from `base` by step
   int64_t first = at, base = at, step = (int64_t)a.batch.tokens * a.q_heads;
@@ -167,19 +207,20 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, int tile_r
 int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads) {
   // the kernels number a key head's rows in 32 bits, up to the end of a tile
   if ((int64_t)b.max_new * (q_heads / c.heads) > 0x7FFFFFFF - kAttnTileRows) return FP8_ERR_SIZE;
-  // the window may shorten the span and so raise the split, up to most_splits
-  const AttnPlan p = plan_of(c, b, q_heads, 0);
-  if (p.base > 0x7FFFFFFF / p.most_splits) return FP8_ERR_SIZE;
   // tiles of a sequence over its heads are counted in 32 bits
   if ((int64_t)c.heads * (b.max_len / kAttnTile + 1) > 0x7FFFFFFF) return FP8_ERR_SIZE;
-  if (p.shares == 0 && p.most_splits == 1) return 0;
+  // the window may shorten the span and so raise the split, up to most_splits, and
+  // leave a mixed batch to one kernel
+  const AttnPlan p = plan_of(c, b, q_heads, 0, b.max_new);
+  if (p.base > 0x7FFFFFFF / p.most_splits) return FP8_ERR_SIZE;
   // the join's workgroups
-  if ((int64_t)b.batch * b.max_new > 0x7FFFFFFF / q_heads) return FP8_ERR_SIZE;
-  return part_rows(p, b, q_heads, p.most_splits) * (c.head_dim + 2) * 4 + (p.shares ? p.base * 8 : 0);
+  if ((p.shares || p.most_splits > 1) && (int64_t)b.batch * b.max_new > 0x7FFFFFFF / q_heads) return FP8_ERR_SIZE;
+  const int64_t bytes = plan_bytes(p, c, b, q_heads, p.most_splits);
+  const int few = mixed_new(c, b, q_heads, 0);
+  return bytes + (few ? plan_bytes(plan_of(c, b, q_heads, 0, few), c, b, q_heads, 1) : 0);
 }
 
 hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stream) {
-  const AttnPlan p = plan_of(pr.cache, pr.batch, pr.q_heads, pr.window);
   AttnArgs a{};
   a.cache = pr.cache;
   a.batch = pr.batch;
@@ -194,29 +235,41 @@ hipError_t launch_kv_attention(const AttnProblem& pr, void* ws, hipStream_t stre
   a.window = pr.window;
   a.out = pr.out;
   a.lse = pr.lse;
-  a.part_o = static_cast<float*>(ws);
-  const int64_t parts = part_rows(p, pr.batch, pr.q_heads, p.splits);
-  a.part_sum = reinterpret_cast<float2*>(a.part_o + parts * pr.cache.head_dim);
-  a.segments = reinterpret_cast<int2*>(a.part_sum + parts);
-  a.shares = p.shares;
-  a.chunk = p.chunk;
-  a.splits = p.splits;
-  a.row_tiles = p.row_tiles;
-  hipError_t e = hipSuccess;
-  in_stretches(p.shares ? p.shares : p.base * p.splits, kAttnThreads, [&](uint32_t first, uint32_t count) {
-    if (e != hipSuccess) return;
-    a.first = first;
-    e = p.few ? launch_attn_rows(a, p.row_blocks, count, stream) : launch_attn_tile(a, count, stream);
-  });
-  if (e != hipSuccess || (p.splits == 1 && p.shares == 0)) return e;
-  const int64_t joins = (int64_t)pr.batch.batch * pr.batch.max_new * pr.q_heads;
-  // shares: a segment's parts are about its tiles over a share's
-  const int64_t parts_most = p.shares ? (p.base < p.shares ? (p.shares + p.base - 1) / p.base + 1 : 3) : p.splits;
-  const bool few = parts_most <= kFewParts;
-  const int per = few ? kJoin / (pr.cache.head_dim / 4) : 1;
-  hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)((joins + per - 1) / per)), dim3(kJoin), 0, stream, a,
-                     p.tile_rows, few);
-  return hipGetLastError();
+  // the launches of a plan, for sequences of `least` to `most` rows of a key head
+  auto run = [&](const AttnPlan& p, int least, int most) -> hipError_t {
+    a.least = least;
+    a.most = most;
+    a.part_o = static_cast<float*>(ws);
+    const int64_t parts = part_rows(p, pr.batch, pr.q_heads, p.splits);
+    a.part_sum = reinterpret_cast<float2*>(a.part_o + parts * pr.cache.head_dim);
+    a.segments = reinterpret_cast<int2*>(a.part_sum + parts);
+    ws = static_cast<char*>(ws) + plan_bytes(p, pr.cache, pr.batch, pr.q_heads, p.splits);
+    a.shares = p.shares;
+    a.chunk = p.chunk;
+    a.splits = p.splits;
+    a.row_tiles = p.row_tiles;
+    hipError_t e = hipSuccess;
+    in_stretches(p.shares ? p.shares : p.base * p.splits, kAttnThreads, [&](uint32_t first, uint32_t count) {
+      if (e != hipSuccess) return;
+      a.first = first;
+      e = p.few ? launch_attn_rows(a, p.row_blocks, count, stream) : launch_attn_tile(a, count, stream);
+    });
+    if (e != hipSuccess || (p.splits == 1 && p.shares == 0)) return e;
+    const int64_t joins = (int64_t)pr.batch.batch * p.max_new * pr.q_heads;
+    // shares: a segment's parts are about its tiles over a share's
+    const int64_t parts_most = p.shares ? (p.base < p.shares ? (p.shares + p.base - 1) / p.base + 1 : 3) : p.splits;
+    const bool few = parts_most <= kFewParts;
+    const int per = few ? kJoin / (pr.cache.head_dim / 4) : 1;
+    hipLaunchKernelGGL(attn_join_kernel, dim3((uint32_t)((joins + per - 1) / per)), dim3(kJoin), 0, stream, a,
+                       p.tile_rows, few, p.max_new);
+    return hipGetLastError();
+  };
+  const AttnPlan whole = plan_of(pr.cache, pr.batch, pr.q_heads, pr.window, pr.batch.max_new);
+  const int few = mixed_new(pr.cache, pr.batch, pr.q_heads, pr.window);
+  if (!few) return run(whole, 0, INT_MAX);
+  const hipError_t e = run(whole, kFewRows + 1, INT_MAX);
+  if (e != hipSuccess) return e;
+  return run(plan_of(pr.cache, pr.batch, pr.q_heads, pr.window, few), 0, kFewRows);
 }
 
 }  // namespace fp8lin
