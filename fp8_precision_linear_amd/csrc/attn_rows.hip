@@ -10,8 +10,8 @@
 // keys are in flight during this tile's softmax, its values during the next
 // one's logits.
 //
-// 131071 tokens of 8 heads of 128: 268 MB in 52-54 us (5.1 TB/s), and 6 us of
-// join; 32 sequences of 1000 to 8191 tokens: 302 MB in 67-69 us (4.5 TB/s: the
+// 131071 tokens of 8 heads of 128: 268 MB in 50-52 us (5.3 TB/s), and 6 us of
+// join; 32 sequences of 1000 to 8191 tokens: 302 MB in 65-68 us (4.5 TB/s: the
 // start, the walk to a share's first segment and the meeting in LDS cost some
 // 10 us of it), and 5 us of join.  One workgroup per segment instead of even
 // shares took 107 us over the 32.

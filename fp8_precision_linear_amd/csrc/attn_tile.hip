@@ -2,7 +2,7 @@
 // cache: attn_common.h has the mathematics.
 //
 // MFMA- and VALU-bound: two prompts of 1777 to 2048 tokens on 1500 to 2048
-// cached, 64 heads of 128 on 8: 312 GFLOP in 337-357 us, 875-925 TFLOP/s, where
+// cached, 64 heads of 128 on 8: 312 GFLOP in 333-354 us, 880-940 TFLOP/s, where
 // a large bf16 product of a library reaches 1205 and converts nothing.  Heads of
 // 256 leave one wave a SIMD (the output alone takes 128 registers), which then
 // waits out what two would overlap.
