@@ -203,9 +203,11 @@ hipError_t launch_swiglu_fwd(const float* h, int64_t rows, int64_t f, uint16_t* 
     const Grid g = grid_of(rows, f);
     in_stretches(g.blocks, kThreads, [&](uint32_t first, uint32_t count) {
       if (g.vec)
-        hipLaunchKernelGGL(swiglu_fwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax, first);
+        hipLaunchKernelGGL(swiglu_fwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax,
+                           first);
       else
-        hipLaunchKernelGGL(swiglu_fwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax, first);
+        hipLaunchKernelGGL(swiglu_fwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, f, g.upr, g.bpr, a, amax,
+                           first);
     });
   }
   return hipGetLastError();
@@ -218,9 +220,11 @@ hipError_t launch_swiglu_bwd(const float* h, const float* da, int64_t rows, int6
     const Grid g = grid_of(rows, f);
     in_stretches(g.blocks, kThreads, [&](uint32_t first, uint32_t count) {
       if (g.vec)
-        hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax, first);
+        hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax,
+                           first);
       else
-        hipLaunchKernelGGL(swiglu_bwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax, first);
+        hipLaunchKernelGGL(swiglu_bwd_kernel<1>, dim3(count), dim3(kThreads), 0, stream, h, da, f, g.upr, g.bpr, dh, amax,
+                           first);
     });
   }
   return hipGetLastError();
