@@ -7,10 +7,12 @@
 #include <cstring>
 
 #include "internal.h"
+#include "seq_attn.h"
 
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxRowStride = 1 << 24;  // of attention over packed sequences
 // 0 = not checked yet, 1 = gfx950, 2 = something else.
 std::atomic<int> g_arch_ok[kMaxDevices];
 
@@ -144,6 +146,41 @@ fp8_kv_batch_t bounded(const fp8_kv_batch_t* b) {
 }
 
 bool kv_empty(const fp8_kv_batch_t& b) { return b.batch == 0 || b.tokens == 0 || b.max_new == 0; }
+
+// Packed sequences and the heads over them (no device call).
+int seqs_checks(const fp8_seqs_t* s, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  if (!s) return FP8_ERR_NULL;
+  if (s->batch < 0 || s->tokens < 0 || s->max_len < 0 || s->max_len > (1 << 30)) return FP8_ERR_SIZE;
+  if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return FP8_ERR_SIZE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP8_ERR_SIZE;
+  if ((int64_t)q_heads * head_dim > kMaxRowStride) return FP8_ERR_SIZE;
+  if (s->batch == 0 || s->tokens == 0 || s->max_len == 0) return FP8_OK;  // nothing to do
+  if (!s->cu_tokens) return FP8_ERR_NULL;
+  if (misaligned_word(s->cu_tokens)) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+bool seqs_empty(const fp8_seqs_t& s) { return s.batch == 0 || s.tokens == 0 || s.max_len == 0; }
+fp8lin::SeqAttnArgs seq_args(const fp8_seqs_t& s, int32_t q_heads, int32_t kv_heads, float scale, int32_t causal,
+                             int32_t window) {
+  fp8lin::SeqAttnArgs a{};
+  a.cu = s.cu_tokens;
+  a.batch = s.batch;
+  a.tokens = s.tokens;
+  a.max_len = s.max_len < s.tokens ? s.max_len : s.tokens;  // a caller's bound may be loose
+  a.q_heads = q_heads;
+  a.heads = kv_heads;
+  a.group = q_heads / kv_heads;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.causal = causal != 0;
+  a.window = window;
+  return a;
+}
+// Rows whose 32-bit offsets within a tile the kernels form.
+int seq_rows_checks(const void* p, int64_t stride, int64_t heads, int64_t head_dim) {
+  if (stride > kMaxRowStride) return FP8_ERR_SIZE;
+  return rows_checks(p, stride, heads, head_dim, 2);
+}
 
 }  // namespace
 
@@ -666,6 +703,65 @@ int fp8_kv_attention(const fp8_kv_cache_t* cache, const fp8_kv_batch_t* batch, c
   if ((st = device_ok()) != FP8_OK) return st;
   const fp8lin::AttnProblem p{*cache, b, q, q_stride, q_heads, scale, causal, window, out, lse};
   return hip_status(fp8lin::launch_kv_attention(p, ws, (hipStream_t)stream));
+}
+
+int fp8_attention_fwd(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                      int64_t v_stride, const fp8_seqs_t* seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                      float scale, int32_t causal, int32_t window, uint16_t* out, float* lse, void* stream) {
+  int st = seqs_checks(seqs, q_heads, kv_heads, head_dim);
+  if (st != FP8_OK) return st;
+  if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
+  if (seqs_empty(*seqs)) return FP8_OK;
+  if ((st = seq_rows_checks(q, q_stride, q_heads, head_dim)) != FP8_OK) return st;
+  if ((st = seq_rows_checks(k, k_stride, kv_heads, head_dim)) != FP8_OK) return st;
+  if ((st = seq_rows_checks(v, v_stride, kv_heads, head_dim)) != FP8_OK) return st;
+  if (!out || !lse) return FP8_ERR_NULL;
+  if (misaligned(out) || misaligned_word(lse)) return FP8_ERR_ALIGN;
+  if ((st = device_ok()) != FP8_OK) return st;
+  fp8lin::SeqAttnArgs a = seq_args(*seqs, q_heads, kv_heads, scale, causal, window);
+  a.q = q, a.k = k, a.v = v;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.out = out;
+  a.lse = lse;
+  return hip_status(fp8lin::launch_seq_attn_fwd(a, head_dim, (hipStream_t)stream));
+}
+
+int64_t fp8_attention_bwd_workspace_bytes(const fp8_seqs_t* seqs, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim) {
+  const int st = seqs_checks(seqs, q_heads, kv_heads, head_dim);
+  if (st != FP8_OK) return st;
+  if (seqs_empty(*seqs)) return 0;
+  const fp8lin::SeqAttnArgs a = seq_args(*seqs, q_heads, kv_heads, 1.0f, 0, 0);
+  return fp8lin::seq_attn_bwd_workspace_bytes({a.batch, a.tokens, a.max_len, q_heads, kv_heads, head_dim});
+}
+
+int fp8_attention_bwd(const uint16_t* dout, int64_t dout_stride, const uint16_t* q, int64_t q_stride,
+                      const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const uint16_t* out,
+                      const float* lse, const fp8_seqs_t* seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                      float scale, int32_t causal, int32_t window, uint16_t* dq, int64_t dq_stride, uint16_t* dk,
+                      int64_t dk_stride, uint16_t* dv, int64_t dv_stride, void* ws, int64_t ws_bytes, void* stream) {
+  const int64_t need = fp8_attention_bwd_workspace_bytes(seqs, q_heads, kv_heads, head_dim);
+  if (need < 0) return (int)need;
+  if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
+  if (seqs_empty(*seqs)) return FP8_OK;
+  int st = FP8_OK;
+  const struct { const void* p; int64_t stride; int32_t heads; } rows[] = {
+      {dout, dout_stride, q_heads}, {q, q_stride, q_heads}, {k, k_stride, kv_heads}, {v, v_stride, kv_heads},
+      {dq, dq_stride, q_heads}, {dk, dk_stride, kv_heads}, {dv, dv_stride, kv_heads}};
+  for (const auto& r : rows)
+    if ((st = seq_rows_checks(r.p, r.stride, r.heads, head_dim)) != FP8_OK) return st;
+  if (!out || !lse || !ws) return FP8_ERR_NULL;
+  if (misaligned(out) || misaligned_word(lse) || misaligned(ws)) return FP8_ERR_ALIGN;
+  if (ws_bytes < need) return FP8_ERR_SIZE;
+  if ((st = device_ok()) != FP8_OK) return st;
+  fp8lin::SeqAttnArgs a = seq_args(*seqs, q_heads, kv_heads, scale, causal, window);
+  a.q = q, a.k = k, a.v = v, a.dout = dout;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.dout_stride = dout_stride;
+  a.out = const_cast<uint16_t*>(out);
+  a.lse = const_cast<float*>(lse);
+  a.dq = dq, a.dk = dk, a.dv = dv;
+  a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
+  return hip_status(fp8lin::launch_seq_attn_bwd(a, head_dim, ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 
 #include "fp8lin.h"
 #include "fp8lin_block.h"
+#include "fp8lin_train.h"
 
 namespace fp8lin {
 

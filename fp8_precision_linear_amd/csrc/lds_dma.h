@@ -58,4 +58,14 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t offset, uint
       : "memory", "m0");
 }
 
+// 4 bytes per lane from `src` into LDS at `lds_base + 4 * lane`.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds_base) {
+  asm volatile(
+      "s_mov_b32 m0, %1\n\t"
+      "global_load_lds_dword %0, off"
+      :
+      : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds_base))
+      : "memory", "m0");
+}
+
 }  // namespace fp8lin

@@ -1,0 +1,237 @@
+// Attention over packed sequences, forward: seq_attn.h has the mathematics.
+//
+// A workgroup of four waves takes 128 query rows of one head; a wave owns 32 of
+// them, its queries, logits and output in registers.  Tiles of 64 keys and
+// values go through LDS by DMA, the next one on its way while one is consumed.
+// Logits against a reference that follows the row maximum lazily: it moves when
+// a tile's probabilities outgrow it, so most tiles rescale nothing.
+#include "seq_attn.h"
+
+namespace fp8lin {
+namespace {
+
+// Keys of a tile.
+template <int D>
+constexpr int kKeysOf = D == 256 ? 32 : 64;
+// A lane's 32 probabilities of a tile may add up to this before its row's
+// reference moves.
+constexpr float kMostPart = 0x1p16f;
+// References from here on have their logits rounded before they are subtracted
+// (attn_common.h).
+constexpr float kHuge = 0x1p22f;
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(SeqAttnArgs a) {
+  constexpr int J = D / 16, DT = D / 32, kKeys = kKeysOf<D>, SUB = kKeys / 32;
+  using Load = TileLoad<D, kKeys>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][Load::kBytes];  // [buffer][keys, values]
+  __shared__ int found[4];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int r32 = lane & 31, h = lane >> 5;
+  uint32_t x = a.first + blockIdx.x;
+  const int kv_head = x % a.heads;
+  x /= a.heads;
+  const int head = kv_head * a.group + x % a.group;
+  x /= a.group;
+  const Seq s = seq_of(a, x % a.batch);
+  const int row0 = (a.tiles - 1 - (int)(x / a.batch)) * kSeqRows;  // late rows see most: first
+  if (row0 >= s.n) return;
+  const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
+  const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
+
+  const int wrow = row0 + 32 * wave, row = wrow + r32;
+  v8b q[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) q[j] = v8b{};
+  if (row < s.n) {
+    const uint16_t* p = a.q + (int64_t)(s.first + row) * a.q_stride + head * D + 8 * h;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      q[j] = __builtin_bit_cast(v8b, sign_queries(*reinterpret_cast<const uint4*>(p + 16 * j), a.scale));
+  }
+  const float c_log2 = a.scale == 0.0f ? 1.0f : fabsf(a.scale_log2);
+  // the keys of the lane's row, and of any of the wave's
+  const int hi = a.causal ? min(row + 1, s.n) : s.n, lo = a.window ? row - a.window + 1 : 0;
+  const int whi = wrow >= s.n ? 0 : (a.causal ? min(wrow + 32, s.n) : s.n);
+  const int wlo = a.window ? wrow - a.window + 1 : 0;
+  // the keys that every row of the workgroup sees
+  const int all_hi = a.causal ? min(s.n, row0 + 1) : s.n;
+  const int all_lo = a.window ? min(row0 + kSeqRows, s.n) - a.window : 0;
+
+  v16f o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = zero16();
+  float m = kNoRef, l = 0.0f;
+  bool huge = false;
+
+  const uint32_t ring0 = lds_addr(ring);
+  const int64_t ks = a.k_stride * 2, vs = a.v_stride * 2;
+  const Load load_k(lane, wave, (uint32_t)ks), load_v(lane, wave, (uint32_t)vs);
+  const uint16_t* kp = a.k + (int64_t)(s.first + klo) * a.k_stride + kv_head * D;
+  const uint16_t* vp = a.v + (int64_t)(s.first + klo) * a.v_stride + kv_head * D;
+  auto issue = [&](int T, int buf) {
+    load_k.issue(kp + (int64_t)(T - klo) * a.k_stride, ks, s.n - T, ring0 + buf * 2 * Load::kBytes, wave);
+    load_v.issue(vp + (int64_t)(T - klo) * a.v_stride, vs, s.n - T, ring0 + (2 * buf + 1) * Load::kBytes, wave);
+  };
+  const uint32_t krow = row_place<D>(lane), vcol = column_place<D>(lane);
+
+  auto consume = [&](bool masked, int T, uint32_t tile) {
+    auto seen = [&](int sub, int e) {
+      const int key = T + 32 * sub + result_row(e, h);
+      return key >= lo && key < hi;
+    };
+    v16f t[SUB];
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) t[sub] = zero16();
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) t[sub] = mma(lds_row(((tile + krow) ^ (32 * j)) + sub * 64 * D), q[j], t[sub]);
+      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // LDS reads do not run further ahead: registers
+    }
+    if (masked) {
+      asm volatile("");  // a branch: as selects it would cost every tile
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[sub][e] = seen(sub, e) ? t[sub][e] : -INFINITY;
+    }
+    float scale = c_log2;
+    auto round_logits = [&] {
+      asm volatile("");  // a branch of its own, and a rare one
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[sub][e] = rounded(t[sub][e], scale);
+      scale = 1.0f;
+    };
+    if (__builtin_expect(huge, 0)) round_logits();
+    v8b p[SUB][2];
+    float part;
+    auto probabilities = [&] {
+      part = 0.0f;
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) {
+        v16f w;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          w[e] = __builtin_amdgcn_exp2f(fmaf(t[sub][e], scale, -m));
+          part += w[e];  // of the fp32 values
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) p[sub][c] = operand(w, c);
+      }
+    };
+    probabilities();
+    if (__any(!(part <= kMostPart))) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = raw_max(top, t[sub][e]);
+      top = swap32_max(top * scale);
+      const float to = top > m ? top : m;
+      const float f = __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= f;
+      if (__any(fabsf(m) > kHuge && m != kNoRef)) {
+        if (!huge) round_logits();
+        huge = true;
+      }
+      probabilities();
+    }
+    l += part;
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t v = tile + Load::kBytes + vcol;
+#pragma unroll
+    for (int c = 0; c < 2 * SUB; ++c) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = mma(column_step<D>(v + c * 32 * D, d), p[c >> 1][c & 1], o[d]);
+      if (c & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Values of a tile that are NaN or infinite: the outputs of the rows that see
+  // them become NaN -- counted by a product of "is bad" with what is seen --
+  // before they are cleared.
+  auto record = [&](int T, uint32_t values) {
+    v8b see[2 * SUB];
+#pragma unroll
+    for (int c = 0; c < 2 * SUB; ++c) {
+      v8s w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int key = T + 32 * (c >> 1) + result_row(8 * (c & 1) + e, h);
+        w[e] = key >= lo && key < hi ? 0x3F80 : 0;  // 1.0
+      }
+      see[c] = __builtin_bit_cast(v8b, w);
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      v16f n = zero16();
+#pragma unroll
+      for (int c = 0; c < 2 * SUB; ++c) {
+        __builtin_amdgcn_sched_barrier(0);
+        v4i32 bad = bad_of(column_step<D>(values + vcol + c * 32 * D, d));
+        bad &= 0x3F803F80;
+        n = mma(__builtin_bit_cast(v8b, bad), see[c], n);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = n[e] > 0.0f ? NAN : o[d][e];
+    }
+  };
+
+  issue(klo, 0);
+  int buf = 0;
+  for (int T = klo; T < khi; T += kKeys, buf ^= 1) {
+    wait_vmcnt<0>();
+    bare_barrier();  // this tile is whole, and every wave is done with the one before
+    if (T + kKeys < khi) issue(T + kKeys, buf ^ 1);
+    const uint32_t tile = ring0 + buf * 2 * Load::kBytes;
+    if (T + kKeys > all_hi || T < all_lo) {
+      const uint32_t values = tile + Load::kBytes;
+      if (has_bad<Load::kBytes>(values, found)) {
+        record(T, values);
+        clear_bad<Load::kBytes>(values, 2 * D, nullptr);
+      }
+    }
+    if (T >= whi || T + kKeys <= wlo) continue;
+    // (rows past the sequence's end see what its last row sees: not stored)
+    const bool whole = T + kKeys <= min(s.n, a.causal ? wrow + 1 : s.n) && (!a.window || T > wrow + 31 - a.window);
+    consume(!whole, T, tile);
+  }
+
+  l = swap32_sum(l);
+  if (row >= s.n) return;
+  const float inv = 1.0f / l;
+  const int64_t cell = (int64_t)(s.first + row) * a.q_heads + head;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = finite_or_nan(o[d][4 * u + e]) * inv;
+      *reinterpret_cast<uint2*>(a.out + cell * D + 32 * d + 8 * u + 4 * h) =
+          make_uint2(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]));
+    }
+  if (h == 0) a.lse[cell] = row_lse(m, l);
+}
+
+}  // namespace
+
+hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) {
+  a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
+  in_stretches((int64_t)a.tiles * a.batch * a.q_heads, 256, [&](uint32_t first, uint32_t count) {
+    a.first = first;
+    if (head_dim == 64) hipLaunchKernelGGL(seq_attn_fwd_kernel<64>, dim3(count), dim3(256), 0, stream, a);
+    else if (head_dim == 128) hipLaunchKernelGGL(seq_attn_fwd_kernel<128>, dim3(count), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(seq_attn_fwd_kernel<256>, dim3(count), dim3(256), 0, stream, a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace fp8lin
