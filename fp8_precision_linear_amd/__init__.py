@@ -78,6 +78,14 @@ SIGNATURES = {
     "fp8_kv_attention_workspace_bytes": (_i64, [_vp, _vp, _i32]),
     "fp8_kv_attention": (_ci, [_vp, _vp, _vp, _i64, _i32, _cf, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
     # include/fp8lin_train.h
+    "fp8_embedding_fwd": (_ci, [_vp, _i32, _i64, _vp, _ci, _i64, _i64, _cf, _vp, _ci, _vp]),
+    "fp8_embedding_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "fp8_embedding_bwd": (_ci, [_vp, _ci, _vp, _i32, _i64, _i64, _i64, _cf, _i32, _vp, _vp, _i64, _vp]),
+    "fp8_qk_norm_rope_fwd": (_ci, [_vp, _ci, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _ci, _cf, _vp, _vp, _vp, _i32, _i32,
+                                   _vp, _vp]),
+    "fp8_qk_norm_rope_bwd_workspace_bytes": (_i64, [_i64, _i32, _i32, _i32]),
+    "fp8_qk_norm_rope_bwd": (_ci, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _ci, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _ci,
+                                   _cf, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
     "fp8_attention_fwd": (_ci, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _cf, _i32, _i32, _vp, _vp,
                                 _vp]),
     "fp8_attention_bwd_workspace_bytes": (_i64, [_vp, _i32, _i32, _i32]),

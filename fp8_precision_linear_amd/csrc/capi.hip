@@ -12,6 +12,7 @@
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - (1 << 16);  // of the embedding's gradient
 constexpr int64_t kMaxRowStride = 1 << 24;  // of attention over packed sequences
 // 0 = not checked yet, 1 = gfx950, 2 = something else.
 std::atomic<int> g_arch_ok[kMaxDevices];
@@ -176,6 +177,34 @@ fp8lin::SeqAttnArgs seq_args(const fp8_seqs_t& s, int32_t q_heads, int32_t kv_he
   a.window = window;
   return a;
 }
+// Ids and sizes of the embedding (no device call).
+int embedding_checks(const void* ids, int32_t id_bits, int64_t tokens, int64_t vocab, int64_t d) {
+  if (id_bits != 32 && id_bits != 64) return FP8_ERR_DTYPE;
+  if (tokens < 0 || tokens > kMaxTokens || vocab < 0 || vocab > (int64_t)0x7FFFFFFF || d < 1 || d > (1 << 24))
+    return FP8_ERR_SIZE;
+  // workgroups of 1024 elements are counted in 32 bits
+  if (tokens * ((d + 1023) / 1024) > (int64_t)0x7FFFFFFF) return FP8_ERR_SIZE;
+  if (tokens > 0 && !ids) return FP8_ERR_NULL;
+  if (((uintptr_t)ids & (id_bits / 8 - 1)) != 0) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+
+// The fused rows of queries, keys and values, their norms and their rotation.
+int qk_checks(const fp8lin::QkProblem& p) {
+  if (p.tokens < 0 || p.tokens > (int64_t)0x7FFFFFFF || p.q_heads < 1 || p.kv_heads < 1) return FP8_ERR_SIZE;
+  if (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256) return FP8_ERR_SIZE;
+  const int64_t heads = (int64_t)p.q_heads + 2 * (int64_t)p.kv_heads;
+  if (heads * p.head_dim > kMaxRowStride) return FP8_ERR_SIZE;
+  if (!(p.eps >= 0)) return FP8_ERR_SIZE;
+  if (bad_dtype(p.x_dtype) || (p.wq && bad_dtype(p.w_dtype))) return FP8_ERR_DTYPE;
+  if (!p.wq != !p.wk || !p.cos != !p.sin) return FP8_ERR_NULL;
+  if (p.cos && (p.rope_rows < 1 || (!p.positions && p.rope_rows < p.tokens))) return FP8_ERR_SIZE;
+  if (misaligned(p.wq) || misaligned(p.wk) || misaligned(p.cos) || misaligned(p.sin) || misaligned_word(p.positions))
+    return FP8_ERR_ALIGN;
+  if (p.tokens == 0) return FP8_OK;
+  return rows_checks(p.x, p.x_stride, heads, p.head_dim, p.x_dtype == FP8_IN_FP32 ? 4 : 2);
+}
+
 // Rows whose 32-bit offsets within a tile the kernels form.
 int seq_rows_checks(const void* p, int64_t stride, int64_t heads, int64_t head_dim) {
   if (stride > kMaxRowStride) return FP8_ERR_SIZE;
@@ -762,6 +791,92 @@ int fp8_attention_bwd(const uint16_t* dout, int64_t dout_stride, const uint16_t*
   a.dq = dq, a.dk = dk, a.dv = dv;
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
   return hip_status(fp8lin::launch_seq_attn_bwd(a, head_dim, ws, (hipStream_t)stream));
+}
+
+int fp8_embedding_fwd(const void* ids, int32_t id_bits, int64_t tokens, const void* table, fp8_dtype_t table_dtype,
+                      int64_t vocab, int64_t d, float scale, void* out, fp8_dtype_t out_dtype, void* stream) {
+  int st = embedding_checks(ids, id_bits, tokens, vocab, d);
+  if (st != FP8_OK) return st;
+  if (bad_dtype(table_dtype) || bad_dtype(out_dtype)) return FP8_ERR_DTYPE;
+  if (tokens == 0) return FP8_OK;
+  if (!out || (vocab > 0 && !table)) return FP8_ERR_NULL;
+  if (misaligned(table) || misaligned(out)) return FP8_ERR_ALIGN;
+  if ((st = device_ok()) != FP8_OK) return st;
+  return hip_status(fp8lin::launch_embedding_fwd(ids, id_bits == 64, tokens, table, table_dtype, vocab, d, scale, out,
+                                                 out_dtype, (hipStream_t)stream));
+}
+
+int64_t fp8_embedding_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t d) {
+  const int st = embedding_checks(reinterpret_cast<const void*>(16), 32, tokens, vocab, d);
+  return st != FP8_OK ? st : fp8lin::embedding_bwd_workspace_bytes(tokens, vocab, d);
+}
+
+int fp8_embedding_bwd(const void* dout, fp8_dtype_t dout_dtype, const void* ids, int32_t id_bits, int64_t tokens,
+                      int64_t vocab, int64_t d, float scale, int32_t accumulate, float* dtable, void* ws,
+                      int64_t ws_bytes, void* stream) {
+  int st = embedding_checks(ids, id_bits, tokens, vocab, d);
+  if (st != FP8_OK) return st;
+  if (bad_dtype(dout_dtype)) return FP8_ERR_DTYPE;
+  if (vocab == 0 || (tokens == 0 && accumulate)) return FP8_OK;
+  if (!dtable || (tokens > 0 && (!dout || !ws))) return FP8_ERR_NULL;
+  if (misaligned(dtable) || misaligned(dout) || misaligned(ws)) return FP8_ERR_ALIGN;
+  if (ws_bytes < fp8lin::embedding_bwd_workspace_bytes(tokens, vocab, d)) return FP8_ERR_SIZE;
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::EmbeddingGrad g{dout, dout_dtype, ids, id_bits == 64, tokens, vocab, d, scale, accumulate != 0, dtable};
+  return hip_status(fp8lin::launch_embedding_bwd(g, ws, (hipStream_t)stream));
+}
+
+int fp8_qk_norm_rope_fwd(const void* x, fp8_dtype_t x_dtype, int64_t x_stride, int64_t tokens, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim, const void* wq, const void* wk, fp8_dtype_t w_dtype,
+                         float eps, const int32_t* positions, const float* cos, const float* sin, int32_t rope_rows,
+                         int32_t rope_pairs, uint16_t* y, void* stream) {
+  const fp8lin::QkProblem p{x, x_dtype, x_stride, tokens, q_heads, kv_heads, head_dim, wq, wk, w_dtype, eps,
+                            positions, cos, sin, rope_rows, rope_pairs};
+  int st = qk_checks(p);
+  if (st != FP8_OK) return st;
+  if (tokens == 0) return FP8_OK;
+  if (!y) return FP8_ERR_NULL;
+  if (misaligned(y)) return FP8_ERR_ALIGN;
+  if ((st = device_ok()) != FP8_OK) return st;
+  return hip_status(fp8lin::launch_qk_norm_fwd(p, y, (hipStream_t)stream));
+}
+
+int64_t fp8_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  fp8lin::QkProblem p{};
+  p.x = reinterpret_cast<const void*>(16);
+  p.x_stride = ((int64_t)q_heads + 2 * (int64_t)kv_heads) * head_dim;
+  p.tokens = tokens, p.q_heads = q_heads, p.kv_heads = kv_heads, p.head_dim = head_dim;
+  const int st = qk_checks(p);
+  return st != FP8_OK ? st : fp8lin::qk_norm_bwd_workspace_bytes(p);
+}
+
+int fp8_qk_norm_rope_bwd(const uint16_t* dq, int64_t dq_stride, const uint16_t* dk, int64_t dk_stride,
+                         const uint16_t* dv, int64_t dv_stride, const void* x, fp8_dtype_t x_dtype, int64_t x_stride,
+                         int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* wq,
+                         const void* wk, fp8_dtype_t w_dtype, float eps, const int32_t* positions, const float* cos,
+                         const float* sin, int32_t rope_rows, int32_t rope_pairs, void* dx, float* dwq, float* dwk,
+                         void* ws, int64_t ws_bytes, void* stream) {
+  const fp8lin::QkProblem p{x, x_dtype, x_stride, tokens, q_heads, kv_heads, head_dim, wq, wk, w_dtype, eps,
+                            positions, cos, sin, rope_rows, rope_pairs};
+  int st = qk_checks(p);
+  if (st != FP8_OK) return st;
+  if (tokens > 0) {
+    if ((st = rows_checks(dq, dq_stride, q_heads, head_dim, 2)) != FP8_OK) return st;
+    if ((st = rows_checks(dk, dk_stride, kv_heads, head_dim, 2)) != FP8_OK) return st;
+    if ((st = rows_checks(dv, dv_stride, kv_heads, head_dim, 2)) != FP8_OK) return st;
+    if (!dx) return FP8_ERR_NULL;
+    if (misaligned(dx)) return FP8_ERR_ALIGN;
+  }
+  if (wq) {
+    if (!dwq || !dwk || !ws) return FP8_ERR_NULL;
+    if (misaligned_word(dwq) || misaligned_word(dwk) || misaligned(ws)) return FP8_ERR_ALIGN;
+    if (ws_bytes < fp8lin::qk_norm_bwd_workspace_bytes(p)) return FP8_ERR_SIZE;
+  } else if (tokens == 0) {
+    return FP8_OK;
+  }
+  if ((st = device_ok()) != FP8_OK) return st;
+  const fp8lin::QkGrads g{dq, dk, dv, dq_stride, dk_stride, dv_stride, dx, dwq, dwk};
+  return hip_status(fp8lin::launch_qk_norm_bwd(p, g, static_cast<float*>(ws), (hipStream_t)stream));
 }
 
 }  // extern "C"

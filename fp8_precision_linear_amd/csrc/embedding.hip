@@ -1,0 +1,503 @@
+// Embedding and its gradient (include/fp8lin_train.h has the definitions).
+//
+// Lookup: HBM-bound, a row read and a row written for each token.
+//
+// Gradient.  Tokens are sorted by id, stably, so that the rows of an id lie
+// together in the tokens' order; then rows are added without atomics, in an
+// order that does not depend on the launch.  The sort is a radix sort by digits
+// of up to nine bits.  Up to kTile tokens it is one workgroup's, in LDS, while
+// the others of its launch write the gradient's zeros; more tokens take three
+// launches a digit.  The sums: sorted positions are cut into chunks of kChunk; a
+// chunk writes the ids that lie whole in it, and leaves the sums of those that
+// reach past its ends in the workspace, which a last kernel adds in order.
+// HBM-bound by the gradient's writing: vocab x d floats, and dout read once.
+#include <algorithm>
+
+#include "norm_kernel.h"
+
+namespace fp8lin {
+namespace {
+
+__device__ __forceinline__ int64_t id_at(const void* ids, bool wide, int64_t t) {
+  return wide ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
+}
+// A unit's element in its row, and what is left of the row there.
+struct Unit {
+  int64_t row;
+  int col, left;
+};
+
+// ---------------------------------------------------------------- lookup
+struct LookupArgs {
+  const void* ids;
+  bool wide;
+  int64_t tokens, vocab;
+  const void* table;
+  int d, units;  // units of four elements of a row
+  float scale;
+  void* out;
+  uint32_t first;
+};
+
+// Units of all rows in turn, U of a lane, a workgroup's width apart.
+template <int TT, int OT, bool WHOLE, int U>
+__global__ __launch_bounds__(256) void embedding_fwd_kernel(LookupArgs a) {
+  const int64_t base = (int64_t)(a.first + blockIdx.x) * (256 * U);
+  const int64_t row0 = base / a.units;
+  const int rem = (int)(base - row0 * a.units) + threadIdx.x;
+  Raw<TT> raw[U];
+  Unit at[U];
+  bool there[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t x = (uint32_t)rem + 256 * i, r = x / (uint32_t)a.units;
+    at[i].row = row0 + r;
+    at[i].col = 4 * (int)(x - r * (uint32_t)a.units);
+    at[i].left = a.d - at[i].col;
+    there[i] = at[i].row < a.tokens;
+    raw[i] = Raw<TT>{};
+    if (there[i]) {
+      const int64_t id = id_at(a.ids, a.wide, at[i].row);
+      if (id >= 0 && id < a.vocab) raw[i] = load_raw<TT, WHOLE, false>(a.table, id * a.d + at[i].col, at[i].left);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (!there[i]) continue;
+    float v[4];
+    unpack<TT>(raw[i], v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= a.scale;
+    store_as<OT, WHOLE>(a.out, at[i].row * a.d + at[i].col, at[i].left, v);
+  }
+}
+
+// ---------------------------------------------------------------- sort
+constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
+constexpr int kItems = 16;                       // of a lane
+constexpr int kTile = kSortThreads * kItems;     // tokens of a workgroup
+constexpr int kMaxDigit = 9, kBins = 1 << kMaxDigit;
+
+struct SortArgs {
+  const void* ids;
+  bool wide;
+  int64_t tokens, vocab;
+  int passes, bits;           // digits, and the bits of each
+  uint32_t *key, *order;      // sorted; a key of vocab: no token of the table
+  uint32_t *key2, *order2;    // more than one tile: between passes
+  uint32_t* hist;             // [bins][tiles]
+  int tiles;
+  float* zero;                // cleared by the workgroups behind the tiles', or null
+  int64_t zeros;              // floats
+};
+
+__device__ __forceinline__ uint32_t key_at(const SortArgs& a, int64_t t) {
+  const int64_t id = id_at(a.ids, a.wide, t);
+  return id >= 0 && id < a.vocab ? (uint32_t)id : (uint32_t)a.vocab;
+}
+
+// Workgroups past the sorting ones clear the gradient.
+__device__ __forceinline__ void clear_share(const SortArgs& a, int sorting) {
+  const int64_t groups = (int64_t)gridDim.x - sorting, units = (a.zeros + 3) / 4;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t i = ((int64_t)blockIdx.x - sorting) * kSortThreads + threadIdx.x; i < units; i += groups * kSortThreads) {
+    if (4 * i + 4 <= a.zeros) {
+      __builtin_nontemporal_store(zero, reinterpret_cast<f32x4*>(a.zero + 4 * i));
+    } else {
+      for (int64_t j = 4 * i; j < a.zeros; ++j) a.zero[j] = 0.0f;
+    }
+  }
+}
+
+// A wave's LDS operations complete in order; this keeps the compiler to it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+struct SortShared {
+  uint16_t count[kSortWaves][kBins];  // of a wave's items with that digit, then their first place
+  uint32_t wave_total[kSortWaves];
+};
+
+// The places of a tile's items when they are sorted by one digit, stably.  Items
+// lie wave by wave: item (wave, i, lane) is number wave * 64 * kItems + 64 i +
+// lane.  Absent items (past n) have the last place.  Ends with a barrier.
+// first_of: receives the first place of each digit.
+__device__ __forceinline__ void digit_places(const uint32_t (&key)[kItems], int n, int shift, int bits,
+                                             SortShared& s, uint32_t (&place)[kItems], uint32_t* first_of) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bins = 1 << bits;
+  for (int b = lane; b < bins; b += 64) s.count[wave][b] = 0;
+  wave_fence();
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const bool there = wave * 64 * kItems + 64 * i + lane < n;
+    const uint32_t digit = (key[i] >> shift) & (bins - 1);
+    uint64_t same = __ballot(there);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((digit >> b) & 1);
+      same &= (digit >> b) & 1 ? set : ~set;
+    }
+    const uint32_t before = there ? s.count[wave][digit] : 0;
+    place[i] = before + __popcll(same & below);
+    wave_fence();
+    if (there && (same & below) == 0) s.count[wave][digit] = (uint16_t)(before + __popcll(same));
+    wave_fence();
+  }
+  __syncthreads();
+  // first places: digits in order, within a digit the waves in order
+  uint32_t total = 0;
+  if ((int)threadIdx.x < bins)
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = s.count[w][threadIdx.x];
+      s.count[w][threadIdx.x] = (uint16_t)total;
+      total += c;
+    }
+  uint32_t upto = total;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = __shfl_up(upto, off, 64);
+    if (lane >= off) upto += o;
+  }
+  if (lane == 63) s.wave_total[wave] = upto;
+  __syncthreads();
+  uint32_t base = upto - total;
+  for (int w = 0; w < wave; ++w) base += s.wave_total[w];
+  if ((int)threadIdx.x < bins) first_of[threadIdx.x] = base;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const uint32_t digit = (key[i] >> shift) & (bins - 1);
+    if (wave * 64 * kItems + 64 * i + lane < n) place[i] += s.count[wave][digit] + first_of[digit];
+  }
+}
+
+// Up to kTile tokens: every digit in LDS.
+__global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(SortArgs a) {
+  __shared__ SortShared s;
+  __shared__ uint32_t first_of[kBins];
+  __shared__ uint32_t keys[kTile];
+  __shared__ uint16_t orders[kTile];
+  if (blockIdx.x > 0) return clear_share(a, 1);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = (int)a.tokens;
+  uint32_t key[kItems], order[kItems], place[kItems];
+  const int mine = wave * 64 * kItems + lane;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    order[i] = mine + 64 * i;
+    key[i] = mine + 64 * i < n ? key_at(a, mine + 64 * i) : 0xFFFFFFFFu;
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    digit_places(key, n, pass * a.bits, a.bits, s, place, first_of);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (mine + 64 * i < n) {
+        keys[place[i]] = key[i];
+        orders[place[i]] = (uint16_t)order[i];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (mine + 64 * i < n) {
+        key[i] = keys[mine + 64 * i];
+        order[i] = orders[mine + 64 * i];
+      }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (mine + 64 * i < n) {
+      a.key[mine + 64 * i] = key[i];
+      a.order[mine + 64 * i] = order[i];
+    }
+}
+
+// More tokens.  A pass: how many items of each digit a tile has, where the
+// digits of the tiles start, and the items to their places.
+struct Pass {
+  const uint32_t *key, *order;  // null: the first pass, from the ids
+  uint32_t *to_key, *to_order;
+  int shift, bits;
+};
+__device__ __forceinline__ uint32_t pass_key(const SortArgs& a, const Pass& p, int64_t t) {
+  return p.key ? p.key[t] : key_at(a, t);
+}
+__global__ __launch_bounds__(kSortThreads) void embedding_count_kernel(SortArgs a, Pass p) {
+  __shared__ uint32_t count[kBins];
+  if ((int)blockIdx.x >= a.tiles) return clear_share(a, a.tiles);
+  const int bins = 1 << p.bits;
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * kTile, t1 = min(t0 + kTile, a.tokens);
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += kSortThreads)
+    atomicAdd(&count[(pass_key(a, p, t) >> p.shift) & (bins - 1)], 1u);  // (a count: its order does not matter)
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) a.hist[(int64_t)b * a.tiles + blockIdx.x] = count[b];
+}
+__global__ __launch_bounds__(kSortThreads) void embedding_scan_kernel(SortArgs a, Pass p) {
+  __shared__ uint32_t wave_total[kSortWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = ((int64_t)1 << p.bits) * a.tiles;
+  uint32_t base = 0;
+  for (int64_t i0 = 0; i0 < n; i0 += kSortThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const uint32_t v = i < n ? a.hist[i] : 0;
+    uint32_t upto = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += o;
+    }
+    if (lane == 63) wave_total[wave] = upto;
+    __syncthreads();
+    uint32_t before = base;
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (w < wave) before += wave_total[w];
+      base += wave_total[w];
+    }
+    if (i < n) a.hist[i] = before + upto - v;
+    __syncthreads();
+  }
+}
+__global__ __launch_bounds__(kSortThreads) void embedding_place_kernel(SortArgs a, Pass p) {
+  __shared__ SortShared s;
+  __shared__ uint32_t first_of[kBins];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bins = 1 << p.bits;
+  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  const int n = (int)min((int64_t)kTile, a.tokens - t0), mine = wave * 64 * kItems + lane;
+  uint32_t key[kItems], order[kItems], place[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const bool there = mine + 64 * i < n;
+    key[i] = there ? pass_key(a, p, t0 + mine + 64 * i) : 0xFFFFFFFFu;
+    order[i] = there && p.order ? p.order[t0 + mine + 64 * i] : (uint32_t)(t0 + mine + 64 * i);
+  }
+  digit_places(key, n, p.shift, p.bits, s, place, first_of);
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (mine + 64 * i < n) {
+      const uint32_t digit = (key[i] >> p.shift) & (bins - 1);
+      const uint32_t to = a.hist[(int64_t)digit * a.tiles + blockIdx.x] + place[i] - first_of[digit];
+      p.to_key[to] = key[i];
+      p.to_order[to] = order[i];
+    }
+}
+
+// ---------------------------------------------------------------- sums
+constexpr int kChunk = 32;  // sorted positions
+constexpr int kAhead = 8;   // rows in flight
+
+struct SumArgs {
+  const void* dout;
+  const uint32_t *key, *order;
+  int64_t tokens, vocab, d;
+  float scale;
+  bool accumulate;
+  float* dtable;
+  float* part;     // [chunks][2][d]: sums that reach past the chunk's first, its last position
+  int64_t chunks;
+  int cols;        // workgroups across a row
+  uint32_t first;
+};
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_sum(const SumArgs& a, uint32_t id, int col, int left, const float (&sum)[4]) {
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = sum[e] * a.scale;
+  const int64_t at = (int64_t)id * a.d + col;
+  if (a.accumulate) {
+    float was[4];
+    unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.dtable, at, left), was);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += was[e];
+  }
+  store_as<FP8_IN_FP32, WHOLE>(a.dtable, at, left, v);
+}
+
+// One chunk, 1024 columns a workgroup.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
+  const uint32_t g = a.first + blockIdx.x;
+  const int64_t chunk = g / (uint32_t)a.cols, p0 = chunk * kChunk;
+  const int col = ((int)(g % (uint32_t)a.cols) * 256 + threadIdx.x) * 4, left = (int)a.d - col;
+  const int n = (int)min((int64_t)kChunk, a.tokens - p0);
+  if (left <= 0) return;
+  const bool from_before = p0 > 0 && a.key[p0 - 1] == a.key[p0];
+  const bool to_after = p0 + n < a.tokens && a.key[p0 + n] == a.key[p0 + n - 1];
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  int begun = 0;  // position of the run's first row here
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    Raw<DT> raw[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      raw[i] = Raw<DT>{};
+      if (i0 + i < n && a.key[p0 + i0 + i] < (uint32_t)a.vocab)
+        raw[i] = load_raw<DT, WHOLE, true>(a.dout, (int64_t)a.order[p0 + i0 + i] * a.d + col, left);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int at = i0 + i;
+      if (at >= n) break;
+      const uint32_t id = a.key[p0 + at];
+      if (id >= (uint32_t)a.vocab) return;  // those left are no tokens
+      float v[4];
+      unpack<DT>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v[e];
+      const bool last = at + 1 == n;
+      if (!last && a.key[p0 + at + 1] == id) continue;
+      if (begun == 0 && from_before) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk) * a.d + col, left, sum);
+      else if (last && to_after) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk + 1) * a.d + col, left, sum);
+      else store_sum<WHOLE>(a, id, col, left, sum);
+      begun = at + 1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = 0.0f;
+    }
+  }
+}
+
+// Ids whose rows begin in one chunk and end in another: the chunks' sums in order.
+template <bool WHOLE>
+__global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs a) {
+  const uint32_t g = a.first + blockIdx.x;
+  const int64_t chunk = g / (uint32_t)a.cols, p0 = chunk * kChunk, p1 = p0 + kChunk;  // (not the last chunk)
+  const int col = ((int)(g % (uint32_t)a.cols) * 256 + threadIdx.x) * 4, left = (int)a.d - col;
+  const uint32_t id = a.key[p1 - 1];
+  if (left <= 0 || id >= (uint32_t)a.vocab || a.key[p1] != id) return;
+  if (p0 > 0 && a.key[p0 - 1] == id && a.key[p0] == id) return;  // begun in an earlier one
+  float sum[4];
+  unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, (2 * chunk + 1) * a.d + col, left), sum);
+  for (int64_t c = chunk + 1; c < a.chunks && a.key[c * kChunk] == id; ++c) {
+    float v[4];
+    unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, 2 * c * a.d + col, left), v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += v[e];
+  }
+  store_sum<WHOLE>(a, id, col, left, sum);
+}
+
+int64_t aligned(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
+struct GradPlan {
+  int64_t tiles, chunks;
+  int passes, bits;
+  int64_t key, order, key2, order2, hist, part, bytes;  // offsets
+};
+GradPlan plan_of(int64_t tokens, int64_t vocab, int64_t d) {
+  GradPlan p{};
+  p.tiles = (tokens + kTile - 1) / kTile;
+  p.chunks = (tokens + kChunk - 1) / kChunk;
+  int bits = 1;
+  while ((vocab >> bits) != 0) ++bits;  // keys 0 .. vocab
+  p.passes = (bits + kMaxDigit - 1) / kMaxDigit;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t r = at;
+    at += aligned(bytes);
+    return r;
+  };
+  p.key = take(4 * tokens);
+  p.order = take(4 * tokens);
+  if (p.tiles > 1) {
+    p.key2 = take(4 * tokens);
+    p.order2 = take(4 * tokens);
+    p.hist = take(4 * ((int64_t)1 << p.bits) * p.tiles);
+  }
+  p.part = take(8 * p.chunks * ((d + 3) & ~(int64_t)3));
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace
+
+hipError_t launch_embedding_fwd(const void* ids, bool wide, int64_t tokens, const void* table, int table_dtype,
+                                int64_t vocab, int64_t d, float scale, void* out, int out_dtype, hipStream_t stream) {
+  LookupArgs a{ids, wide, tokens, vocab, table, (int)d, (int)((d + 3) / 4), scale, out, 0};
+  const int64_t units = tokens * a.units;
+  auto run = [&](auto tt, auto ot, auto whole, auto u) {
+    constexpr int U = decltype(u)::value;
+    in_stretches((units + 256 * U - 1) / (256 * U), 256, [&](uint32_t first, uint32_t count) {
+      a.first = first;
+      hipLaunchKernelGGL((embedding_fwd_kernel<decltype(tt)::value, decltype(ot)::value, decltype(whole)::value, U>),
+                         dim3(count), dim3(256), 0, stream, a);
+    });
+  };
+  using std::integral_constant;
+  auto sized = [&](auto tt, auto ot, auto whole) {
+    if (units > 1024 * 1024) run(tt, ot, whole, integral_constant<int, 4>{});
+    else run(tt, ot, whole, integral_constant<int, 1>{});
+  };
+  auto typed = [&](auto tt, auto ot) {
+    if (d % 4 == 0) sized(tt, ot, std::true_type{});
+    else sized(tt, ot, std::false_type{});
+  };
+  constexpr integral_constant<int, FP8_IN_BF16> b16{};
+  constexpr integral_constant<int, FP8_IN_FP32> f32{};
+  if (table_dtype == FP8_IN_BF16) out_dtype == FP8_IN_BF16 ? typed(b16, b16) : typed(b16, f32);
+  else out_dtype == FP8_IN_BF16 ? typed(f32, b16) : typed(f32, f32);
+  return hipGetLastError();
+}
+
+int64_t embedding_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t d) {
+  return plan_of(tokens, vocab, d).bytes;
+}
+
+hipError_t launch_embedding_bwd(const EmbeddingGrad& g, void* ws, hipStream_t stream) {
+  const GradPlan p = plan_of(g.tokens, g.vocab, g.d);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(w + at); };
+  SortArgs s{};
+  s.ids = g.ids, s.wide = g.wide, s.tokens = g.tokens, s.vocab = g.vocab;
+  s.passes = p.passes, s.bits = p.bits, s.tiles = (int)p.tiles;
+  s.key = words(p.key), s.order = words(p.order);
+  s.key2 = words(p.key2), s.order2 = words(p.order2), s.hist = words(p.hist);
+  int clearing = 0;
+  if (!g.accumulate) {
+    s.zero = g.dtable;
+    s.zeros = g.vocab * g.d;
+    clearing = (int)std::min<int64_t>(1024, (s.zeros + 4 * kSortThreads - 1) / (4 * kSortThreads));
+  }
+  if (p.tiles <= 1) {
+    hipLaunchKernelGGL(embedding_sort_kernel, dim3(1 + clearing), dim3(kSortThreads), 0, stream, s);
+  } else {
+    Pass pass{nullptr, nullptr, nullptr, nullptr, 0, p.bits};
+    for (int i = 0; i < p.passes; ++i) {
+      const bool last_here = (p.passes - 1 - i) % 2 == 0;  // the last pass ends in key, order
+      pass.to_key = last_here ? s.key : s.key2;
+      pass.to_order = last_here ? s.order : s.order2;
+      pass.shift = i * p.bits;
+      hipLaunchKernelGGL(embedding_count_kernel, dim3((uint32_t)p.tiles + (i == 0 ? clearing : 0)), dim3(kSortThreads),
+                         0, stream, s, pass);
+      hipLaunchKernelGGL(embedding_scan_kernel, dim3(1), dim3(kSortThreads), 0, stream, s, pass);
+      hipLaunchKernelGGL(embedding_place_kernel, dim3((uint32_t)p.tiles), dim3(kSortThreads), 0, stream, s, pass);
+      pass.key = pass.to_key;
+      pass.order = pass.to_order;
+    }
+  }
+  SumArgs a{};
+  a.dout = g.dout, a.key = s.key, a.order = s.order;
+  a.tokens = g.tokens, a.vocab = g.vocab, a.d = g.d;
+  a.scale = g.scale, a.accumulate = g.accumulate, a.dtable = g.dtable;
+  a.part = reinterpret_cast<float*>(w + p.part);
+  a.chunks = p.chunks;
+  a.cols = (int)((g.d + 1023) / 1024);
+  auto launch = [&](auto kernel, int64_t groups) {
+    in_stretches(groups, 256, [&](uint32_t first, uint32_t count) {
+      a.first = first;
+      hipLaunchKernelGGL(kernel, dim3(count), dim3(256), 0, stream, a);
+    });
+  };
+  const bool whole = g.d % 4 == 0;
+  if (g.dout_dtype == FP8_IN_BF16)
+    launch(whole ? embedding_sum_kernel<FP8_IN_BF16, true> : embedding_sum_kernel<FP8_IN_BF16, false>,
+           p.chunks * a.cols);
+  else
+    launch(whole ? embedding_sum_kernel<FP8_IN_FP32, true> : embedding_sum_kernel<FP8_IN_FP32, false>,
+           p.chunks * a.cols);
+  launch(whole ? embedding_join_kernel<true> : embedding_join_kernel<false>, (p.chunks - 1) * a.cols);
+  return hipGetLastError();
+}
+
+}  // namespace fp8lin

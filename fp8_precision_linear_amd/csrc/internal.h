@@ -120,6 +120,45 @@ struct AttnProblem {
 int64_t kv_attention_workspace_bytes(const fp8_kv_cache_t& c, const fp8_kv_batch_t& b, int q_heads);
 hipError_t launch_kv_attention(const AttnProblem& p, void* ws, hipStream_t stream);
 
+// Norms of queries and keys with the rotation (qk_norm.hip).
+struct QkProblem {
+  const void* x;
+  int x_dtype;
+  int64_t x_stride, tokens;
+  int q_heads, kv_heads, head_dim;
+  const void *wq, *wk;  // both or neither
+  int w_dtype;
+  float eps;
+  const int32_t* positions;  // optional
+  const float *cos, *sin;    // both or neither
+  int rope_rows, rope_pairs;
+};
+struct QkGrads {
+  const uint16_t *dq, *dk, *dv;
+  int64_t dq_stride, dk_stride, dv_stride;
+  void* dx;
+  float *dwq, *dwk;
+};
+hipError_t launch_qk_norm_fwd(const QkProblem& p, uint16_t* y, hipStream_t stream);
+int64_t qk_norm_bwd_workspace_bytes(const QkProblem& p);
+hipError_t launch_qk_norm_bwd(const QkProblem& p, const QkGrads& g, float* ws, hipStream_t stream);
+
+// Embedding (embedding.hip).  ids: int32, or int64 where wide.
+hipError_t launch_embedding_fwd(const void* ids, bool wide, int64_t tokens, const void* table, int table_dtype,
+                                int64_t vocab, int64_t d, float scale, void* out, int out_dtype, hipStream_t stream);
+int64_t embedding_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t d);
+struct EmbeddingGrad {
+  const void* dout;
+  int dout_dtype;
+  const void* ids;
+  bool wide;
+  int64_t tokens, vocab, d;
+  float scale;
+  bool accumulate;
+  float* dtable;
+};
+hipError_t launch_embedding_bwd(const EmbeddingGrad& p, void* ws, hipStream_t stream);
+
 // Product arithmetic (the values of fp8_scaled_gemm's `math` argument).
 #define FP8LIN_MATH_EXACT FP8_GEMM_EXACT
 #define FP8LIN_MATH_NATIVE_FP8 FP8_GEMM_NATIVE_FP8
