@@ -14,7 +14,10 @@ the layer with current or delayed scaling) and ``fp8_precision_linear_amd.mlp``
 (the chained FP8 MLP with SwiGLU).  The operators around them:
 ``fp8_precision_linear_amd.norm`` (RMS norm with the residual's addition and
 FP8 output), ``fp8_precision_linear_amd.attention`` (the paged FP8 cache and
-attention over it), run together by ``fp8_precision_linear_amd.decoder``.
+attention over it), run together by ``fp8_precision_linear_amd.decoder``; and those
+that train: ``fp8_precision_linear_amd.embedding``, ``.qk_norm`` (norms of queries
+and keys with the rotation) and ``.self_attention`` (attention over packed
+sequences), run together by ``fp8_precision_linear_amd.block``.
 
 Importing this module loads the library and raises ImportError if it is not
 built; build it with ``python fp8_precision_linear_amd/build.py``.

@@ -118,6 +118,15 @@ class KVBatch:
         table = i32([list(t) + [-1] * (width - len(t)) for t in tables]).reshape(len(new), width)
         return cls(i32(cu), i32(list(lens)).reshape(-1), table, max([0, *new]), max([0, *lens]), cu[-1])
 
+    def positions(self):
+        """The position of each row of the packed tensors, int32 [tokens], from
+        what the device arrays hold now (rows behind the last sequence count on)."""
+        t = torch.arange(self.tokens, dtype=torch.int32, device=self.device)
+        if self.batch == 0:
+            return t
+        i = torch.searchsorted(self.cu_tokens[1:], t, right=True).clamp_(max=self.batch - 1)
+        return t + (self.lens - self.cu_tokens[1:])[i]
+
 
 def _opt(t):
     return 0 if t is None else t.data_ptr()

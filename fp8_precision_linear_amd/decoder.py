@@ -3,6 +3,7 @@ the cache, the attention and the gated MLP of this package run together.
 
     h  = x + residual                       rmsnorm_quantize -> codes
     q, k, v = h8 . wqkv^T                   scaled_gemm, float32
+    q, k <- norms of the heads, rotated     qk_norm_rope_fwd, where the layer has them
     q  <- rotated; k, v -> the FP8 cache    kv_append
     o  = attention(q, cache)                kv_attention, bf16
     a  = o8 . wo^T                          quantize, scaled_gemm
@@ -24,7 +25,9 @@ import torch
 
 from . import E4M3, OP_FWD, compute_bias, quantize, scale_cast, scaled_gemm_auto, swiglu_fwd
 from .attention import KVBatch, KVCache, kv_append, kv_attention
+from .embedding import embedding_fwd
 from .norm import rmsnorm_fwd, rmsnorm_quantize
+from .qk_norm import qk_norm_rope_fwd
 
 
 def rope_tables(positions, head_dim, base=10000.0, device="cuda"):
@@ -36,9 +39,11 @@ def rope_tables(positions, head_dim, base=10000.0, device="cuda"):
 
 class FP8DecoderLayer:
     """Weights: wqkv [(q_heads + 2 kv_heads) head_dim, d], wo [d, q_heads
-    head_dim], w_gate_up [2f, d], w_down [d, f]; norm weights [d]."""
+    head_dim], w_gate_up [2f, d], w_down [d, f]; norm weights [d].  q_norm, k_norm
+    [head_dim], both or neither: the norms of queries and keys."""
 
-    def __init__(self, norm_attn, wqkv, wo, norm_mlp, w_gate_up, w_down, q_heads, kv_heads, head_dim, eps=1e-5):
+    def __init__(self, norm_attn, wqkv, wo, norm_mlp, w_gate_up, w_down, q_heads, kv_heads, head_dim, eps=1e-5,
+                 q_norm=None, k_norm=None):
         d = norm_attn.shape[0]
         if wqkv.shape != ((q_heads + 2 * kv_heads) * head_dim, d) or wo.shape != (d, q_heads * head_dim):
             raise ValueError(f"wqkv {tuple(wqkv.shape)} and wo {tuple(wo.shape)} do not fit {q_heads} + 2 * {kv_heads} "
@@ -47,6 +52,9 @@ class FP8DecoderLayer:
             raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not chain")
         self.q_heads, self.kv_heads, self.head_dim, self.eps = q_heads, kv_heads, head_dim, eps
         self.norm_attn, self.norm_mlp = norm_attn, norm_mlp
+        if (q_norm is None) != (k_norm is None):
+            raise ValueError("norm weights for both queries and keys, or for neither")
+        self.q_norm, self.k_norm = q_norm, k_norm
         # codes and biases, made once
         self.wqkv, self.wo, self.w_gate_up, self.w_down = (
             quantize(w.contiguous(), E4M3)[:2] for w in (wqkv, wo, w_gate_up, w_down))
@@ -61,14 +69,29 @@ class FP8DecoderLayer:
     def cache(self, num_blocks, block_size=64, fmt=E4M3, device="cuda"):
         return KVCache(num_blocks, self.kv_heads, self.head_dim, block_size, fmt, device)
 
+    @classmethod
+    def from_block(cls, block):
+        """The layer that serves what block.FP8Block trained."""
+        w = lambda t: None if t is None else t.detach()  # noqa: E731
+        return cls(w(block.attn_in.norm_weight), w(block.attn_in.weight), w(block.attn_out.weight), w(block.norm_mlp),
+                   w(block.mlp.w1), w(block.mlp.w2), block.q_heads, block.kv_heads, block.head_dim, block.eps,
+                   w(block.q_norm), w(block.k_norm))
+
     @torch.no_grad()
-    def forward(self, x, residual, cache, batch, rope, window=0):
+    def forward(self, x, residual, cache, batch, rope, window=0, positions=None):
         """(x, h) for the next layer; x [tokens, d] float32 or bf16, residual
-        [tokens, d] bf16 or None (the first layer: x is the residual stream)."""
+        [tokens, d] bf16 or None (the first layer: x is the residual stream).
+        positions: batch.positions(), made here if None; a layer with norms of
+        queries and keys asks for it."""
         T, Hq, H, D = batch.tokens, self.q_heads, self.kv_heads, self.head_dim
         n8, bn, _, h, _ = rmsnorm_quantize(x, self.norm_attn, E4M3, residual=residual, eps=self.eps)
         qkv = scaled_gemm_auto(OP_FWD, n8, E4M3, bn, self.wqkv[0], E4M3, self.wqkv[1]).view(T, Hq + 2 * H, D)
-        q = kv_append(cache, batch, qkv[:, Hq:Hq + H], qkv[:, Hq + H:], q=qkv[:, :Hq], rope=rope)
+        if self.q_norm is None:
+            q = kv_append(cache, batch, qkv[:, Hq:Hq + H], qkv[:, Hq + H:], q=qkv[:, :Hq], rope=rope)
+        else:
+            positions = batch.positions() if positions is None else positions
+            q, k, v = qk_norm_rope_fwd(qkv, Hq, H, self.q_norm, self.k_norm, self.eps, rope, positions)
+            kv_append(cache, batch, k, v)
         o = kv_attention(cache, batch, q, window=window).view(T, Hq * D)
         o8, bo, _ = quantize(o, E4M3)
         a = scaled_gemm_auto(OP_FWD, o8, E4M3, bo, self.wo[0], E4M3, self.wo[1])
@@ -84,23 +107,32 @@ class FP8DecoderLayer:
 
 
 class FP8Decoder:
-    """Layers and their caches over one block table, with a final norm."""
+    """Layers and their caches over one block table, with a final norm.
+    embedding: optional [vocab, d] table; forward then also takes token ids."""
 
-    def __init__(self, layers, norm_weight, num_blocks, positions, block_size=64, fmt=E4M3, eps=1e-5):
+    def __init__(self, layers, norm_weight, num_blocks, positions, block_size=64, fmt=E4M3, eps=1e-5, embedding=None,
+                 embed_scale=1.0):
         self.layers, self.norm_weight, self.eps = list(layers), norm_weight, eps
         dev = norm_weight.device
         self.caches = [l.cache(num_blocks, block_size, fmt, dev) for l in self.layers]
         self.block_size = block_size
         self.rope = rope_tables(positions, self.layers[0].head_dim, device=dev)
+        self.embedding, self.embed_scale = embedding, embed_scale
 
     @torch.no_grad()
     def forward(self, x, batch):
         """Final hidden states [tokens, d] bf16 of the batch's new tokens, whose
-        embeddings are x [tokens, d] bf16; the caches receive their keys and
-        values."""
+        embeddings are x [tokens, d] bf16, or whose ids are x [tokens] int32 or
+        int64; the caches receive their keys and values."""
+        if x.dim() == 1:
+            if self.embedding is None:
+                raise ValueError("token ids for a decoder without an embedding")
+            x = embedding_fwd(x, self.embedding, self.embed_scale)
         h = None
+        normed = any(getattr(l, "q_norm", None) is not None for l in self.layers)
+        more = {"positions": batch.positions()} if normed else {}   # made once for all of them
         for layer, cache in zip(self.layers, self.caches):
-            x, h = layer(x, h, cache, batch, self.rope)
+            x, h = layer(x, h, cache, batch, self.rope, **more)
         return rmsnorm_fwd(x, self.norm_weight, residual=h, eps=self.eps)[0]
 
     __call__ = forward

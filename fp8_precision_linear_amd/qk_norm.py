@@ -124,12 +124,24 @@ def qk_norm_rope_bwd(dq, dk, dv, qkv, wq=None, wk=None, eps=1e-5, rope=None, pos
     return out, dwq, dwk
 
 
+def _packed(t):
+    """t, or a copy whose rows the kernels can read: heads side by side, rows
+    that do not overlap, on 16-byte boundaries."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        row, head, one = t.stride()
+        n, d = t.shape[1:]
+        if one != 1 or head != d or row < n * d or row * t.element_size() % 16 or t.data_ptr() % 16:
+            return t.contiguous()
+    return t
+
+
 class QKNormRopeFunction(torch.autograd.Function):
     """(q, k, v) of qk_norm_rope_fwd; gradients for qkv and the weights."""
 
     @staticmethod
     def forward(ctx, qkv, wq, wk, q_heads, kv_heads, eps, rope, positions, rope_pairs):
         cos, sin = (None, None) if rope is None else rope
+        qkv, wq, wk = _packed(qkv), *(None if w is None else w.contiguous() for w in (wq, wk))
         ctx.save_for_backward(qkv, wq, wk, cos, sin, positions)
         ctx.heads, ctx.eps, ctx.rope_pairs = (q_heads, kv_heads), eps, rope_pairs
         return qk_norm_rope_fwd(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs)
@@ -138,7 +150,7 @@ class QKNormRopeFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq, dk, dv):
         qkv, wq, wk, cos, sin, positions = ctx.saved_tensors
-        dx, dwq, dwk = qk_norm_rope_bwd(dq.contiguous(), dk.contiguous(), dv.contiguous(), qkv, wq, wk, ctx.eps,
+        dx, dwq, dwk = qk_norm_rope_bwd(_packed(dq), _packed(dk), _packed(dv), qkv, wq, wk, ctx.eps,
                                         None if cos is None else (cos, sin), positions, ctx.rope_pairs)
         if wq is not None:
             dwq, dwk = dwq.to(wq.dtype), dwk.to(wk.dtype)
@@ -146,5 +158,5 @@ class QKNormRopeFunction(torch.autograd.Function):
 
 
 def qk_norm_rope(qkv, q_heads, kv_heads, wq=None, wk=None, eps=1e-5, rope=None, positions=None, rope_pairs=False):
-    """qk_norm_rope_fwd with gradients."""
+    """qk_norm_rope_fwd with gradients.  qkv of any strides."""
     return QKNormRopeFunction.apply(qkv, wq, wk, q_heads, kv_heads, eps, rope, positions, rope_pairs)

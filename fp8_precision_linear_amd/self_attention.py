@@ -31,10 +31,10 @@ class Sequences:
     """Sequences packed one behind the other: cu_tokens [batch + 1] int32 on the
     device, sequence i in rows cu_tokens[i] .. cu_tokens[i + 1] - 1.  max_len
     bounds their lengths, `tokens` is the packed tensors' row count (the host's
-    numbers: the device array is not read here).  positions: int32 [tokens], each
-    row's place in its sequence, where it was built from lists; else None."""
+    numbers: the device array is not read here).  whole: every row belongs to a
+    sequence; otherwise the autograd function clears the rows that may not."""
 
-    def __init__(self, cu_tokens, max_len, tokens, positions=None):
+    def __init__(self, cu_tokens, max_len, tokens, whole=False):
         _need_kind(cu_tokens, "cu_tokens", torch.int32)
         if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1:
             raise ValueError(f"cu_tokens must be [batch + 1], got {tuple(cu_tokens.shape)}")
@@ -42,9 +42,7 @@ class Sequences:
         for v, name, most in ((max_len, "max_len", 1 << 30), (tokens, "tokens", (1 << 31) - 1)):
             if not 0 <= int(v) <= most:
                 raise ValueError(f"{name} is out of range: {v}")
-        if positions is not None:
-            _need(positions, "positions", torch.int32, cu_tokens.device, shape=(int(tokens),))
-        self.cu_tokens, self.positions = cu_tokens, positions
+        self.cu_tokens, self.whole = cu_tokens, bool(whole)
         self.batch, self.tokens, self.max_len = cu_tokens.shape[0] - 1, int(tokens), int(max_len)
         self.device = cu_tokens.device
         self._struct = _SeqsStruct(cu_tokens.data_ptr(), self.batch, self.tokens, self.max_len, 0)
@@ -61,10 +59,16 @@ class Sequences:
             cu.append(cu[-1] + n)
         if cu[-1] >= 1 << 31:
             raise ValueError(f"{cu[-1]} tokens: fewer than 2^31 are wanted")
-        cu = torch.tensor(cu, dtype=torch.int32)
-        start = cu[:-1].repeat_interleave(torch.tensor(lens, dtype=torch.int64))
-        pos = torch.arange(int(cu[-1]), dtype=torch.int32) - start
-        return cls(cu.to(device), max([0, *lens]), int(cu[-1]), pos.to(device))
+        return cls(torch.tensor(cu, dtype=torch.int32).to(device), max([0, *lens]), cu[-1], whole=True)
+
+    def positions(self):
+        """Each row's place in its sequence, int32 [tokens], from what cu_tokens
+        holds now (rows behind the last sequence count on)."""
+        t = torch.arange(self.tokens, dtype=torch.int32, device=self.device)
+        if self.batch == 0:
+            return t
+        i = torch.searchsorted(self.cu_tokens[1:], t, right=True).clamp_(max=self.batch - 1)
+        return t - self.cu_tokens[i]
 
 
 def _rows(t, name, seqs, heads, d, dev):
@@ -158,7 +162,12 @@ class AttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, seqs, scale, causal, window):
-        out, lse = attention_fwd(q, k, v, seqs, scale, causal, window)
+        q, k, v = (_packed(t) for t in (q, k, v))
+        out = lse = None
+        if not seqs.whole and isinstance(q, torch.Tensor):   # rows of no sequence: zeros
+            out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+            lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+        out, lse = attention_fwd(q, k, v, seqs, scale, causal, window, out, lse)
         ctx.save_for_backward(q, k, v, out, lse)
         ctx.call = (seqs, scale, causal, window)
         return out
@@ -167,9 +176,22 @@ class AttentionFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
-        return (*attention_bwd(dout.contiguous(), q, k, v, out, lse, *ctx.call), None, None, None, None)
+        new = torch.empty if ctx.call[0].whole else torch.zeros
+        grads = [new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        return (*attention_bwd(_packed(dout), q, k, v, out, lse, *ctx.call, *grads), None, None, None, None)
+
+
+def _packed(t):
+    """t, or a copy whose rows the kernels can read: heads side by side, rows
+    that do not overlap, on 16-byte boundaries."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        row, head, one = t.stride()
+        n, d = t.shape[1:]
+        if one != 1 or head != d or row % 8 or not n * d <= row <= MAX_STRIDE or t.data_ptr() % 16:
+            return t.contiguous()
+    return t
 
 
 def attention(q, k, v, seqs, scale=None, causal=True, window=0):
-    """attention_fwd's out, with gradients."""
+    """attention_fwd's out, with gradients.  Tensors of any strides."""
     return AttentionFunction.apply(q, k, v, seqs, scale, causal, window)
