@@ -155,6 +155,11 @@ int seqs_checks(const fp8_seqs_t* s, int32_t q_heads, int32_t kv_heads, int32_t 
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return FP8_ERR_SIZE;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP8_ERR_SIZE;
   if ((int64_t)q_heads * head_dim > kMaxRowStride) return FP8_ERR_SIZE;
+  // workgroups are counted in 32 bits: three kinds of them in the backward pass
+  const int64_t longest = s->max_len < s->tokens ? s->max_len : s->tokens;
+  if ((longest + 127) / 128 * s->batch > (int64_t)0x7FFFFFFF / (3 * (int64_t)q_heads) ||
+      s->tokens > (int64_t)0x7FFFFFFF / q_heads)
+    return FP8_ERR_SIZE;
   if (s->batch == 0 || s->tokens == 0 || s->max_len == 0) return FP8_OK;  // nothing to do
   if (!s->cu_tokens) return FP8_ERR_NULL;
   if (misaligned_word(s->cu_tokens)) return FP8_ERR_ALIGN;

@@ -23,6 +23,12 @@
 
 namespace fp8lin {
 
+// A key tile: its walk's start on the head's line, its sequence and first key.
+struct SeqLine {
+  int64_t start;
+  int seq, k0;
+};
+
 struct SeqAttnArgs {
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
@@ -41,9 +47,11 @@ struct SeqAttnArgs {
   int64_t dout_stride, dq_stride, dk_stride, dv_stride;
   uint16_t *dq, *dk, *dv;
   float *lse2, *delta;  // [q_heads][tokens], lse * log2(e) and rowsum(dout * out)
-  float *part_k, *part_v;  // [splits][tokens][heads][D], where dk and dv are split
-  int chunk;   // query tiles (over the heads of the group) of a chunk
-  int splits;  // most chunks of any key tile
+  float *part_k, *part_v;  // [key heads * shares][2][kSeqRows][D]: sums of walks that are cut
+  SeqLine *line, *line_end;  // key tiles of a head; their walks' length, and their number in `seq`
+  int most_tiles;  // of `line`
+  int shares;      // of a head's line, or 0: a workgroup takes a key tile
+  uint32_t dkv_groups;  // workgroups of dk and dv, each
 };
 
 namespace {
@@ -197,13 +205,6 @@ __device__ __forceinline__ int result_row(int e, int h) { return 8 * (e >> 2) + 
 
 // NaN for an infinite value (include/fp8lin_train.h).
 __device__ __forceinline__ float finite_or_nan(float v) { return v + (v - v); }
-
-// Workgroup x's head, sequence and tile.  Workgroups a multiple of the key heads
-// apart read the same keys, and so do those that one XCD gets where the key
-// heads are a multiple of 8.
-struct SeqPlace {
-  int head, seq, tile;
-};
 
 }  // namespace
 

@@ -1,18 +1,23 @@
 // Attention over packed sequences, backward: seq_attn.h has the mathematics.
 //
 // Probabilities are recomputed from q, k and lse, so nothing of the size of the
-// logits is stored.  Two kernels, each the owner of what it sums, so that no sum
-// depends on an order of atomics: seven products where one kernel that adds dq
-// from every key tile would need five.
+// logits is stored.  Two kinds of workgroups, each the owner of what it sums, so
+// that no sum depends on an order of atomics: seven products where a kernel that
+// adds dq from every key tile would need five.
 //
 // dq.  As the forward: 128 query rows of one head a workgroup, 32 a wave, q and
-// dout in registers; keys and values through LDS.  It runs first and leaves, for
-// each row, -lse log2(e) and -delta for the other kernel.
+// dout in registers; keys and values through LDS.
 //
-// dk, dv.  128 keys of a key head a workgroup, 32 a wave, k and v in registers;
-// the queries and dout of all its heads through LDS.  Where the key tiles are
-// too few to fill the chip, a tile's walk over the queries is cut into chunks
-// whose partial sums a third kernel joins in order.
+// dk, dv.  128 keys of a key head at a time, 32 a wave, k and v in registers;
+// the queries and dout of all its heads through LDS.  A workgroup takes a key
+// tile where there are enough of them.  Otherwise -- few key heads, short
+// batches -- the tiles' walks over the queries, of very different lengths under a
+// causal mask, are laid one behind the other for each key head and cut into
+// equal shares, one for each workgroup that runs at the same time; a cut walk's
+// partial sums are joined in order by a last kernel.
+//
+// Both kinds run in one launch, behind a small one that leaves -lse log2(e) and
+// -delta of every row and head.
 #include <algorithm>
 
 #include "seq_attn.h"
@@ -20,38 +25,125 @@
 namespace fp8lin {
 namespace {
 
-// What a row's gradients are formed from; NaN where the forward's results are
-// not finite, which makes everything that the row sees NaN.
-struct RowStat {
-  float minus_lse2, minus_delta;
+// Query rows of a tile of the dk, dv kernel.
+template <int D>
+constexpr int kQueriesOf = D == 256 ? 32 : 64;
+
+// A key tile's walk: tiles of query rows from `lo` on, of each head of the group.
+struct Walk {
+  int lo, tiles;
 };
-__device__ __forceinline__ RowStat row_stat(float lse, float delta) {
-  const bool fine = lse - lse == 0.0f && delta - delta == 0.0f;
-  return {fine ? lse * -1.44269504088896340736f : NAN, -delta};
+template <int D>
+__device__ __forceinline__ Walk walk_of(const SeqAttnArgs& a, int n, int k0) {
+  constexpr int kQueries = kQueriesOf<D>;
+  const int lo = a.causal ? k0 : 0;
+  const int64_t hi = a.window ? (int64_t)min(k0 + kSeqRows, n) - 1 + a.window : n;
+  return {lo, ((int)min((int64_t)n, hi) - lo + kQueries - 1) / kQueries};
 }
 
+// The line of all key tiles of a head: where each one's walk starts on it, in
+// query tiles.  Written by one workgroup, a sequence a lane, sequences in order.
 template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqAttnArgs a) {
-  constexpr int J = D / 16, DT = D / 32, kKeys = D == 256 ? 32 : 64;
+__device__ void write_line(const SeqAttnArgs& a) {
+  __shared__ int64_t part[4][2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t tiles0 = 0, its0 = 0;
+  for (int i0 = 0; i0 < a.batch; i0 += 256) {
+    const int i = i0 + threadIdx.x;
+    int n = 0;
+    if (i < a.batch) {
+      const int first = max(0, min(a.cu[i], a.tokens));
+      n = min(max(first, min(a.cu[i + 1], a.tokens)) - first, a.max_len);
+    }
+    int64_t its = 0;
+    for (int k0 = 0; k0 < n; k0 += kSeqRows) its += (int64_t)walk_of<D>(a, n, k0).tiles * a.group;
+    int64_t t = (n + kSeqRows - 1) / kSeqRows, w = its;
+    const int64_t my_tiles = t;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t ot = __shfl_up(t, off, 64), ow = __shfl_up(w, off, 64);
+      if (lane >= off) t += ot, w += ow;
+    }
+    __syncthreads();  // the chunk before is done with `part`
+    if (lane == 63) part[wave][0] = t, part[wave][1] = w;
+    __syncthreads();
+    int64_t at = tiles0 + t - my_tiles, start = its0 + w - its;
+    for (int v = 0; v < 4; ++v) {
+      if (v < wave) at += part[v][0], start += part[v][1];
+      tiles0 += part[v][0];
+      its0 += part[v][1];
+    }
+    for (int k0 = 0; k0 < n; k0 += kSeqRows, ++at) {
+      if (at >= a.most_tiles) break;  // (overlapping sequences: past what there is room for)
+      a.line[at] = {start, i, k0};
+      start += (int64_t)walk_of<D>(a, n, k0).tiles * a.group;
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.line_end->start = its0;
+    a.line_end->seq = (int)min(tiles0, (int64_t)a.most_tiles);
+  }
+}
+
+// Share j of a line of `total` query tiles: from here to share j + 1's.
+__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int64_t j) { return total * j / shares; }
+
+// What a row's gradients are formed from: -lse log2(e), or NaN where the forward's
+// results are not finite, which makes everything that the row sees NaN, and
+// -delta.  D / 8 lanes a row; one more workgroup writes the line of key tiles.
+template <int D>
+__global__ __launch_bounds__(256) void seq_attn_stats_kernel(SeqAttnArgs a) {
+  constexpr int kLanes = D / 8;
+  uint32_t x = a.first + blockIdx.x;
+  if (a.shares > 0 && x-- == 0) return write_line<D>(a);
+  const int64_t i = (int64_t)x * (256 / kLanes) + threadIdx.x / kLanes, token = i / a.q_heads;
+  if (token >= a.tokens) return;
+  const int head = (int)(i - token * a.q_heads), d = 8 * (threadIdx.x % kLanes);
+  const v8b g = *reinterpret_cast<const v8b*>(a.dout + token * a.dout_stride + head * D + d);
+  const v8b o = *reinterpret_cast<const v8b*>(a.out + i * D + d);
+  float delta = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) delta = fmaf((float)g[e], (float)o[e], delta);
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) delta += __shfl_xor(delta, off, 64);
+  if (d != 0) return;
+  const float lse = a.lse[i];
+  const bool fine = lse - lse == 0.0f && delta - delta == 0.0f;
+  const int64_t to = head * (int64_t)a.tokens + token;
+  a.lse2[to] = fine ? lse * -1.44269504088896340736f : NAN;
+  a.delta[to] = -delta;
+}
+
+// LDS of a workgroup.
+template <int D>
+struct GradShared {
+  static constexpr int kRows = kQueriesOf<D>;  // of a tile, for either kind
+  __attribute__((aligned(1024))) uint8_t ring[2][2][kRows * D * 2];  // [buffer][keys, values or queries, dout]
+  __attribute__((aligned(16))) float stats[2][2][64];                // [buffer][-lse2, -delta]
+  int bad_key[kRows];
+  int found[4];
+};
+
+template <int D>
+__device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& lds, uint32_t x) {
+  constexpr int J = D / 16, DT = D / 32, kKeys = GradShared<D>::kRows;
   using Load = TileLoad<D, kKeys>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][Load::kBytes];  // [buffer][keys, values]
-  __shared__ int found[4];
-  __shared__ int bad_key[kKeys];
+  int* const found = lds.found;
+  int* const bad_key = lds.bad_key;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r32 = lane & 31, h = lane >> 5;
-  uint32_t x = a.first + blockIdx.x;
   const int kv_head = x % a.heads;
   x /= a.heads;
   const int head = kv_head * a.group + x % a.group;
   x /= a.group;
   const Seq s = seq_of(a, x % a.batch);
-  const int row0 = (a.tiles - 1 - (int)(x / a.batch)) * kSeqRows;
+  const int row0 = (a.tiles - 1 - (int)(x / a.batch)) * kSeqRows;  // late rows see most: first
   if (row0 >= s.n) return;
   const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
   const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
 
-  const uint32_t ring0 = lds_addr(ring);
+  const uint32_t ring0 = lds_addr(lds.ring);
   const int64_t ks = a.k_stride * 2, vs = a.v_stride * 2;
   const Load load_k(lane, wave, (uint32_t)ks), load_v(lane, wave, (uint32_t)vs);
   const uint16_t* kp = a.k + (int64_t)(s.first + klo) * a.k_stride + kv_head * D;
@@ -61,12 +153,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqA
     load_v.issue(vp + (int64_t)(T - klo) * a.v_stride, vs, s.n - T, ring0 + (2 * buf + 1) * Load::kBytes, wave);
   };
 
+  issue(klo, 0);
+
   const int wrow = row0 + 32 * wave, row = wrow + r32;
   v8b q[J], g[J];
-  float delta = 0.0f;
 #pragma unroll
   for (int j = 0; j < J; ++j) q[j] = g[j] = v8b{};
-  const int64_t cell = (int64_t)(s.first + min(row, s.n - 1)) * a.q_heads + head;
   if (row < s.n) {
     const uint16_t* qp = a.q + (int64_t)(s.first + row) * a.q_stride + head * D + 8 * h;
     const uint16_t* gp = a.dout + (int64_t)(s.first + row) * a.dout_stride + head * D + 8 * h;
@@ -74,19 +166,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqA
     for (int j = 0; j < J; ++j) {
       q[j] = *reinterpret_cast<const v8b*>(qp + 16 * j);
       g[j] = *reinterpret_cast<const v8b*>(gp + 16 * j);
-      const v8b o = *reinterpret_cast<const v8b*>(a.out + cell * D + 8 * h + 16 * j);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) delta = fmaf((float)g[j][e], (float)o[e], delta);
     }
   }
-  delta = swap32_sum(delta);
-  const RowStat stat = row_stat(a.lse[cell], delta);
-  if (row < s.n && h == 0) {
-    const int64_t at = (int64_t)head * a.tokens + s.first + row;
-    a.lse2[at] = stat.minus_lse2;
-    a.delta[at] = stat.minus_delta;
-  }
-  issue(klo, 0);
+  const int64_t stat = (int64_t)head * a.tokens + s.first + min(row, s.n - 1);
+  const float minus_lse2 = a.lse2[stat], minus_delta = a.delta[stat];
 
   const int hi = a.causal ? min(row + 1, s.n) : s.n, lo = a.window ? row - a.window + 1 : 0;
   const int whi = wrow >= s.n ? 0 : (a.causal ? min(wrow + 32, s.n) : s.n);
@@ -103,7 +186,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqA
   auto consume = [&](bool masked, bool any_bad, int K, uint32_t keys, uint32_t values, int slot) {
     v16f t = zero16(), dp;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dp[e] = stat.minus_delta;
+    for (int e = 0; e < 16; ++e) dp[e] = minus_delta;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       t = mma(lds_row((keys + by_row) ^ (32 * j)), q[j], t);
@@ -117,7 +200,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqA
     }
     v16f ds;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ds[e] = __builtin_amdgcn_exp2f(fmaf(t[e], a.scale_log2, stat.minus_lse2)) * dp[e];
+    for (int e = 0; e < 16; ++e) ds[e] = __builtin_amdgcn_exp2f(fmaf(t[e], a.scale_log2, minus_lse2)) * dp[e];
     if (masked) {
       asm volatile("");
 #pragma unroll
@@ -170,207 +253,252 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dq_kernel(SeqA
                      pack_bf16(dq[d][4 * u + 2] * a.scale, dq[d][4 * u + 3] * a.scale));
 }
 
-// Query rows of a tile of the dk, dv kernel.
-template <int D>
-constexpr int kQueriesOf = D == 256 ? 32 : 64;
-
-// A key tile's walk: tiles of query rows [lo, hi) of each head of the group.
-struct Walk {
-  int lo, tiles, chunks;
-};
-template <int D>
-__device__ __forceinline__ Walk walk_of(const SeqAttnArgs& a, const Seq& s, int k0) {
-  constexpr int kQueries = kQueriesOf<D>;
-  Walk w;
-  w.lo = a.causal ? k0 : 0;
-  const int64_t hi = a.window ? (int64_t)min(k0 + kSeqRows, s.n) - 1 + a.window : s.n;
-  w.tiles = ((int)min((int64_t)s.n, hi) - w.lo + kQueries - 1) / kQueries;
-  w.chunks = (int)(((int64_t)w.tiles * a.group + a.chunk - 1) / a.chunk);
-  return w;
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int64_t scalar(int64_t v) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
-template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_dkv_kernel(SeqAttnArgs a) {
+// Which of the two sums a workgroup forms.  With heads of 256 one: the two sums
+// alone would fill the registers (spilled, 2000 tokens of 16 heads on 4 took 1100
+// us; two kinds of workgroups, which form p twice, 420).
+constexpr int kDk = 1, kDv = 2;
+
+// x: the workgroup among those of its kind.
+template <int D, int SUMS>
+__device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& lds, uint32_t x) {
   constexpr int J = D / 16, DT = D / 32, kQueries = kQueriesOf<D>;
+  constexpr bool kWantK = (SUMS & kDk) != 0, kWantV = (SUMS & kDv) != 0;
   using Load = TileLoad<D, kQueries>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][Load::kBytes];  // [buffer][queries, dout]
-  __shared__ __attribute__((aligned(1024))) float stats[2][2][64];             // [buffer][-lse2, -delta]
-  __shared__ int found[4];
+  int* const found = lds.found;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r32 = lane & 31, h = lane >> 5;
-  uint32_t x = a.first + blockIdx.x;
-  const int kv_head = x % a.heads;
-  x /= a.heads;
-  const int split = x % a.splits;
-  x /= a.splits;
-  const Seq s = seq_of(a, x % a.batch);
-  const int k0 = (int)(x / a.batch) * kSeqRows;  // early keys are seen most: first
-  if (k0 >= s.n) return;
-  const Walk walk = walk_of<D>(a, s, k0);
-  if (split >= walk.chunks) return;
-  const int it0 = split * a.chunk, its = (int)min((int64_t)a.chunk, (int64_t)walk.tiles * a.group - it0);
-
-  const int wkey = k0 + 32 * wave, key = wkey + r32;
-  v8b k[J], v[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) k[j] = v[j] = v8b{};
-  if (key < s.n) {
-    const uint16_t* kp = a.k + (int64_t)(s.first + key) * a.k_stride + kv_head * D + 8 * h;
-    const uint16_t* vp = a.v + (int64_t)(s.first + key) * a.v_stride + kv_head * D + 8 * h;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      k[j] = *reinterpret_cast<const v8b*>(kp + 16 * j);
-      v[j] = *reinterpret_cast<const v8b*>(vp + 16 * j);
+  const int kv_head = x % a.heads, place = x / a.heads;
+  // a share of the head's line, or one key tile
+  int64_t pos = 0, end = 1;
+  int at = 0, key_tiles = 1;
+  if (a.shares > 0) {
+    const int64_t total = scalar(a.line_end->start);
+    pos = share_start(total, a.shares, place);
+    end = share_start(total, a.shares, place + 1);
+    if (pos >= end) return;
+    key_tiles = __builtin_amdgcn_readfirstlane(a.line_end->seq);
+    at = -1;  // the key tile that the share begins in: the last that starts at or before it
+    for (int i0 = 0; i0 < key_tiles; i0 += 256) {
+      const int i = i0 + (int)threadIdx.x;
+      at += __syncthreads_count(i < key_tiles && a.line[min(i, key_tiles - 1)].start <= pos);
     }
+    at = __builtin_amdgcn_readfirstlane(at);
   }
-  // the queries that see the lane's key
-  const int lo = a.causal ? key : 0;
-  const int hi = a.window ? (int)min((int64_t)s.n, (int64_t)key + a.window) : s.n;
 
-  v16f dk[DT], dv[DT];
-#pragma unroll
-  for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zero16();
-
-  const uint32_t ring0 = lds_addr(ring), stats0 = lds_addr(stats);
+  const uint32_t ring0 = lds_addr(lds.ring), stats0 = lds_addr(lds.stats);
   const int64_t qs = a.q_stride * 2, gs = a.dout_stride * 2;
   const Load load_q(lane, wave, (uint32_t)qs), load_g(lane, wave, (uint32_t)gs);
-  auto issue = [&](int group, int t, int buf) {
-    const int head = kv_head * a.group + group, T = walk.lo + t * kQueries, left = s.n - T;
-    const int64_t token = s.first + T;
-    load_q.issue(a.q + token * a.q_stride + head * D, qs, left, ring0 + buf * 2 * Load::kBytes, wave);
-    load_g.issue(a.dout + token * a.dout_stride + head * D, gs, left, ring0 + (2 * buf + 1) * Load::kBytes, wave);
-    // every wave brings all of the rows' statistics: the same words to the same place
-    const int64_t at = (int64_t)head * a.tokens + token + min(lane, left - 1);
-    dma4(a.lse2 + at, stats0 + buf * 512);
-    dma4(a.delta + at, stats0 + buf * 512 + 256);
-  };
   const uint32_t by_row = row_place<D>(lane), by_column = column_place<D>(lane);
 
-  // 32 query rows from Q on, in LDS at `queries` and `grads`
-  auto consume = [&](bool masked, int Q, uint32_t queries, uint32_t grads, const float* stat) {
-    v16f t = zero16(), dp;
+  for (; pos < end && at < key_tiles; ++at) {
+    SeqLine tile = {0, place % a.batch, place / a.batch * kSeqRows};  // early keys are seen most: first
+    if (a.shares > 0) tile = a.line[at];
+    const Seq s = seq_of(a, __builtin_amdgcn_readfirstlane(tile.seq));
+    const int k0 = __builtin_amdgcn_readfirstlane(tile.k0);
+    if (k0 >= s.n) return;  // (not one of a line)
+    const Walk walk = walk_of<D>(a, s.n, k0);
+    // (a walk has fewer than 2^31 tiles: at most 2^30 / 32 for each head)
+    const int64_t start = scalar(tile.start);
+    const int64_t length = (int64_t)walk.tiles * a.group, begin = pos - start;
+    const int64_t stop = a.shares > 0 ? min(length, end - start) : length, its = stop - begin;
+    pos = start + stop;
+
+    const int wkey = k0 + 32 * wave, key = wkey + r32;
+    v8b k[J], v[J];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const v4f w = *reinterpret_cast<const v4f*>(stat + 64 + 8 * u + 4 * h);
+    for (int j = 0; j < J; ++j) k[j] = v[j] = v8b{};
+    if (key < s.n) {
+      const uint16_t* kp = a.k + (int64_t)(s.first + key) * a.k_stride + kv_head * D + 8 * h;
+      const uint16_t* vp = a.v + (int64_t)(s.first + key) * a.v_stride + kv_head * D + 8 * h;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dp[4 * u + e] = w[e];
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      t = mma(lds_row((queries + by_row) ^ (32 * j)), k[j], t);
-      dp = mma(lds_row((grads + by_row) ^ (32 * j)), v[j], dp);
-      if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const v4f w = *reinterpret_cast<const v4f*>(stat + 8 * u + 4 * h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[4 * u + e] = __builtin_amdgcn_exp2f(fmaf(t[4 * u + e], a.scale_log2, w[e]));
-    }
-    if (masked) {
-      asm volatile("");
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int row = Q + result_row(e, h);
-        const bool seen = row >= lo && row < hi;
-        t[e] = seen ? t[e] : 0.0f;
-        dp[e] = seen ? dp[e] : 0.0f;
+      for (int j = 0; j < J; ++j) {
+        k[j] = *reinterpret_cast<const v8b*>(kp + 16 * j);
+        if constexpr (kWantK) v[j] = *reinterpret_cast<const v8b*>(vp + 16 * j);
       }
     }
-    v8b p[2], ds[2];
+    // the queries that see the lane's key
+    const int lo = a.causal ? key : 0;
+    const int hi = a.window ? (int)min((int64_t)s.n, (int64_t)key + a.window) : s.n;
+
+    v16f dk[DT], dv[DT];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) p[c] = operand(t, c);
-    dp *= t;
+    for (int d = 0; d < DT; ++d) dk[d] = dv[d] = zero16();
+
+    auto issue = [&](int group, int t, int buf) {
+      const int head = kv_head * a.group + group, T = walk.lo + t * kQueries, left = s.n - T;
+      const int64_t token = s.first + T;
+      load_q.issue(a.q + token * a.q_stride + head * D, qs, left, ring0 + buf * 2 * Load::kBytes, wave);
+      load_g.issue(a.dout + token * a.dout_stride + head * D, gs, left, ring0 + (2 * buf + 1) * Load::kBytes, wave);
+      // every wave brings all of the rows' statistics: the same words to the same place
+      const int64_t row = (int64_t)head * a.tokens + token + min(lane, left - 1);
+      dma4(a.lse2 + row, stats0 + buf * 512);
+      if constexpr (kWantK) dma4(a.delta + row, stats0 + buf * 512 + 256);
+    };
+
+    // 32 query rows from Q on, in LDS at `queries` and `grads`
+    auto consume = [&](bool masked, int Q, uint32_t queries, uint32_t grads, const float* stat) {
+      v16f t = zero16(), dp;
+      if constexpr (kWantK) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) ds[c] = operand(dp, c);
-    __builtin_amdgcn_sched_barrier(0);
+        for (int u = 0; u < 4; ++u) {
+          const v4f w = *reinterpret_cast<const v4f*>(stat + 64 + 8 * u + 4 * h);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        dv[d] = mma(column_step<D>(grads + by_column + c * 32 * D, d), p[c], dv[d]);
-        dk[d] = mma(column_step<D>(queries + by_column + c * 32 * D, d), ds[c], dk[d]);
-        if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+          for (int e = 0; e < 4; ++e) dp[4 * u + e] = w[e];
+        }
       }
-  };
-
-  int group = it0 / walk.tiles, t = it0 % walk.tiles, buf = 0;
-  issue(group, t, 0);
-  for (int it = 0; it < its; ++it, buf ^= 1) {
-    const int T = walk.lo + t * kQueries;
-    wait_vmcnt<0>();
-    bare_barrier();
-    if (++t == walk.tiles) t = 0, ++group;
-    if (it + 1 < its) issue(group, t, buf ^ 1);
-    const uint32_t queries = ring0 + buf * 2 * Load::kBytes, grads = queries + Load::kBytes;
-    // rows that some key of the workgroup is not seen by
-    if ((a.causal && T < min(k0 + kSeqRows, s.n) - 1) || T + kQueries > s.n ||
-        (a.window && T + kQueries > (int64_t)k0 + a.window)) {
-      if (has_bad<2 * Load::kBytes>(queries, found)) clear_bad<2 * Load::kBytes>(queries, 2 * D, nullptr);
-    }
 #pragma unroll
-    for (int sub = 0; sub < kQueries / 32; ++sub) {
-      const int Q = T + 32 * sub;
-      if (wkey >= s.n || Q >= s.n || (a.causal && Q + 31 < wkey)) continue;
-      if (a.window && Q >= (int64_t)wkey + 31 + a.window) continue;
-      const bool whole = Q + 32 <= s.n && (!a.causal || Q >= wkey + 31) &&
-                         (!a.window || Q + 31 < (int64_t)wkey + a.window);
-      consume(!whole, Q, queries + sub * 64 * D, grads + sub * 64 * D, &stats[buf][0][32 * sub]);
-    }
-  }
-
-  if (key >= s.n) return;
-  const int64_t token = s.first + key;
-  if (walk.chunks == 1) {
-    uint16_t* to_k = a.dk + token * a.dk_stride + kv_head * D + 4 * h;
-    uint16_t* to_v = a.dv + token * a.dv_stride + kv_head * D + 4 * h;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int j = 0; j < J; ++j) {
+        t = mma(lds_row((queries + by_row) ^ (32 * j)), k[j], t);
+        if constexpr (kWantK) dp = mma(lds_row((grads + by_row) ^ (32 * j)), v[j], dp);
+        if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int e = 4 * u;
-        *reinterpret_cast<uint2*>(to_k + 32 * d + 8 * u) =
-            make_uint2(pack_bf16(dk[d][e] * a.scale, dk[d][e + 1] * a.scale),
-                       pack_bf16(dk[d][e + 2] * a.scale, dk[d][e + 3] * a.scale));
-        *reinterpret_cast<uint2*>(to_v + 32 * d + 8 * u) =
-            make_uint2(pack_bf16(dv[d][e], dv[d][e + 1]), pack_bf16(dv[d][e + 2], dv[d][e + 3]));
+        const v4f w = *reinterpret_cast<const v4f*>(stat + 8 * u + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[4 * u + e] = __builtin_amdgcn_exp2f(fmaf(t[4 * u + e], a.scale_log2, w[e]));
       }
-    return;
-  }
-  const int64_t at = (((int64_t)split * a.tokens + token) * a.heads + kv_head) * D + 4 * h;
+      if (masked) {
+        asm volatile("");
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+        for (int e = 0; e < 16; ++e) {
+          const int row = Q + result_row(e, h);
+          const bool seen = row >= lo && row < hi;
+          t[e] = seen ? t[e] : 0.0f;
+          if constexpr (kWantK) dp[e] = seen ? dp[e] : 0.0f;
+        }
+      }
+      v8b p[2], ds[2];
+      if constexpr (kWantV) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = 4 * u;
-      *reinterpret_cast<v4f*>(a.part_k + at + 32 * d + 8 * u) = v4f{dk[d][e], dk[d][e + 1], dk[d][e + 2], dk[d][e + 3]};
-      *reinterpret_cast<v4f*>(a.part_v + at + 32 * d + 8 * u) = v4f{dv[d][e], dv[d][e + 1], dv[d][e + 2], dv[d][e + 3]};
+        for (int c = 0; c < 2; ++c) p[c] = operand(t, c);
+      }
+      if constexpr (kWantK) {
+        dp *= t;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ds[c] = operand(dp, c);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (kWantV) dv[d] = mma(column_step<D>(grads + by_column + c * 32 * D, d), p[c], dv[d]);
+          if constexpr (kWantK) dk[d] = mma(column_step<D>(queries + by_column + c * 32 * D, d), ds[c], dk[d]);
+          if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    int group = (int)(begin / walk.tiles), t = (int)(begin % walk.tiles), buf = 0;
+    issue(group, t, 0);
+    for (int64_t it = 0; it < its; ++it, buf ^= 1) {
+      const int T = walk.lo + t * kQueries;
+      wait_vmcnt<0>();
+      bare_barrier();
+      if (++t == walk.tiles) t = 0, ++group;
+      if (it + 1 < its) issue(group, t, buf ^ 1);
+      const uint32_t queries = ring0 + buf * 2 * Load::kBytes, grads = queries + Load::kBytes;
+      // rows that some key of the workgroup is not seen by
+      if ((a.causal && T < min(k0 + kSeqRows, s.n) - 1) || T + kQueries > s.n ||
+          (a.window && T + kQueries > (int64_t)k0 + a.window)) {
+        if (has_bad<2 * Load::kBytes>(queries, found)) clear_bad<2 * Load::kBytes>(queries, 2 * D, nullptr);
+      }
+#pragma unroll
+      for (int sub = 0; sub < kQueries / 32; ++sub) {
+        const int Q = T + 32 * sub;
+        if (wkey >= s.n || Q >= s.n || (a.causal && Q + 31 < wkey)) continue;
+        if (a.window && Q >= (int64_t)wkey + 31 + a.window) continue;
+        const bool whole = Q + 32 <= s.n && (!a.causal || Q >= wkey + 31) &&
+                           (!a.window || Q + 31 < (int64_t)wkey + a.window);
+        consume(!whole, Q, queries + sub * 64 * D, grads + sub * 64 * D, &lds.stats[buf][0][32 * sub]);
+      }
     }
+    bare_barrier();  // every wave is done with the ring
+
+    if (key >= s.n) continue;
+    if (its == length) {
+      const int64_t token = s.first + key;
+      uint16_t* to_k = a.dk + token * a.dk_stride + kv_head * D + 4 * h;
+      uint16_t* to_v = a.dv + token * a.dv_stride + kv_head * D + 4 * h;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = 4 * u;
+          if constexpr (kWantK)
+            *reinterpret_cast<uint2*>(to_k + 32 * d + 8 * u) =
+                make_uint2(pack_bf16(dk[d][e] * a.scale, dk[d][e + 1] * a.scale),
+                           pack_bf16(dk[d][e + 2] * a.scale, dk[d][e + 3] * a.scale));
+          if constexpr (kWantV)
+            *reinterpret_cast<uint2*>(to_v + 32 * d + 8 * u) =
+                make_uint2(pack_bf16(dv[d][e], dv[d][e + 1]), pack_bf16(dv[d][e + 2], dv[d][e + 3]));
+        }
+    } else {
+      // a share cuts at most two walks: the one it begins inside of (0), the one it ends in (1)
+      const int64_t slot = 2 * (int64_t)x + (begin == 0);
+      const int64_t to = (slot * kSeqRows + 32 * wave + r32) * D + 4 * h;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = 4 * u;
+          if constexpr (kWantK)
+            *reinterpret_cast<v4f*>(a.part_k + to + 32 * d + 8 * u) = v4f{dk[d][e], dk[d][e + 1], dk[d][e + 2], dk[d][e + 3]};
+          if constexpr (kWantV)
+            *reinterpret_cast<v4f*>(a.part_v + to + 32 * d + 8 * u) = v4f{dv[d][e], dv[d][e + 1], dv[d][e + 2], dv[d][e + 3]};
+        }
+    }
+  }
 }
 
-// Adds the chunks' sums of key tiles that were split, in order.
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_grad_kernel(SeqAttnArgs a) {
+  __shared__ GradShared<D> lds;
+  const uint32_t x = a.first + blockIdx.x;
+  if constexpr (D == 256) {
+    if (x < a.dkv_groups) dkv_group<D, kDk>(a, lds, x);
+    else if (x < 2 * a.dkv_groups) dkv_group<D, kDv>(a, lds, x - a.dkv_groups);
+    else dq_group<D>(a, lds, x - 2 * a.dkv_groups);
+  } else {
+    if (x < a.dkv_groups) dkv_group<D, kDk | kDv>(a, lds, x);
+    else dq_group<D>(a, lds, x - a.dkv_groups);
+  }
+}
+
+// Adds the sums of the key tiles whose walks were cut, share by share; a
+// workgroup takes kJoinKeys of a tile's keys.
+constexpr int kJoinKeys = 32;
 template <int D>
 __global__ __launch_bounds__(256) void seq_attn_join_kernel(SeqAttnArgs a) {
   uint32_t x = a.first + blockIdx.x;
   const int kv_head = x % a.heads;
   x /= a.heads;
-  const Seq s = seq_of(a, x % a.batch);
-  const int k0 = (int)(x / a.batch) * kSeqRows;
-  if (k0 >= s.n) return;
-  const int chunks = walk_of<D>(a, s, k0).chunks;
-  if (chunks == 1) return;
-  const int keys = min(kSeqRows, s.n - k0);
-  const int64_t step = (int64_t)a.tokens * a.heads * D;
+  const int key0 = (x % (kSeqRows / kJoinKeys)) * kJoinKeys, at = x / (kSeqRows / kJoinKeys);
+  if (at >= a.line_end->seq) return;
+  const SeqLine tile = a.line[at];
+  const Seq s = seq_of(a, tile.seq);
+  const int64_t total = a.line_end->start, last = tile.start + (int64_t)walk_of<D>(a, s.n, tile.k0).tiles * a.group - 1;
+  // the shares that hold the walk's first and last tile
+  const int64_t j0 = ((tile.start + 1) * a.shares - 1) / total, j1 = ((last + 1) * a.shares - 1) / total;
+  if (j0 == j1) return;
+  const int keys = min(kJoinKeys, s.n - tile.k0 - key0);
   for (int i = threadIdx.x; i < keys * (D / 4); i += 256) {
-    const int64_t token = s.first + k0 + i / (D / 4);
-    const int d = 4 * (i % (D / 4));
-    const int64_t at = (token * a.heads + kv_head) * D + d;
-    v4f k = *reinterpret_cast<const v4f*>(a.part_k + at), v = *reinterpret_cast<const v4f*>(a.part_v + at);
-    for (int c = 1; c < chunks; ++c) {
-      k += *reinterpret_cast<const v4f*>(a.part_k + at + c * step);
-      v += *reinterpret_cast<const v4f*>(a.part_v + at + c * step);
+    const int key = key0 + i / (D / 4), d = 4 * (i % (D / 4));
+    v4f k = {0.0f, 0.0f, 0.0f, 0.0f}, v = k;
+    for (int64_t j = j0; j <= j1; ++j) {
+      if (share_start(total, a.shares, j) == share_start(total, a.shares, j + 1)) continue;  // nobody's
+      const int64_t from = ((2 * (j * a.heads + kv_head) + (j == j0)) * kSeqRows + key) * D + d;
+      k += *reinterpret_cast<const v4f*>(a.part_k + from);
+      v += *reinterpret_cast<const v4f*>(a.part_v + from);
     }
+    const int64_t token = s.first + tile.k0 + key;
     k *= a.scale;
     *reinterpret_cast<uint2*>(a.dk + token * a.dk_stride + kv_head * D + d) =
         make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
@@ -379,26 +507,32 @@ __global__ __launch_bounds__(256) void seq_attn_join_kernel(SeqAttnArgs a) {
   }
 }
 
-// How the walks of the key tiles are cut: chunk in query tiles, the most chunks
-// of one.  From the shape alone, so that the workspace does not depend on the mask.
-struct Cut {
-  int chunk, splits;
-};
-Cut cut_of(const SeqAttnShape& s) {
-  const int64_t queries = s.head_dim == 256 ? 32 : 64;
-  const int64_t longest = (s.max_len + queries - 1) / queries * (s.q_heads / s.heads);  // of a key tile's walk
-  const int64_t key_tiles = (s.tokens + kSeqRows - 1) / kSeqRows;                       // about, of all sequences
-  // enough chunks for four workgroups a CU, none shorter than eight tiles
-  const int64_t want = 1024, have = key_tiles * s.heads;
-  const int64_t splits = std::max<int64_t>(1, std::min(want / std::max<int64_t>(have, 1), longest / 8));
-  const int64_t chunk = (longest + splits - 1) / splits;
-  return {(int)chunk, (int)((longest + chunk - 1) / chunk)};
-}
+// Fewest query tiles of a share (were every query to see every key).
+constexpr int64_t kLeastShare = 8;
 
-int64_t aligned(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
-int64_t stat_bytes(const SeqAttnShape& s) { return aligned((int64_t)s.tokens * s.q_heads * 4); }
-int64_t part_bytes(const SeqAttnShape& s, int splits) {
-  return aligned((int64_t)splits * s.tokens * s.heads * s.head_dim * 4);
+// From the shape alone, so that the workspace does not depend on the mask.
+struct BwdPlan {
+  int most_tiles, shares;  // shares 0: whole key tiles
+  int64_t stat, part, line, bytes;  // bytes of each
+};
+BwdPlan plan_of(const SeqAttnShape& s) {
+  BwdPlan p;
+  const int64_t tiles = (s.max_len + kSeqRows - 1) / kSeqRows;
+  p.most_tiles = (int)std::min((int64_t)s.tokens / kSeqRows + s.batch, tiles * s.batch);
+  // Workgroups that run at once on 256 CUs.  Twice as many key tiles: one each,
+  // whose neighbours walk the same queries at the same time (four sequences of
+  // 4096, 32 heads: tiles 2086 us, shares 2356).
+  const int64_t resident = s.head_dim == 256 ? 256 : 512, queries = s.head_dim == 256 ? 32 : 64;
+  const int64_t work = p.most_tiles * ((s.max_len + queries - 1) / queries) * (s.q_heads / s.heads);
+  p.shares = 0;
+  if (p.most_tiles * (int64_t)s.heads < 2 * resident)
+    p.shares = (int)std::max<int64_t>(1, std::min(resident / s.heads, work / kLeastShare));
+  auto aligned = [](int64_t bytes) { return (bytes + 255) & ~(int64_t)255; };
+  p.stat = aligned((int64_t)s.tokens * s.q_heads * 4);
+  p.part = (int64_t)p.shares * s.heads * 2 * kSeqRows * s.head_dim * 4;
+  p.line = aligned(((int64_t)p.most_tiles + 1) * (int64_t)sizeof(SeqLine));
+  p.bytes = 2 * p.stat + 2 * p.part + p.line;
+  return p;
 }
 
 template <int D>
@@ -409,30 +543,35 @@ void run_bwd(SeqAttnArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL(kernel, dim3(count), dim3(256), 0, stream, a);
     });
   };
+  launch(seq_attn_stats_kernel<D>, ((int64_t)a.tokens * a.q_heads * (D / 8) + 255) / 256 + (a.shares > 0));
   const int64_t tiles = (int64_t)a.tiles * a.batch;
-  launch(seq_attn_dq_kernel<D>, tiles * a.q_heads);
-  launch(seq_attn_dkv_kernel<D>, tiles * a.heads * a.splits);
-  if (a.splits > 1) launch(seq_attn_join_kernel<D>, tiles * a.heads);
+  const int64_t dkv = a.shares > 0 ? (int64_t)a.heads * a.shares : tiles * a.heads;
+  a.dkv_groups = (uint32_t)dkv;
+  launch(seq_attn_grad_kernel<D>, (D == 256 ? 2 : 1) * dkv + tiles * a.q_heads);
+  if (a.shares > 1) launch(seq_attn_join_kernel<D>, (int64_t)a.most_tiles * a.heads * (kSeqRows / kJoinKeys));
 }
 
 }  // namespace
 
-int64_t seq_attn_bwd_workspace_bytes(const SeqAttnShape& s) {
-  const Cut c = cut_of(s);
-  return 2 * stat_bytes(s) + (c.splits > 1 ? 2 * part_bytes(s, c.splits) : 0);
-}
+int64_t seq_attn_bwd_workspace_bytes(const SeqAttnShape& s) { return plan_of(s).bytes; }
 
 hipError_t launch_seq_attn_bwd(SeqAttnArgs a, int head_dim, void* ws, hipStream_t stream) {
-  const SeqAttnShape s{a.batch, a.tokens, a.max_len, a.q_heads, a.heads, head_dim};
-  const Cut c = cut_of(s);
-  a.chunk = c.chunk;
-  a.splits = c.splits;
+  const BwdPlan p = plan_of({a.batch, a.tokens, a.max_len, a.q_heads, a.heads, head_dim});
+  a.shares = p.shares;
+  a.most_tiles = p.most_tiles;
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
-  uint8_t* p = static_cast<uint8_t*>(ws);
-  a.lse2 = reinterpret_cast<float*>(p);
-  a.delta = reinterpret_cast<float*>(p + stat_bytes(s));
-  a.part_k = reinterpret_cast<float*>(p + 2 * stat_bytes(s));
-  a.part_v = reinterpret_cast<float*>(p + 2 * stat_bytes(s) + part_bytes(s, c.splits));
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  auto take = [&](int64_t bytes) {
+    uint8_t* r = at;
+    at += bytes;
+    return r;
+  };
+  a.line = reinterpret_cast<SeqLine*>(take(p.line));
+  a.line_end = a.line + p.most_tiles;
+  a.lse2 = reinterpret_cast<float*>(take(p.stat));
+  a.delta = reinterpret_cast<float*>(take(p.stat));
+  a.part_k = reinterpret_cast<float*>(take(p.part));
+  a.part_v = reinterpret_cast<float*>(take(p.part));
   if (head_dim == 64) run_bwd<64>(a, stream);
   else if (head_dim == 128) run_bwd<128>(a, stream);
   else run_bwd<256>(a, stream);
