@@ -51,7 +51,9 @@ struct SeqAttnArgs {
   SeqLine *line, *line_end;  // key tiles of a head; their walks' length, and their number in `seq`
   int most_tiles;  // of `line`
   int shares;      // of a head's line, or 0: a workgroup takes a key tile
+  int64_t share_tiles;  // query tiles of a share, about
   uint32_t dkv_groups;  // workgroups of dk and dv, each
+  uint32_t dq_first;    // workgroups of dq, where they come first, or 0
 };
 
 namespace {

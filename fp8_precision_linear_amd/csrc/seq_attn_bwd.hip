@@ -114,6 +114,11 @@ __global__ __launch_bounds__(256) void seq_attn_stats_kernel(SeqAttnArgs a) {
   a.delta[to] = -delta;
 }
 
+// Sub-tiles of 32 rows (keys) whose products run side by side: two where the
+// registers hold them.
+template <int D>
+constexpr int kSubs = D == 64 ? 2 : 1;
+
 // LDS of a workgroup.
 template <int D>
 struct GradShared {
@@ -126,7 +131,7 @@ struct GradShared {
 
 template <int D>
 __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& lds, uint32_t x) {
-  constexpr int J = D / 16, DT = D / 32, kKeys = GradShared<D>::kRows;
+  constexpr int J = D / 16, DT = D / 32, kKeys = GradShared<D>::kRows, SUB = kSubs<D>, kStep = 32 * SUB;
   using Load = TileLoad<D, kKeys>;
   int* const found = lds.found;
   int* const bad_key = lds.bad_key;
@@ -182,41 +187,53 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
   for (int d = 0; d < DT; ++d) dq[d] = zero16();
   const uint32_t by_row = row_place<D>(lane), by_column = column_place<D>(lane);
 
-  // 32 keys from position K on, in LDS at `keys` and `values`
+  // kStep keys from position K on, in LDS at `keys` and `values`
   auto consume = [&](bool masked, bool any_bad, int K, uint32_t keys, uint32_t values, int slot) {
-    v16f t = zero16(), dp;
+    v16f t[SUB], dp[SUB];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dp[e] = minus_delta;
+    for (int sub = 0; sub < SUB; ++sub) {
+      t[sub] = zero16();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dp[sub][e] = minus_delta;
+    }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      t = mma(lds_row((keys + by_row) ^ (32 * j)), q[j], t);
-      dp = mma(lds_row((values + by_row) ^ (32 * j)), g[j], dp);
-      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) {
+        t[sub] = mma(lds_row(((keys + by_row) ^ (32 * j)) + sub * 64 * D), q[j], t[sub]);
+        dp[sub] = mma(lds_row(((values + by_row) ^ (32 * j)) + sub * 64 * D), g[j], dp[sub]);
+      }
+      if (D > 64 && j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
     if (any_bad) {
       asm volatile("");
 #pragma unroll
-      for (int e = 0; e < 16; ++e) t[e] = bad_key[slot + result_row(e, h)] ? NAN : t[e];
-    }
-    v16f ds;
+      for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ds[e] = __builtin_amdgcn_exp2f(fmaf(t[e], a.scale_log2, minus_lse2)) * dp[e];
+        for (int e = 0; e < 16; ++e) t[sub][e] = bad_key[slot + 32 * sub + result_row(e, h)] ? NAN : t[sub][e];
+    }
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dp[sub][e] *= __builtin_amdgcn_exp2f(fmaf(t[sub][e], a.scale_log2, minus_lse2));
     if (masked) {
       asm volatile("");
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int key = K + result_row(e, h);
-        ds[e] = key >= lo && key < hi ? ds[e] : 0.0f;
-      }
+      for (int sub = 0; sub < SUB; ++sub)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = K + 32 * sub + result_row(e, h);
+          dp[sub][e] = key >= lo && key < hi ? dp[sub][e] : 0.0f;
+        }
     }
-    v8b b[2];
+    v8b ds[2 * SUB];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) b[c] = operand(ds, c);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int c = 0; c < 2 * SUB; ++c) ds[c] = operand(dp[c >> 1], c & 1);
+    if (D > 64) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2 * SUB; ++c)
 #pragma unroll
-      for (int d = 0; d < DT; ++d) dq[d] = mma(column_step<D>(keys + by_column + c * 32 * D, d), b[c], dq[d]);
+      for (int d = 0; d < DT; ++d) dq[d] = mma(column_step<D>(keys + by_column + c * 32 * D, d), ds[c], dq[d]);
   };
 
   int buf = 0;
@@ -234,11 +251,11 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
       }
     }
 #pragma unroll
-    for (int sub = 0; sub < kKeys / 32; ++sub) {
-      const int K = T + 32 * sub;
-      if (K >= whi || K + 32 <= wlo) continue;
-      const bool whole = K + 32 <= min(s.n, a.causal ? wrow + 1 : s.n) && (!a.window || K > wrow + 31 - a.window);
-      consume(!whole, any_bad, K, keys + sub * 64 * D, values + sub * 64 * D, 32 * sub);
+    for (int slot = 0; slot < kKeys; slot += kStep) {
+      const int K = T + slot;
+      if (K >= whi || K + kStep <= wlo) continue;
+      const bool whole = K + kStep <= min(s.n, a.causal ? wrow + 1 : s.n) && (!a.window || K > wrow + 31 - a.window);
+      consume(!whole, any_bad, K, keys + slot * 2 * D, values + slot * 2 * D, slot);
     }
   }
 
@@ -267,7 +284,7 @@ constexpr int kDk = 1, kDv = 2;
 // x: the workgroup among those of its kind.
 template <int D, int SUMS>
 __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& lds, uint32_t x) {
-  constexpr int J = D / 16, DT = D / 32, kQueries = kQueriesOf<D>;
+  constexpr int J = D / 16, DT = D / 32, kQueries = kQueriesOf<D>, SUB = kSubs<D>, kStep = 32 * SUB;
   constexpr bool kWantK = (SUMS & kDk) != 0, kWantV = (SUMS & kDv) != 0;
   using Load = TileLoad<D, kQueries>;
   int* const found = lds.found;
@@ -342,57 +359,70 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
       if constexpr (kWantK) dma4(a.delta + row, stats0 + buf * 512 + 256);
     };
 
-    // 32 query rows from Q on, in LDS at `queries` and `grads`
+    // kStep query rows from Q on, in LDS at `queries` and `grads`
     auto consume = [&](bool masked, int Q, uint32_t queries, uint32_t grads, const float* stat) {
-      v16f t = zero16(), dp;
-      if constexpr (kWantK) {
+      v16f t[SUB], dp[SUB];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const v4f w = *reinterpret_cast<const v4f*>(stat + 64 + 8 * u + 4 * h);
+      for (int sub = 0; sub < SUB; ++sub) {
+        t[sub] = zero16();
+        if constexpr (kWantK) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dp[4 * u + e] = w[e];
+          for (int u = 0; u < 4; ++u) {
+            const v4f w = *reinterpret_cast<const v4f*>(stat + 64 + 32 * sub + 8 * u + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dp[sub][4 * u + e] = w[e];
+          }
         }
       }
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        t = mma(lds_row((queries + by_row) ^ (32 * j)), k[j], t);
-        if constexpr (kWantK) dp = mma(lds_row((grads + by_row) ^ (32 * j)), v[j], dp);
-        if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+          t[sub] = mma(lds_row(((queries + by_row) ^ (32 * j)) + sub * 64 * D), k[j], t[sub]);
+          if constexpr (kWantK) dp[sub] = mma(lds_row(((grads + by_row) ^ (32 * j)) + sub * 64 * D), v[j], dp[sub]);
+        }
+        if (D > 64 && j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const v4f w = *reinterpret_cast<const v4f*>(stat + 8 * u + 4 * h);
+      for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[4 * u + e] = __builtin_amdgcn_exp2f(fmaf(t[4 * u + e], a.scale_log2, w[e]));
-      }
+        for (int u = 0; u < 4; ++u) {
+          const v4f w = *reinterpret_cast<const v4f*>(stat + 32 * sub + 8 * u + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            t[sub][4 * u + e] = __builtin_amdgcn_exp2f(fmaf(t[sub][4 * u + e], a.scale_log2, w[e]));
+        }
       if (masked) {
         asm volatile("");
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int row = Q + result_row(e, h);
-          const bool seen = row >= lo && row < hi;
-          t[e] = seen ? t[e] : 0.0f;
-          if constexpr (kWantK) dp[e] = seen ? dp[e] : 0.0f;
-        }
-      }
-      v8b p[2], ds[2];
-      if constexpr (kWantV) {
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) p[c] = operand(t, c);
+          for (int e = 0; e < 16; ++e) {
+            const int row = Q + 32 * sub + result_row(e, h);
+            const bool seen = row >= lo && row < hi;
+            t[sub][e] = seen ? t[sub][e] : 0.0f;
+            if constexpr (kWantK) dp[sub][e] = seen ? dp[sub][e] : 0.0f;
+          }
+      }
+      v8b p[2 * SUB], ds[2 * SUB];
+#pragma unroll
+      for (int c = 0; c < 2 * SUB; ++c) {
+        if constexpr (kWantV) p[c] = operand(t[c >> 1], c & 1);
       }
       if constexpr (kWantK) {
-        dp *= t;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) ds[c] = operand(dp, c);
+        for (int sub = 0; sub < SUB; ++sub) dp[sub] *= t[sub];
+#pragma unroll
+        for (int c = 0; c < 2 * SUB; ++c) ds[c] = operand(dp[c >> 1], c & 1);
       }
-      __builtin_amdgcn_sched_barrier(0);
+      if (D > 64) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2 * SUB; ++c)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (kWantV) dv[d] = mma(column_step<D>(grads + by_column + c * 32 * D, d), p[c], dv[d]);
           if constexpr (kWantK) dk[d] = mma(column_step<D>(queries + by_column + c * 32 * D, d), ds[c], dk[d]);
-          if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+          if (D > 64 && d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -411,13 +441,13 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
         if (has_bad<2 * Load::kBytes>(queries, found)) clear_bad<2 * Load::kBytes>(queries, 2 * D, nullptr);
       }
 #pragma unroll
-      for (int sub = 0; sub < kQueries / 32; ++sub) {
-        const int Q = T + 32 * sub;
-        if (wkey >= s.n || Q >= s.n || (a.causal && Q + 31 < wkey)) continue;
+      for (int slot = 0; slot < kQueries; slot += kStep) {
+        const int Q = T + slot;
+        if (wkey >= s.n || Q >= s.n || (a.causal && Q + kStep - 1 < wkey)) continue;
         if (a.window && Q >= (int64_t)wkey + 31 + a.window) continue;
-        const bool whole = Q + 32 <= s.n && (!a.causal || Q >= wkey + 31) &&
-                           (!a.window || Q + 31 < (int64_t)wkey + a.window);
-        consume(!whole, Q, queries + sub * 64 * D, grads + sub * 64 * D, &lds.stats[buf][0][32 * sub]);
+        const bool whole = Q + kStep <= s.n && (!a.causal || Q >= wkey + 31) &&
+                           (!a.window || Q + kStep - 1 < (int64_t)wkey + a.window);
+        consume(!whole, Q, queries + slot * 2 * D, grads + slot * 2 * D, &lds.stats[buf][0][slot]);
       }
     }
     bare_barrier();  // every wave is done with the ring
@@ -458,53 +488,70 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
   }
 }
 
+// The kind whose workgroups take longest comes first.
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_grad_kernel(SeqAttnArgs a) {
   __shared__ GradShared<D> lds;
-  const uint32_t x = a.first + blockIdx.x;
-  if constexpr (D == 256) {
-    if (x < a.dkv_groups) dkv_group<D, kDk>(a, lds, x);
-    else if (x < 2 * a.dkv_groups) dkv_group<D, kDv>(a, lds, x - a.dkv_groups);
-    else dq_group<D>(a, lds, x - 2 * a.dkv_groups);
-  } else {
-    if (x < a.dkv_groups) dkv_group<D, kDk | kDv>(a, lds, x);
-    else dq_group<D>(a, lds, x - a.dkv_groups);
+  uint32_t x = a.first + blockIdx.x;
+  if (x >= a.dq_first) {
+    const uint32_t y = x - a.dq_first;
+    if constexpr (D == 256) {
+      if (y < a.dkv_groups) return dkv_group<D, kDk>(a, lds, y);
+      if (y < 2 * a.dkv_groups) return dkv_group<D, kDv>(a, lds, y - a.dkv_groups);
+      x -= 2 * a.dkv_groups;
+    } else {
+      if (y < a.dkv_groups) return dkv_group<D, kDk | kDv>(a, lds, y);
+      x -= a.dkv_groups;
+    }
   }
+  dq_group<D>(a, lds, x);
 }
 
-// Adds the sums of the key tiles whose walks were cut, share by share; a
-// workgroup takes kJoinKeys of a tile's keys.
-constexpr int kJoinKeys = 32;
+// Adds the sums of the key tiles whose walks were cut, share by share: a lane
+// four dimensions of a key.
 template <int D>
 __global__ __launch_bounds__(256) void seq_attn_join_kernel(SeqAttnArgs a) {
+  constexpr int kKeys = 1024 / D, kParts = kSeqRows / kKeys;
   uint32_t x = a.first + blockIdx.x;
   const int kv_head = x % a.heads;
   x /= a.heads;
-  const int key0 = (x % (kSeqRows / kJoinKeys)) * kJoinKeys, at = x / (kSeqRows / kJoinKeys);
+  const int at = x / kParts, key = (int)(x % kParts) * kKeys + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
   if (at >= a.line_end->seq) return;
   const SeqLine tile = a.line[at];
   const Seq s = seq_of(a, tile.seq);
   const int64_t total = a.line_end->start, last = tile.start + (int64_t)walk_of<D>(a, s.n, tile.k0).tiles * a.group - 1;
   // the shares that hold the walk's first and last tile
   const int64_t j0 = ((tile.start + 1) * a.shares - 1) / total, j1 = ((last + 1) * a.shares - 1) / total;
-  if (j0 == j1) return;
-  const int keys = min(kJoinKeys, s.n - tile.k0 - key0);
-  for (int i = threadIdx.x; i < keys * (D / 4); i += 256) {
-    const int key = key0 + i / (D / 4), d = 4 * (i % (D / 4));
-    v4f k = {0.0f, 0.0f, 0.0f, 0.0f}, v = k;
-    for (int64_t j = j0; j <= j1; ++j) {
-      if (share_start(total, a.shares, j) == share_start(total, a.shares, j + 1)) continue;  // nobody's
-      const int64_t from = ((2 * (j * a.heads + kv_head) + (j == j0)) * kSeqRows + key) * D + d;
-      k += *reinterpret_cast<const v4f*>(a.part_k + from);
-      v += *reinterpret_cast<const v4f*>(a.part_v + from);
+  if (j0 == j1 || key >= s.n - tile.k0) return;
+  // slots: the first share's second one, the others' first
+  const int64_t step = (int64_t)a.heads * 2 * kSeqRows * D;
+  const int64_t from = ((2 * (j0 * a.heads + kv_head)) * kSeqRows + key) * D + d;
+  v4f k = *reinterpret_cast<const v4f*>(a.part_k + from + kSeqRows * D);
+  v4f v = *reinterpret_cast<const v4f*>(a.part_v + from + kSeqRows * D);
+  // (where the line is shorter than its shares are many, some are empty)
+  for (int64_t j = j0 + 1; j <= j1; j += 4) {
+    v4f pk[4], pv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool there = j + i <= j1 && share_start(total, a.shares, j + i) < share_start(total, a.shares, j + i + 1);
+      pk[i] = pv[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      if (there) {
+        pk[i] = *reinterpret_cast<const v4f*>(a.part_k + from + (j + i - j0) * step);
+        pv[i] = *reinterpret_cast<const v4f*>(a.part_v + from + (j + i - j0) * step);
+      }
     }
-    const int64_t token = s.first + tile.k0 + key;
-    k *= a.scale;
-    *reinterpret_cast<uint2*>(a.dk + token * a.dk_stride + kv_head * D + d) =
-        make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
-    *reinterpret_cast<uint2*>(a.dv + token * a.dv_stride + kv_head * D + d) =
-        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k += pk[i];
+      v += pv[i];
+    }
   }
+  const int64_t token = s.first + tile.k0 + key;
+  k *= a.scale;
+  *reinterpret_cast<uint2*>(a.dk + token * a.dk_stride + kv_head * D + d) =
+      make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
+  *reinterpret_cast<uint2*>(a.dv + token * a.dv_stride + kv_head * D + d) =
+      make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
 // Fewest query tiles of a share (were every query to see every key).
@@ -513,6 +560,7 @@ constexpr int64_t kLeastShare = 8;
 // From the shape alone, so that the workspace does not depend on the mask.
 struct BwdPlan {
   int most_tiles, shares;  // shares 0: whole key tiles
+  int64_t share_tiles;     // query tiles of a share, about
   int64_t stat, part, line, bytes;  // bytes of each
 };
 BwdPlan plan_of(const SeqAttnShape& s) {
@@ -525,8 +573,10 @@ BwdPlan plan_of(const SeqAttnShape& s) {
   const int64_t resident = s.head_dim == 256 ? 256 : 512, queries = s.head_dim == 256 ? 32 : 64;
   const int64_t work = p.most_tiles * ((s.max_len + queries - 1) / queries) * (s.q_heads / s.heads);
   p.shares = 0;
+  p.share_tiles = 0;
   if (p.most_tiles * (int64_t)s.heads < 2 * resident)
     p.shares = (int)std::max<int64_t>(1, std::min(resident / s.heads, work / kLeastShare));
+  if (p.shares > 0) p.share_tiles = work / p.shares;
   auto aligned = [](int64_t bytes) { return (bytes + 255) & ~(int64_t)255; };
   p.stat = aligned((int64_t)s.tokens * s.q_heads * 4);
   p.part = (int64_t)p.shares * s.heads * 2 * kSeqRows * s.head_dim * 4;
@@ -546,9 +596,11 @@ void run_bwd(SeqAttnArgs& a, hipStream_t stream) {
   launch(seq_attn_stats_kernel<D>, ((int64_t)a.tokens * a.q_heads * (D / 8) + 255) / 256 + (a.shares > 0));
   const int64_t tiles = (int64_t)a.tiles * a.batch;
   const int64_t dkv = a.shares > 0 ? (int64_t)a.heads * a.shares : tiles * a.heads;
+  const int64_t dq = tiles * a.q_heads;
   a.dkv_groups = (uint32_t)dkv;
-  launch(seq_attn_grad_kernel<D>, (D == 256 ? 2 : 1) * dkv + tiles * a.q_heads);
-  if (a.shares > 1) launch(seq_attn_join_kernel<D>, (int64_t)a.most_tiles * a.heads * (kSeqRows / kJoinKeys));
+  a.dq_first = a.share_tiles > 0 && a.share_tiles < (a.max_len + kQueriesOf<D> - 1) / kQueriesOf<D> ? (uint32_t)dq : 0;
+  launch(seq_attn_grad_kernel<D>, (D == 256 ? 2 : 1) * dkv + dq);
+  if (a.shares > 1) launch(seq_attn_join_kernel<D>, (int64_t)a.most_tiles * a.heads * (kSeqRows * D / 1024));
 }
 
 }  // namespace
@@ -558,6 +610,7 @@ int64_t seq_attn_bwd_workspace_bytes(const SeqAttnShape& s) { return plan_of(s).
 hipError_t launch_seq_attn_bwd(SeqAttnArgs a, int head_dim, void* ws, hipStream_t stream) {
   const BwdPlan p = plan_of({a.batch, a.tokens, a.max_len, a.q_heads, a.heads, head_dim});
   a.shares = p.shares;
+  a.share_tiles = p.share_tiles;
   a.most_tiles = p.most_tiles;
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
   uint8_t* at = static_cast<uint8_t*>(ws);

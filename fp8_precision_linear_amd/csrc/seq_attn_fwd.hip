@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
     for (int j = 0; j < J; ++j) {
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub) t[sub] = mma(lds_row(((tile + krow) ^ (32 * j)) + sub * 64 * D), q[j], t[sub]);
-      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // LDS reads do not run further ahead: registers
+      if (D > 64 && j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // LDS reads do not run further ahead: registers
     }
     if (masked) {
       asm volatile("");  // a branch: as selects it would cost every tile
@@ -144,13 +144,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
       probabilities();
     }
     l += part;
-    __builtin_amdgcn_sched_barrier(0);
+    if (D > 64) __builtin_amdgcn_sched_barrier(0);
     const uint32_t v = tile + Load::kBytes + vcol;
 #pragma unroll
     for (int c = 0; c < 2 * SUB; ++c) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = mma(column_step<D>(v + c * 32 * D, d), p[c >> 1][c & 1], o[d]);
-      if (c & 1) __builtin_amdgcn_sched_barrier(0);
+      if (D > 64 && (c & 1)) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
