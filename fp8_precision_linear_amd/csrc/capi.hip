@@ -156,6 +156,7 @@ int seqs_checks(const fp8_seqs_t* s, int32_t q_heads, int32_t kv_heads, int32_t 
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP8_ERR_SIZE;
   if ((int64_t)q_heads * head_dim > kMaxRowStride) return FP8_ERR_SIZE;
   // workgroups are counted in 32 bits: three kinds of them in the backward pass
+  // (cut walks and their joins are of shapes with few)
   const int64_t longest = s->max_len < s->tokens ? s->max_len : s->tokens;
   if ((longest + 127) / 128 * s->batch > (int64_t)0x7FFFFFFF / (3 * (int64_t)q_heads) ||
       s->tokens > (int64_t)0x7FFFFFFF / q_heads)

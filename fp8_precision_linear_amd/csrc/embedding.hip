@@ -120,19 +120,19 @@ struct SortShared {
   uint32_t wave_total[kSortWaves];
 };
 
-// The places of a tile's items when they are sorted by one digit, stably.  Items
-// lie wave by wave: item (wave, i, lane) is number wave * 64 * kItems + 64 i +
-// lane.  Absent items (past n) have the last place.  Ends with a barrier.
-// first_of: receives the first place of each digit.
-__device__ __forceinline__ void digit_places(const uint32_t (&key)[kItems], int n, int shift, int bits,
-                                             SortShared& s, uint32_t (&place)[kItems], uint32_t* first_of) {
+// The places of a tile's n items when they are sorted by one digit, stably.
+// Items lie wave by wave, `items` of a lane: item (wave, i, lane) is number wave
+// * 64 * items + 64 i + lane.  first_of: receives the first place of each digit.
+__device__ __forceinline__ void digit_places(const uint32_t (&key)[kItems], int items, int n, int shift,
+                                             int bits, SortShared& s, uint32_t (&place)[kItems], uint32_t* first_of) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bins = 1 << bits;
   for (int b = lane; b < bins; b += 64) s.count[wave][b] = 0;
   wave_fence();
   const uint64_t below = ((uint64_t)1 << lane) - 1;
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    const bool there = wave * 64 * kItems + 64 * i + lane < n;
+    if (i >= items) break;
+    const bool there = wave * 64 * items + 64 * i + lane < n;
     const uint32_t digit = (key[i] >> shift) & (bins - 1);
     uint64_t same = __ballot(there);
     for (int b = 0; b < bits; ++b) {
@@ -169,7 +169,7 @@ __device__ __forceinline__ void digit_places(const uint32_t (&key)[kItems], int 
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     const uint32_t digit = (key[i] >> shift) & (bins - 1);
-    if (wave * 64 * kItems + 64 * i + lane < n) place[i] += s.count[wave][digit] + first_of[digit];
+    if (i < items && wave * 64 * items + 64 * i + lane < n) place[i] += s.count[wave][digit] + first_of[digit];
   }
 }
 
@@ -181,25 +181,26 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(SortArgs a
   __shared__ uint16_t orders[kTile];
   if (blockIdx.x > 0) return clear_share(a, 1);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = (int)a.tokens;
+  const int items = (n + kSortThreads - 1) / kSortThreads, mine = wave * 64 * items + lane;
+  auto there = [&](int i) { return i < items && mine + 64 * i < n; };
   uint32_t key[kItems], order[kItems], place[kItems];
-  const int mine = wave * 64 * kItems + lane;
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     order[i] = mine + 64 * i;
-    key[i] = mine + 64 * i < n ? key_at(a, mine + 64 * i) : 0xFFFFFFFFu;
+    key[i] = there(i) ? key_at(a, mine + 64 * i) : 0xFFFFFFFFu;
   }
   for (int pass = 0; pass < a.passes; ++pass) {
-    digit_places(key, n, pass * a.bits, a.bits, s, place, first_of);
+    digit_places(key, items, n, pass * a.bits, a.bits, s, place, first_of);
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
-      if (mine + 64 * i < n) {
+      if (there(i)) {
         keys[place[i]] = key[i];
         orders[place[i]] = (uint16_t)order[i];
       }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
-      if (mine + 64 * i < n) {
+      if (there(i)) {
         key[i] = keys[mine + 64 * i];
         order[i] = orders[mine + 64 * i];
       }
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(SortArgs a
   }
 #pragma unroll
   for (int i = 0; i < kItems; ++i)
-    if (mine + 64 * i < n) {
+    if (there(i)) {
       a.key[mine + 64 * i] = key[i];
       a.order[mine + 64 * i] = order[i];
     }
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_place_kernel(SortArgs 
     key[i] = there ? pass_key(a, p, t0 + mine + 64 * i) : 0xFFFFFFFFu;
     order[i] = there && p.order ? p.order[t0 + mine + 64 * i] : (uint32_t)(t0 + mine + 64 * i);
   }
-  digit_places(key, n, p.shift, p.bits, s, place, first_of);
+  digit_places(key, kItems, n, p.shift, p.bits, s, place, first_of);
 #pragma unroll
   for (int i = 0; i < kItems; ++i)
     if (mine + 64 * i < n) {
@@ -285,8 +286,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_place_kernel(SortArgs 
 }
 
 // ---------------------------------------------------------------- sums
-constexpr int kChunk = 32;  // sorted positions
-constexpr int kAhead = 8;   // rows in flight
+constexpr int kChunk = 16;  // sorted positions, whose rows are all on their way at once
 
 struct SumArgs {
   const void* dout;
@@ -297,7 +297,7 @@ struct SumArgs {
   float* dtable;
   float* part;     // [chunks][2][d]: sums that reach past the chunk's first, its last position
   int64_t chunks;
-  int cols;        // workgroups across a row
+  int cols;        // waves across a row, 256 columns each
   uint32_t first;
 };
 
@@ -316,64 +316,80 @@ __device__ __forceinline__ void store_sum(const SumArgs& a, uint32_t id, int col
   store_as<FP8_IN_FP32, WHOLE>(a.dtable, at, left, v);
 }
 
-// One chunk, 1024 columns a workgroup.
+// A chunk and 256 columns a wave.  The chunk's ids and rows are scalars.
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
-  const uint32_t g = a.first + blockIdx.x;
-  const int64_t chunk = g / (uint32_t)a.cols, p0 = chunk * kChunk;
-  const int col = ((int)(g % (uint32_t)a.cols) * 256 + threadIdx.x) * 4, left = (int)a.d - col;
+  const int lane = threadIdx.x & 63;
+  const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t chunk = g / a.cols, p0 = chunk * kChunk;
+  if (chunk >= a.chunks) return;
+  const int col = ((int)(g - chunk * a.cols) * 64 + lane) * 4, left = (int)a.d - col;
   const int n = (int)min((int64_t)kChunk, a.tokens - p0);
-  if (left <= 0) return;
-  const bool from_before = p0 > 0 && a.key[p0 - 1] == a.key[p0];
-  const bool to_after = p0 + n < a.tokens && a.key[p0 + n] == a.key[p0 + n - 1];
+  // lane i: the id at position p0 - 1 + i (none before the first and after the
+  // last position), and the row at p0 + i
+  const int64_t at = p0 - 1 + lane;
+  constexpr uint32_t kNoId = 0xFFFFFFFFu;
+  const uint32_t my_key = lane < n + 2 && at >= 0 && at < a.tokens ? a.key[at] : kNoId;
+  const uint32_t my_row = lane < n ? a.order[p0 + lane] : 0;
+  auto key = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane((int)my_key, i + 1); };
+  Raw<DT> raw[kChunk];
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    raw[i] = Raw<DT>{};
+    const int64_t row = (uint32_t)__builtin_amdgcn_readlane((int)my_row, i);
+    if (i < n && key(i) < (uint32_t)a.vocab && left > 0)
+      raw[i] = load_raw<DT, WHOLE, true>(a.dout, row * a.d + col, left);
+  }
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  int begun = 0;  // position of the run's first row here
-  for (int i0 = 0; i0 < n; i0 += kAhead) {
-    Raw<DT> raw[kAhead];
+  bool from_before = key(-1) == key(0);  // the run goes on from the chunk before
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      raw[i] = Raw<DT>{};
-      if (i0 + i < n && a.key[p0 + i0 + i] < (uint32_t)a.vocab)
-        raw[i] = load_raw<DT, WHOLE, true>(a.dout, (int64_t)a.order[p0 + i0 + i] * a.d + col, left);
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int at = i0 + i;
-      if (at >= n) break;
-      const uint32_t id = a.key[p0 + at];
-      if (id >= (uint32_t)a.vocab) return;  // those left are no tokens
+  for (int i = 0; i < kChunk; ++i) {
+    if (i < n && key(i) < (uint32_t)a.vocab) {
       float v[4];
       unpack<DT>(raw[i], v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] += v[e];
-      const bool last = at + 1 == n;
-      if (!last && a.key[p0 + at + 1] == id) continue;
-      if (begun == 0 && from_before) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk) * a.d + col, left, sum);
-      else if (last && to_after) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk + 1) * a.d + col, left, sum);
-      else store_sum<WHOLE>(a, id, col, left, sum);
-      begun = at + 1;
+      const bool goes_on = key(i + 1) == key(i);
+      if (!goes_on || i + 1 == n) {
+        if (left > 0) {
+          if (from_before) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk) * a.d + col, left, sum);
+          else if (goes_on) store_as<FP8_IN_FP32, WHOLE>(a.part, (2 * chunk + 1) * a.d + col, left, sum);
+          else store_sum<WHOLE>(a, key(i), col, left, sum);
+        }
+        from_before = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = 0.0f;
+        for (int e = 0; e < 4; ++e) sum[e] = 0.0f;
+      }
     }
   }
 }
 
-// Ids whose rows begin in one chunk and end in another: the chunks' sums in order.
+// Ids whose rows begin in one chunk and end in another: the chunks' sums in order,
+// a wave for 256 columns.
 template <bool WHOLE>
 __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs a) {
-  const uint32_t g = a.first + blockIdx.x;
-  const int64_t chunk = g / (uint32_t)a.cols, p0 = chunk * kChunk, p1 = p0 + kChunk;  // (not the last chunk)
-  const int col = ((int)(g % (uint32_t)a.cols) * 256 + threadIdx.x) * 4, left = (int)a.d - col;
+  const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t chunk = g / a.cols, p0 = chunk * kChunk, p1 = p0 + kChunk;
+  if (chunk + 1 >= a.chunks) return;  // nothing goes on from the last one
+  const int col = ((int)(g - chunk * a.cols) * 64 + (int)(threadIdx.x & 63)) * 4, left = (int)a.d - col;
   const uint32_t id = a.key[p1 - 1];
   if (left <= 0 || id >= (uint32_t)a.vocab || a.key[p1] != id) return;
   if (p0 > 0 && a.key[p0 - 1] == id && a.key[p0] == id) return;  // begun in an earlier one
   float sum[4];
   unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, (2 * chunk + 1) * a.d + col, left), sum);
-  for (int64_t c = chunk + 1; c < a.chunks && a.key[c * kChunk] == id; ++c) {
-    float v[4];
-    unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, 2 * c * a.d + col, left), v);
+  constexpr int kAhead = 4;
+  for (int64_t c0 = chunk + 1; c0 < a.chunks && a.key[c0 * kChunk] == id; c0 += kAhead) {
+    Raw<FP8_IN_FP32> raw[kAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    for (int i = 0; i < kAhead; ++i) {
+      raw[i] = Raw<FP8_IN_FP32>{};
+      if (c0 + i < a.chunks && a.key[(c0 + i) * kChunk] == id)
+        raw[i] = load_raw<FP8_IN_FP32, WHOLE, false>(a.part, 2 * (c0 + i) * a.d + col, left);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += raw[i][e];
   }
   store_sum<WHOLE>(a, id, col, left, sum);
 }
@@ -482,9 +498,9 @@ hipError_t launch_embedding_bwd(const EmbeddingGrad& g, void* ws, hipStream_t st
   a.scale = g.scale, a.accumulate = g.accumulate, a.dtable = g.dtable;
   a.part = reinterpret_cast<float*>(w + p.part);
   a.chunks = p.chunks;
-  a.cols = (int)((g.d + 1023) / 1024);
-  auto launch = [&](auto kernel, int64_t groups) {
-    in_stretches(groups, 256, [&](uint32_t first, uint32_t count) {
+  a.cols = (int)((g.d + 255) / 256);
+  auto launch = [&](auto kernel, int64_t waves) {
+    in_stretches((waves + 3) / 4, 256, [&](uint32_t first, uint32_t count) {
       a.first = first;
       hipLaunchKernelGGL(kernel, dim3(count), dim3(256), 0, stream, a);
     });

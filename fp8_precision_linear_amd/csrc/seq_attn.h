@@ -48,10 +48,11 @@ struct SeqAttnArgs {
   uint16_t *dq, *dk, *dv;
   float *lse2, *delta;  // [q_heads][tokens], lse * log2(e) and rowsum(dout * out)
   float *part_k, *part_v;  // [key heads * shares][2][kSeqRows][D]: sums of walks that are cut
+  float* part_q;  // [dq_splits][tokens][q_heads][D]: sums of dq of chunks
+  int dq_chunk, dq_splits;  // key tiles of a chunk, and the most chunks; 0, 1: whole walks
   SeqLine *line, *line_end;  // key tiles of a head; their walks' length, and their number in `seq`
   int most_tiles;  // of `line`
   int shares;      // of a head's line, or 0: a workgroup takes a key tile
-  int64_t share_tiles;  // query tiles of a share, about
   uint32_t dkv_groups;  // workgroups of dk and dv, each
   uint32_t dq_first;    // workgroups of dq, where they come first, or 0
 };
@@ -167,25 +168,29 @@ __device__ __forceinline__ v4i32 bad_of(v8b f) {
 // for NaN and infinities (has_bad: whether any wave found one; the tile's four
 // waves call it together), and what is found is cleared in LDS (clear_bad) once
 // those that do see it have it on record.
-template <int BYTES>
-__device__ __forceinline__ bool has_bad(uint32_t tile, int* found) {
+// GROUPS sets of four waves have a tile each, the last ones perhaps none (`there`).
+template <int BYTES, int GROUPS = 1>
+__device__ __forceinline__ bool has_bad(uint32_t tile, int* found, bool there = true) {
   uint32_t bad = 0;
-  const uint32_t mine = tile + threadIdx.x * 16;
+  const uint32_t mine = tile + (threadIdx.x & 255) * 16;
 #pragma unroll
   for (int i = 0; i < BYTES; i += 4096) {
     const v4i32 w = bad_of(lds_row(mine + i));
     bad |= (uint32_t)(w[0] | w[1] | w[2] | w[3]);
   }
-  const bool any = __any(bad != 0);
+  const bool any = __any(bad != 0) && there;
   if ((threadIdx.x & 63) == 0) found[threadIdx.x >> 6] = any;
   __syncthreads();
-  return (found[0] | found[1] | found[2] | found[3]) != 0;
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < 4 * GROUPS; ++w) all |= found[w];
+  return all != 0;
 }
 // rows: where given, set to 1 for each row of `row_bytes` that held one.
 template <int BYTES>
 __device__ __forceinline__ void clear_bad(uint32_t tile, int row_bytes, int* rows) {
   __syncthreads();  // every wave is done with the tile as it was
-  for (int i = threadIdx.x * 16; i < BYTES; i += 4096) {
+  for (int i = (threadIdx.x & 255) * 16; i < BYTES; i += 4096) {
     v4i32 w = __builtin_bit_cast(v4i32, lds_row(tile + i));
     const v4i32 bad = bad_of(__builtin_bit_cast(v8b, w));
     w &= ~bad;

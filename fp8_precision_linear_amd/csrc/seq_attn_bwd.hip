@@ -13,8 +13,9 @@
 // tile where there are enough of them.  Otherwise -- few key heads, short
 // batches -- the tiles' walks over the queries, of very different lengths under a
 // causal mask, are laid one behind the other for each key head and cut into
-// equal shares, one for each workgroup that runs at the same time; a cut walk's
-// partial sums are joined in order by a last kernel.
+// equal shares, one for each workgroup that runs at the same time, and the rows'
+// walks over the keys into chunks; a cut walk's partial sums are joined in order
+// by a last kernel.
 //
 // Both kinds run in one launch, behind a small one that leaves -lse log2(e) and
 // -delta of every row and head.
@@ -129,6 +130,20 @@ struct GradShared {
   int found[4];
 };
 
+// The keys that rows [row0, row0 + kSeqRows) read, and the chunks of them.
+struct KeySpan {
+  int lo, hi, chunks;
+};
+template <int D>
+__device__ __forceinline__ KeySpan keys_of(const SeqAttnArgs& a, int n, int row0) {
+  constexpr int kKeys = kQueriesOf<D>;
+  KeySpan r;
+  r.hi = a.causal ? min(n, row0 + kSeqRows) : n;
+  r.lo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
+  r.chunks = a.dq_chunk > 0 ? ((r.hi - r.lo + kKeys - 1) / kKeys + a.dq_chunk - 1) / a.dq_chunk : 1;
+  return r;
+}
+
 template <int D>
 __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& lds, uint32_t x) {
   constexpr int J = D / 16, DT = D / 32, kKeys = GradShared<D>::kRows, SUB = kSubs<D>, kStep = 32 * SUB;
@@ -142,11 +157,15 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
   x /= a.heads;
   const int head = kv_head * a.group + x % a.group;
   x /= a.group;
+  const int chunk = x % a.dq_splits;
+  x /= a.dq_splits;
   const Seq s = seq_of(a, x % a.batch);
   const int row0 = (a.tiles - 1 - (int)(x / a.batch)) * kSeqRows;  // late rows see most: first
   if (row0 >= s.n) return;
-  const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
-  const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
+  const KeySpan span = keys_of<D>(a, s.n, row0);
+  if (chunk >= span.chunks) return;
+  const int klo = span.lo + chunk * a.dq_chunk * kKeys;
+  const int khi = span.chunks == 1 ? span.hi : min(span.hi, klo + a.dq_chunk * kKeys);
 
   const uint32_t ring0 = lds_addr(lds.ring);
   const int64_t ks = a.k_stride * 2, vs = a.v_stride * 2;
@@ -260,6 +279,16 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
   }
 
   if (row >= s.n) return;
+  if (span.chunks > 1) {
+    float* part = a.part_q + (((int64_t)chunk * a.tokens + s.first + row) * a.q_heads + head) * D + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<v4f*>(part + 32 * d + 8 * u) =
+            v4f{dq[d][4 * u], dq[d][4 * u + 1], dq[d][4 * u + 2], dq[d][4 * u + 3]};
+    return;
+  }
   uint16_t* to = a.dq + (int64_t)(s.first + row) * a.dq_stride + head * D;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -507,12 +536,42 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_grad_kernel(Se
   dq_group<D>(a, lds, x);
 }
 
+// dq of rows whose keys were cut, chunk by chunk; x counts (part of a tile, head).
+template <int D>
+__device__ __forceinline__ void join_dq(const SeqAttnArgs& a, uint32_t x) {
+  constexpr int kRows = 1024 / D, kParts = kSeqRows / kRows;
+  const int head = x % a.q_heads;
+  x /= a.q_heads;
+  const int at = x / kParts, d = 4 * (threadIdx.x % (D / 4));
+  if (at >= a.line_end->seq) return;
+  const SeqLine tile = a.line[at];
+  const Seq s = seq_of(a, tile.seq);
+  const int chunks = keys_of<D>(a, s.n, tile.k0).chunks, row = tile.k0 + (x % kParts) * kRows + threadIdx.x / (D / 4);
+  if (chunks == 1 || row >= s.n) return;
+  const int64_t step = (int64_t)a.tokens * a.q_heads * D, token = s.first + row;
+  const float* from = a.part_q + (token * a.q_heads + head) * D + d;
+  v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c = 0; c < chunks; c += 4) {
+    v4f p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const v4f*>(from + min(c + i, chunks - 1) * step);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < chunks) sum += p[i];
+  }
+  sum *= a.scale;
+  *reinterpret_cast<uint2*>(a.dq + token * a.dq_stride + head * D + d) =
+      make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
+}
+
 // Adds the sums of the key tiles whose walks were cut, share by share: a lane
 // four dimensions of a key.
 template <int D>
 __global__ __launch_bounds__(256) void seq_attn_join_kernel(SeqAttnArgs a) {
   constexpr int kKeys = 1024 / D, kParts = kSeqRows / kKeys;
   uint32_t x = a.first + blockIdx.x;
+  const uint32_t dkv = (uint32_t)a.most_tiles * a.heads * kParts;
+  if (x >= dkv) return join_dq<D>(a, x - dkv);
   const int kv_head = x % a.heads;
   x /= a.heads;
   const int at = x / kParts, key = (int)(x % kParts) * kKeys + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
@@ -554,39 +613,48 @@ __global__ __launch_bounds__(256) void seq_attn_join_kernel(SeqAttnArgs a) {
       make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-// Fewest query tiles of a share (were every query to see every key).
-constexpr int64_t kLeastShare = 8;
+// Fewest query tiles of a share (were every query to see every key), and fewest
+// key tiles of a chunk of dq.
+constexpr int64_t kLeastShare = 8, kLeastChunk = 6;
 
 // From the shape alone, so that the workspace does not depend on the mask.
 struct BwdPlan {
-  int most_tiles, shares;  // shares 0: whole key tiles
-  int64_t share_tiles;     // query tiles of a share, about
-  int64_t stat, part, line, bytes;  // bytes of each
+  int64_t most_tiles;
+  int shares;            // 0: whole key tiles
+  int64_t share_tiles;   // query tiles of a share, about
+  int chunk, splits;     // key tiles of a chunk of dq, and the most of them; 0, 1: whole
+  int64_t stat, part, part_q, line, bytes;  // bytes of each
 };
 BwdPlan plan_of(const SeqAttnShape& s) {
-  BwdPlan p;
+  BwdPlan p{};
   const int64_t tiles = (s.max_len + kSeqRows - 1) / kSeqRows;
-  p.most_tiles = (int)std::min((int64_t)s.tokens / kSeqRows + s.batch, tiles * s.batch);
+  p.most_tiles = std::min((int64_t)s.tokens / kSeqRows + s.batch, tiles * s.batch);
   // Workgroups that run at once on 256 CUs.  Twice as many key tiles: one each,
   // whose neighbours walk the same queries at the same time (four sequences of
   // 4096, 32 heads: tiles 2086 us, shares 2356).
   const int64_t resident = s.head_dim == 256 ? 256 : 512, queries = s.head_dim == 256 ? 32 : 64;
-  const int64_t work = p.most_tiles * ((s.max_len + queries - 1) / queries) * (s.q_heads / s.heads);
-  p.shares = 0;
-  p.share_tiles = 0;
-  if (p.most_tiles * (int64_t)s.heads < 2 * resident)
+  const int64_t length = (s.max_len + queries - 1) / queries, work = p.most_tiles * length * (s.q_heads / s.heads);
+  p.splits = 1;
+  if (p.most_tiles * s.heads < 2 * resident) {
     p.shares = (int)std::max<int64_t>(1, std::min(resident / s.heads, work / kLeastShare));
-  if (p.shares > 0) p.share_tiles = work / p.shares;
+    p.share_tiles = work / p.shares;
+    const int64_t splits = std::min(2 * resident / (p.most_tiles * s.q_heads), length / kLeastChunk);
+    if (splits > 1) {
+      p.chunk = (int)((length + splits - 1) / splits);
+      p.splits = (int)((length + p.chunk - 1) / p.chunk);
+    }
+  }
   auto aligned = [](int64_t bytes) { return (bytes + 255) & ~(int64_t)255; };
   p.stat = aligned((int64_t)s.tokens * s.q_heads * 4);
   p.part = (int64_t)p.shares * s.heads * 2 * kSeqRows * s.head_dim * 4;
-  p.line = aligned(((int64_t)p.most_tiles + 1) * (int64_t)sizeof(SeqLine));
-  p.bytes = 2 * p.stat + 2 * p.part + p.line;
+  p.part_q = p.splits > 1 ? (int64_t)p.splits * s.tokens * s.q_heads * s.head_dim * 4 : 0;
+  p.line = aligned((p.most_tiles + 1) * (int64_t)sizeof(SeqLine));
+  p.bytes = 2 * p.stat + 2 * p.part + p.part_q + p.line;
   return p;
 }
 
 template <int D>
-void run_bwd(SeqAttnArgs& a, hipStream_t stream) {
+void run_bwd(SeqAttnArgs& a, int64_t share_tiles, hipStream_t stream) {
   auto launch = [&](auto kernel, int64_t groups) {
     in_stretches(groups, 256, [&](uint32_t first, uint32_t count) {
       a.first = first;
@@ -596,11 +664,14 @@ void run_bwd(SeqAttnArgs& a, hipStream_t stream) {
   launch(seq_attn_stats_kernel<D>, ((int64_t)a.tokens * a.q_heads * (D / 8) + 255) / 256 + (a.shares > 0));
   const int64_t tiles = (int64_t)a.tiles * a.batch;
   const int64_t dkv = a.shares > 0 ? (int64_t)a.heads * a.shares : tiles * a.heads;
-  const int64_t dq = tiles * a.q_heads;
+  const int64_t dq = tiles * a.q_heads * a.dq_splits;
+  const int64_t dq_tiles = a.dq_chunk > 0 ? a.dq_chunk : (a.max_len + kQueriesOf<D> - 1) / kQueriesOf<D>;
   a.dkv_groups = (uint32_t)dkv;
-  a.dq_first = a.share_tiles > 0 && a.share_tiles < (a.max_len + kQueriesOf<D> - 1) / kQueriesOf<D> ? (uint32_t)dq : 0;
+  a.dq_first = a.shares > 0 && share_tiles < dq_tiles ? (uint32_t)dq : 0;
   launch(seq_attn_grad_kernel<D>, (D == 256 ? 2 : 1) * dkv + dq);
-  if (a.shares > 1) launch(seq_attn_join_kernel<D>, (int64_t)a.most_tiles * a.heads * (kSeqRows * D / 1024));
+  const int64_t joins = (int64_t)a.most_tiles * (kSeqRows * D / 1024);
+  if (a.shares > 1 || a.dq_splits > 1)
+    launch(seq_attn_join_kernel<D>, joins * a.heads + (a.dq_splits > 1 ? joins * a.q_heads : 0));
 }
 
 }  // namespace
@@ -610,8 +681,9 @@ int64_t seq_attn_bwd_workspace_bytes(const SeqAttnShape& s) { return plan_of(s).
 hipError_t launch_seq_attn_bwd(SeqAttnArgs a, int head_dim, void* ws, hipStream_t stream) {
   const BwdPlan p = plan_of({a.batch, a.tokens, a.max_len, a.q_heads, a.heads, head_dim});
   a.shares = p.shares;
-  a.share_tiles = p.share_tiles;
-  a.most_tiles = p.most_tiles;
+  a.dq_chunk = p.chunk;
+  a.dq_splits = p.splits;
+  a.most_tiles = (int)p.most_tiles;
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
   uint8_t* at = static_cast<uint8_t*>(ws);
   auto take = [&](int64_t bytes) {
@@ -625,9 +697,10 @@ hipError_t launch_seq_attn_bwd(SeqAttnArgs a, int head_dim, void* ws, hipStream_
   a.delta = reinterpret_cast<float*>(take(p.stat));
   a.part_k = reinterpret_cast<float*>(take(p.part));
   a.part_v = reinterpret_cast<float*>(take(p.part));
-  if (head_dim == 64) run_bwd<64>(a, stream);
-  else if (head_dim == 128) run_bwd<128>(a, stream);
-  else run_bwd<256>(a, stream);
+  a.part_q = reinterpret_cast<float*>(take(p.part_q));
+  if (head_dim == 64) run_bwd<64>(a, p.share_tiles, stream);
+  else if (head_dim == 128) run_bwd<128>(a, p.share_tiles, stream);
+  else run_bwd<256>(a, p.share_tiles, stream);
   return hipGetLastError();
 }
 

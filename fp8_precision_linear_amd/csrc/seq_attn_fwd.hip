@@ -5,6 +5,12 @@
 // values go through LDS by DMA, the next one on its way while one is consumed.
 // Logits against a reference that follows the row maximum lazily: it moves when
 // a tile's probabilities outgrow it, so most tiles rescale nothing.
+//
+// Where the workgroups would leave CUs without work, eight waves take the 128
+// rows: two sets of four, each with every other tile of the keys, joined in LDS
+// at the end.
+#include <algorithm>
+
 #include "seq_attn.h"
 
 namespace fp8lin {
@@ -20,14 +26,16 @@ constexpr float kMostPart = 0x1p16f;
 // (attn_common.h).
 constexpr float kHuge = 0x1p22f;
 
-template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(SeqAttnArgs a) {
+// SETS of four waves.
+template <int D, int SETS>
+__global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(SeqAttnArgs a) {
   constexpr int J = D / 16, DT = D / 32, kKeys = kKeysOf<D>, SUB = kKeys / 32;
   using Load = TileLoad<D, kKeys>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][Load::kBytes];  // [buffer][keys, values]
-  __shared__ int found[4];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[SETS][2][2][Load::kBytes];  // [set][buffer][keys, values]
+  __shared__ int found[4 * SETS];
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave = all_waves & 3, set = SETS == 1 ? 0 : all_waves >> 2;
   const int r32 = lane & 31, h = lane >> 5;
   uint32_t x = a.first + blockIdx.x;
   const int kv_head = x % a.heads;
@@ -39,6 +47,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
   if (row0 >= s.n) return;
   const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
   const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
+
+  const uint32_t ring0 = lds_addr(ring[set]);
+  const int64_t ks = a.k_stride * 2, vs = a.v_stride * 2;
+  const Load load_k(lane, wave, (uint32_t)ks), load_v(lane, wave, (uint32_t)vs);
+  const uint16_t* kp = a.k + (int64_t)(s.first + klo) * a.k_stride + kv_head * D;
+  const uint16_t* vp = a.v + (int64_t)(s.first + klo) * a.v_stride + kv_head * D;
+  auto issue = [&](int T, int buf) {
+    load_k.issue(kp + (int64_t)(T - klo) * a.k_stride, ks, s.n - T, ring0 + buf * 2 * Load::kBytes, wave);
+    load_v.issue(vp + (int64_t)(T - klo) * a.v_stride, vs, s.n - T, ring0 + (2 * buf + 1) * Load::kBytes, wave);
+  };
+  const int first_key = klo + set * kKeys;
+  if (first_key < khi) issue(first_key, 0);
 
   const int wrow = row0 + 32 * wave, row = wrow + r32;
   v8b q[J];
@@ -65,15 +85,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
   float m = kNoRef, l = 0.0f;
   bool huge = false;
 
-  const uint32_t ring0 = lds_addr(ring);
-  const int64_t ks = a.k_stride * 2, vs = a.v_stride * 2;
-  const Load load_k(lane, wave, (uint32_t)ks), load_v(lane, wave, (uint32_t)vs);
-  const uint16_t* kp = a.k + (int64_t)(s.first + klo) * a.k_stride + kv_head * D;
-  const uint16_t* vp = a.v + (int64_t)(s.first + klo) * a.v_stride + kv_head * D;
-  auto issue = [&](int T, int buf) {
-    load_k.issue(kp + (int64_t)(T - klo) * a.k_stride, ks, s.n - T, ring0 + buf * 2 * Load::kBytes, wave);
-    load_v.issue(vp + (int64_t)(T - klo) * a.v_stride, vs, s.n - T, ring0 + (2 * buf + 1) * Load::kBytes, wave);
-  };
   const uint32_t krow = row_place<D>(lane), vcol = column_place<D>(lane);
 
   auto consume = [&](bool masked, int T, uint32_t tile) {
@@ -184,24 +195,49 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
     }
   };
 
-  issue(klo, 0);
   int buf = 0;
-  for (int T = klo; T < khi; T += kKeys, buf ^= 1) {
+  for (int all = klo; all < khi; all += SETS * kKeys, buf ^= 1) {
+    const int T = all + set * kKeys;
     wait_vmcnt<0>();
     bare_barrier();  // this tile is whole, and every wave is done with the one before
-    if (T + kKeys < khi) issue(T + kKeys, buf ^ 1);
+    if (T + SETS * kKeys < khi) issue(T + SETS * kKeys, buf ^ 1);
     const uint32_t tile = ring0 + buf * 2 * Load::kBytes;
-    if (T + kKeys > all_hi || T < all_lo) {
+    if (all + SETS * kKeys > all_hi || all < all_lo) {
       const uint32_t values = tile + Load::kBytes;
-      if (has_bad<Load::kBytes>(values, found)) {
-        record(T, values);
+      if (has_bad<Load::kBytes, SETS>(values, found, T < khi)) {
+        if (T < khi) record(T, values);
         clear_bad<Load::kBytes>(values, 2 * D, nullptr);
       }
     }
-    if (T >= whi || T + kKeys <= wlo) continue;
+    if (T >= min(whi, khi) || T + kKeys <= wlo) continue;
     // (rows past the sequence's end see what its last row sees: not stored)
     const bool whole = T + kKeys <= min(s.n, a.causal ? wrow + 1 : s.n) && (!a.window || T > wrow + 31 - a.window);
     consume(!whole, T, tile);
+  }
+
+  if constexpr (SETS > 1) {
+    // the second set's rows to LDS, lane by lane; the first set's waves add them
+    static_assert(SETS == 2 && sizeof(ring) >= 4 * 64 * (16 * DT + 2) * 4, "a set's state fits the ring");
+    float* const state = reinterpret_cast<float*>(&ring[0][0][0][0]) + wave * 64 * (16 * DT + 2) + lane;
+    __syncthreads();
+    if (set == 1) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) state[64 * (16 * d + e)] = o[d][e];
+      state[64 * 16 * DT] = m;
+      state[64 * (16 * DT + 1)] = l;
+    }
+    __syncthreads();
+    if (set == 1) return;
+    const float m1 = state[64 * 16 * DT], to = m1 > m ? m1 : m;
+    const float f0 = __builtin_amdgcn_exp2f(m - to), f1 = __builtin_amdgcn_exp2f(m1 - to);
+    m = to;
+    l = l * f0 + state[64 * (16 * DT + 1)] * f1;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f0 + state[64 * (16 * d + e)] * f1;
   }
 
   l = swap32_sum(l);
@@ -225,12 +261,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(Seq
 
 hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) {
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
-  in_stretches((int64_t)a.tiles * a.batch * a.q_heads, 256, [&](uint32_t first, uint32_t count) {
-    a.first = first;
-    if (head_dim == 64) hipLaunchKernelGGL(seq_attn_fwd_kernel<64>, dim3(count), dim3(256), 0, stream, a);
-    else if (head_dim == 128) hipLaunchKernelGGL(seq_attn_fwd_kernel<128>, dim3(count), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(seq_attn_fwd_kernel<256>, dim3(count), dim3(256), 0, stream, a);
-  });
+  const int64_t groups = (int64_t)a.tiles * a.batch * a.q_heads;
+  // Two sets where a workgroup has a CU to itself (256 CUs) and more than one
+  // tile: two sequences of 1024, 12 heads of 64.
+  const int64_t busy = std::min(groups, ((int64_t)a.tokens / kSeqRows + a.batch) * a.q_heads);
+  const bool two = busy <= 256 && a.max_len > 64 && head_dim != 256;
+  auto launch = [&](auto kernel, int threads) {
+    in_stretches(groups, threads, [&](uint32_t first, uint32_t count) {
+      a.first = first;
+      hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, stream, a);
+    });
+  };
+  if (head_dim == 64) two ? launch(seq_attn_fwd_kernel<64, 2>, 512) : launch(seq_attn_fwd_kernel<64, 1>, 256);
+  else if (head_dim == 128) two ? launch(seq_attn_fwd_kernel<128, 2>, 512) : launch(seq_attn_fwd_kernel<128, 1>, 256);
+  else launch(seq_attn_fwd_kernel<256, 1>, 256);
   return hipGetLastError();
 }
 

@@ -37,7 +37,7 @@ extern "C" {
  *              bytes.  The call overwrites it and keeps no pointer; calls in
  *              flight at the same time need separate ones.
  * Tokens are sorted by id, stably, and an id's rows are added in their order
- * in fp32, in runs of at most 64 whose sums are added in their order: same
+ * in fp32, in runs of at most 16 whose sums are added in their order: same
  * inputs, same bits.  vocab < 2^31, tokens < 2^31 - 2^16.
  */
 int fp8_embedding_fwd(const void* ids, int32_t id_bits, int64_t tokens, const void* table, fp8_dtype_t table_dtype,
