@@ -38,10 +38,14 @@ struct QkArgs {
   int64_t dq_stride, dk_stride, dv_stride;
   void* dx;
   float* part;  // [workgroups][2][D]
+  int64_t run;  // items of a workgroup
   uint32_t first;
 };
 
-constexpr int kSteps = 4;  // most of an item: loads in flight
+// Most steps of an item, whose loads are in flight together.  The backward pass
+// holds two tensors and twelve sums beside them: two steps leave four waves a SIMD
+// (4095 tokens of 120 heads of 128: four steps 134 us, two 126).
+constexpr int kSteps = 4, kBwdSteps = 2;
 
 // The sum over the LANES lanes of a head, in every one of them.
 template <int LANES>
@@ -134,6 +138,7 @@ __global__ __launch_bounds__(256) void qk_norm_fwd_kernel(QkArgs a) {
 // the heads that its wave meets, the workgroup adds its lanes in LDS.
 template <int DT, int D, int ROPE, bool NORM>
 __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkArgs a) {
+  constexpr int kSteps = kBwdSteps;
   constexpr int kLanes = D / 8, kHeads = 64 / kLanes;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, u = lane % kLanes;
   const int all = a.q_heads + 2 * a.heads;
@@ -144,8 +149,9 @@ __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkArgs a) {
     load_weights<D>(a, a.wq, u, wq);
     load_weights<D>(a, a.wk, u, wk);
   }
-  const int64_t stride = (int64_t)gridDim.x * 4;
-  for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < a.all_items; i += stride) {
+  // a run of the items, which its waves take in turn
+  const int64_t begin = (int64_t)blockIdx.x * a.run, end = min(begin + a.run, a.all_items);
+  for (int64_t i = begin + wave; i < end; i += 4) {
     const Item it = item_of(a, i);
     auto head_of = [&](int s) { return (64 * (it.step0 + s) + lane) / kLanes; };
     float v[kSteps][8], g[kSteps][8], angle[8];
@@ -239,18 +245,32 @@ __global__ __launch_bounds__(256) void qk_norm_bwd_kernel(QkArgs a) {
 }
 
 // dwq and dwk: the workgroups' shares added in 64 bits, in order.  A workgroup
-// of 256 takes 16 columns, 16 lanes each.
+// takes 16 columns: four lanes of four columns, 64 of them down the rows, eight
+// rows of each on their way at once.
 __global__ __launch_bounds__(256) void qk_norm_dw_kernel(const float* part, int rows, int D, float* dwq, float* dwk) {
-  __shared__ double sums[16][16];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), lane = threadIdx.x >> 4;
-  double s = 0.0;
-  for (int r = lane; r < rows; r += 16) s += (double)part[(int64_t)r * 2 * D + col];
-  sums[lane][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (lane == 0) {
-    for (int r = 1; r < 16; ++r) s += sums[r][threadIdx.x];
-    (col < D ? dwq : dwk)[col % D] = (float)s;
+  __shared__ double sums[64][17];
+  const int quad = threadIdx.x & 3, lane = threadIdx.x >> 2, col = blockIdx.x * 16 + 4 * quad;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int r0 = lane; r0 < rows; r0 += 64 * 8) {
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 64 * i;
+      v[i] = r < rows ? *reinterpret_cast<const float4*>(part + (int64_t)r * 2 * D + col) : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[0] += v[i].x, s[1] += v[i].y, s[2] += v[i].z, s[3] += v[i].w;
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[lane][4 * quad + e] = s[e];
+  __syncthreads();
+  // 16 lanes a column, then across them
+  const int c = threadIdx.x >> 4, part_of = threadIdx.x & 15;
+  double t = (sums[part_of][c] + sums[part_of + 16][c]) + (sums[part_of + 32][c] + sums[part_of + 48][c]);
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) t += __shfl_xor(t, off, 64);
+  const int to = blockIdx.x * 16 + c;
+  if (part_of == 0) (to < D ? dwq : dwk)[to % D] = (float)t;
 }
 
 template <typename F>
@@ -275,7 +295,7 @@ void for_kind(const QkProblem& p, F&& f) {
   else turned(integral_constant<int, 256>{});
 }
 
-QkArgs args_of(const QkProblem& p) {
+QkArgs args_of(const QkProblem& p, int most_steps) {
   QkArgs a{};
   a.x = p.x, a.x_stride = p.x_stride;
   a.wq = p.wq, a.wk = p.wk, a.w_dtype = p.w_dtype, a.eps = p.eps;
@@ -283,22 +303,29 @@ QkArgs args_of(const QkProblem& p) {
   a.rope = {p.cos, p.sin, p.rope_rows};
   a.tokens = p.tokens, a.q_heads = p.q_heads, a.heads = p.kv_heads;
   a.steps = (int)(((int64_t)(p.q_heads + 2 * p.kv_heads) * (p.head_dim / 8) + 63) / 64);
-  a.items = (a.steps + kSteps - 1) / kSteps;
+  a.items = (a.steps + most_steps - 1) / most_steps;
   a.per = (a.steps + a.items - 1) / a.items;
   a.items = (a.steps + a.per - 1) / a.per;
   a.all_items = p.tokens * a.items;
   return a;
 }
 
-// Workgroups of the backward kernel: as many as run at once, each with a share
-// of the weights' gradients to join.
-constexpr int64_t kBwdGroups = 1024;
-int64_t bwd_groups(const QkArgs& a) { return std::max<int64_t>(1, std::min(kBwdGroups, (a.all_items + 3) / 4)); }
+// Items of a workgroup of the backward kernel, whose share of the weights'
+// gradients is joined with the others': few where there are few items, so that
+// every CU has work (2048 tokens of 36 heads of 64, 8 and 16 items 25-26 us, 64 38);
+// otherwise 32 (4095 tokens of 120 heads of 128: 16 items 135 us, 32 126, and a
+// resident grid that strides over them 141), and no more than kMostGroups shares.
+constexpr int64_t kLeastRun = 4, kMostRun = 32, kWantGroups = 512, kMostGroups = 16384;
+int64_t run_of(const QkArgs& a) {
+  const int64_t run = std::max(kLeastRun, std::min(kMostRun, a.all_items / kWantGroups & ~(int64_t)3));
+  return std::max(run, (a.all_items + kMostGroups - 1) / kMostGroups);
+}
+int64_t bwd_groups(const QkArgs& a) { return std::max<int64_t>(1, (a.all_items + run_of(a) - 1) / run_of(a)); }
 
 }  // namespace
 
 hipError_t launch_qk_norm_fwd(const QkProblem& p, uint16_t* y, hipStream_t stream) {
-  QkArgs a = args_of(p);
+  QkArgs a = args_of(p, kSteps);
   a.y = y;
   in_stretches((a.all_items + 3) / 4, 256, [&](uint32_t first, uint32_t count) {
     a.first = first;
@@ -311,14 +338,15 @@ hipError_t launch_qk_norm_fwd(const QkProblem& p, uint16_t* y, hipStream_t strea
   return hipGetLastError();
 }
 
-int64_t qk_norm_bwd_workspace_bytes(const QkProblem& p) { return bwd_groups(args_of(p)) * 2 * p.head_dim * 4; }
+int64_t qk_norm_bwd_workspace_bytes(const QkProblem& p) { return bwd_groups(args_of(p, kBwdSteps)) * 2 * p.head_dim * 4; }
 
 hipError_t launch_qk_norm_bwd(const QkProblem& p, const QkGrads& g, float* ws, hipStream_t stream) {
-  QkArgs a = args_of(p);
+  QkArgs a = args_of(p, kBwdSteps);
   a.dq = g.dq, a.dk = g.dk, a.dv = g.dv;
   a.dq_stride = g.dq_stride, a.dk_stride = g.dk_stride, a.dv_stride = g.dv_stride;
   a.dx = g.dx;
   a.part = ws;
+  a.run = run_of(a);
   const int groups = (int)bwd_groups(a);
   for_kind(p, [&](auto dt, auto d, auto rope, auto norm) {
     hipLaunchKernelGGL((qk_norm_bwd_kernel<decltype(dt)::value, decltype(d)::value, decltype(rope)::value,

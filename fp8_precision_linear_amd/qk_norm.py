@@ -71,7 +71,7 @@ def qk_norm_rope_fwd(qkv, q_heads, kv_heads, wq=None, wk=None, eps=1e-5, rope=No
     else:
         out = _empty(qkv.shape, torch.bfloat16, qkv.device, stream)
     _check("fp8_qk_norm_rope_fwd", lib.fp8_qk_norm_rope_fwd(*args, out.data_ptr(), _stream(stream)))
-    return out[:, :q_heads], out[:, q_heads:q_heads + kv_heads], out[:, q_heads + kv_heads:]
+    return out.split_with_sizes((q_heads, kv_heads, kv_heads), 1)   # one call: half the time of three slices
 
 
 def qk_norm_rope_bwd_workspace_bytes(tokens, q_heads, kv_heads, head_dim):
@@ -111,8 +111,11 @@ def qk_norm_rope_bwd(dq, dk, dv, qkv, wq=None, wk=None, eps=1e-5, rope=None, pos
         for t, name in ((dwq, "dwq"), (dwk, "dwk")):
             if t is not None:
                 _need(t, name, torch.float32, dev, shape=(D,))
-        dwq = _empty((D,), torch.float32, dev, stream) if dwq is None else dwq
-        dwk = _empty((D,), torch.float32, dev, stream) if dwk is None else dwk
+        if dwq is None and dwk is None:
+            dwq, dwk = _empty((2, D), torch.float32, dev, stream).unbind()
+        else:
+            dwq = _empty((D,), torch.float32, dev, stream) if dwq is None else dwq
+            dwk = _empty((D,), torch.float32, dev, stream) if dwk is None else dwk
         if workspace is not None:
             _need_place(workspace, "workspace", dev)
         else:

@@ -129,7 +129,8 @@ def attention_bwd_workspace_bytes(seqs, q_heads, kv_heads, head_dim):
 
 def attention_bwd(dout, q, k, v, out, lse, seqs, scale=None, causal=True, window=0, dq=None, dk=None, dv=None,
                   workspace=None, stream=None):
-    """(dq, dk, dv) bf16 of attention_fwd's out (fp8_attention_bwd).  dq, dk, dv:
+    """(dq, dk, dv) bf16 of attention_fwd's out (fp8_attention_bwd), by default
+    views of one [tokens, q_heads + 2 kv_heads, head_dim] tensor.  dq, dk, dv:
     optional outputs, rows any stride apart (slices of one tensor's rows).
     workspace: optional device tensor of at least
     attention_bwd_workspace_bytes(...) bytes, otherwise from torch's allocator."""
@@ -138,6 +139,8 @@ def attention_bwd(dout, q, k, v, out, lse, seqs, scale=None, causal=True, window
     gs = _rows(dout, "dout", seqs, Hq, D, dev)
     _need(out, "out", torch.bfloat16, dev, shape=(T, Hq, D))
     _need(lse, "lse", torch.float32, dev, shape=(T, Hq))
+    if dq is None and dk is None and dv is None and (Hq + 2 * H) * D <= MAX_STRIDE:   # one tensor's heads
+        dq, dk, dv = _empty((T, Hq + 2 * H, D), torch.bfloat16, dev, stream).split_with_sizes((Hq, H, H), 1)
     grads, strides = [], []
     for t, name, heads in ((dq, "dq", Hq), (dk, "dk", H), (dv, "dv", H)):
         t = _empty((T, heads, D), torch.bfloat16, dev, stream) if t is None else t
