@@ -95,12 +95,14 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
     v16f t[SUB];
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub) t[sub] = zero16();
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub) t[sub] = mma(lds_row(((tile + krow) ^ (32 * j)) + sub * 64 * D), q[j], t[sub]);
       if (D > 64 && j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // LDS reads do not run further ahead: registers
     }
+    __builtin_amdgcn_s_setprio(0);
     if (masked) {
       asm volatile("");  // a branch: as selects it would cost every tile
 #pragma unroll
@@ -157,12 +159,14 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
     l += part;
     if (D > 64) __builtin_amdgcn_sched_barrier(0);
     const uint32_t v = tile + Load::kBytes + vcol;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int c = 0; c < 2 * SUB; ++c) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] = mma(column_step<D>(v + c * 32 * D, d), p[c >> 1][c & 1], o[d]);
       if (D > 64 && (c & 1)) __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   // Values of a tile that are NaN or infinite: the outputs of the rows that see
