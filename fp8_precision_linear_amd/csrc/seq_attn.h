@@ -23,9 +23,11 @@
 
 namespace fp8lin {
 
-// A key tile: its walk's start on the head's line, its sequence and first key.
+// A tile of kSeqRows keys, or rows: where its walk over the queries starts on the
+// head's line of key tiles and its walk over the keys on that of row tiles, its
+// sequence and first position.
 struct SeqLine {
-  int64_t start;
+  int64_t start, start_q;
   int seq, k0;
 };
 
@@ -47,12 +49,11 @@ struct SeqAttnArgs {
   int64_t dout_stride, dq_stride, dk_stride, dv_stride;
   uint16_t *dq, *dk, *dv;
   float *lse2, *delta;  // [q_heads][tokens], lse * log2(e) and rowsum(dout * out)
-  float *part_k, *part_v;  // [key heads * shares][2][kSeqRows][D]: sums of walks that are cut
-  float* part_q;  // [dq_splits][tokens][q_heads][D]: sums of dq of chunks
-  int dq_chunk, dq_splits;  // key tiles of a chunk, and the most chunks; 0, 1: whole walks
-  SeqLine *line, *line_end;  // key tiles of a head; their walks' length, and their number in `seq`
+  // sums of walks that are cut: [workgroups of that kind][2][kSeqRows][D]
+  float *part_k, *part_v, *part_q;
+  SeqLine *line, *line_end;  // tiles of a head; the lines' lengths, and the tiles' number in `seq`
   int most_tiles;  // of `line`
-  int shares;      // of a head's line, or 0: a workgroup takes a key tile
+  int shares, row_shares;  // of a head's line of key tiles, of row tiles; 0: a workgroup takes a tile
   uint32_t dkv_groups;  // workgroups of dk and dv, each
   uint32_t dq_first;    // workgroups of dq, where they come first, or 0
 };
@@ -115,14 +116,17 @@ struct TileLoad {
   static constexpr int kBytes = ROWS * D * 2;
   static constexpr int kLoads = kBytes / 4096;  // of each wave
   static constexpr int kStep = 2048 / D;        // rows between a wave's loads
-  uint32_t lane_row, chunk[2], offset[2];       // by the parity of the load (D = 256: another swizzle)
+  // loads of odd and even number, where their rows are swizzled differently
+  static constexpr int kKinds = D == 256 ? 2 : 1;
+  uint32_t offset[kKinds];
+  static __device__ __forceinline__ uint32_t row_of(int lane, int wave) { return wave * (512 / D) + lane / (D / 8); }
+  static __device__ __forceinline__ uint32_t chunk_of(int lane, uint32_t row) {
+    return ((lane % (D / 8)) ^ swz<D>(row)) * 16;
+  }
   __device__ __forceinline__ TileLoad(int lane, int wave, uint32_t stride_bytes) {
-    lane_row = wave * (512 / D) + lane / (D / 8);
+    const uint32_t row = row_of(lane, wave);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      chunk[p] = ((lane % (D / 8)) ^ swz<D>(lane_row + p * kStep)) * 16;
-      offset[p] = lane_row * stride_bytes + chunk[p];
-    }
+    for (int p = 0; p < kKinds; ++p) offset[p] = row * stride_bytes + chunk_of(lane, row + p * kStep);
   }
   // base: row 0 of the tile; left: rows there are (at least one)
   __device__ __forceinline__ void issue(const uint16_t* base, int64_t stride_bytes, int left, uint32_t lds,
@@ -131,12 +135,14 @@ struct TileLoad {
     if (left >= ROWS) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        dma16(p + (int64_t)(i * kStep) * stride_bytes, offset[i & 1], lds + (wave + 4 * i) * 1024);
+        dma16(p + (int64_t)(i * kStep) * stride_bytes, offset[i % kKinds], lds + (wave + 4 * i) * 1024);
     } else {
+      const int lane = threadIdx.x & 63;
+      const uint32_t row = row_of(lane, wave);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const uint32_t r = min((int)lane_row + i * kStep, left - 1);
-        dma16(p, r * (uint32_t)stride_bytes + chunk[i & 1], lds + (wave + 4 * i) * 1024);
+        const uint32_t r = min((int)row + i * kStep, left - 1);
+        dma16(p, r * (uint32_t)stride_bytes + chunk_of(lane, row + (i % kKinds) * kStep), lds + (wave + 4 * i) * 1024);
       }
     }
   }
