@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = zero16();
   float m = kNoRef, l = 0.0f;
-  bool huge = false;
+  bool huge = false;  // the row's reference passes kHuge
 
   const uint32_t krow = row_place<D>(lane), vcol = column_place<D>(lane);
 
@@ -111,15 +111,16 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
         for (int e = 0; e < 16; ++e) t[sub][e] = seen(sub, e) ? t[sub][e] : -INFINITY;
     }
     float scale = c_log2;
-    auto round_logits = [&] {
+    // of the rows whose reference is huge; what a row's bits are depends on no other row
+    auto round_logits = [&](bool now) {
       asm volatile("");  // a branch of its own, and a rare one
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) t[sub][e] = rounded(t[sub][e], scale);
-      scale = 1.0f;
+        for (int e = 0; e < 16; ++e) t[sub][e] = now ? rounded(t[sub][e], scale) : t[sub][e];
+      scale = now ? 1.0f : scale;
     };
-    if (__builtin_expect(huge, 0)) round_logits();
+    if (__builtin_expect(__any(huge), 0)) round_logits(huge);
     v8b p[SUB][2];
     float part;
     auto probabilities = [&] {
@@ -137,22 +138,25 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
       }
     };
     probabilities();
-    if (__any(!(part <= kMostPart))) {
+    const bool over = !(part <= kMostPart);
+    if (__any(over)) {
       float top = -INFINITY;
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = raw_max(top, t[sub][e]);
       top = swap32_max(top * scale);
-      const float to = top > m ? top : m;
+      const bool move = swap32_max(over ? 1.0f : 0.0f) > 0.0f;  // this row's, in either half
+      const float to = move && top > m ? top : m;
       const float f = __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] *= f;
-      if (__any(fabsf(m) > kHuge && m != kNoRef)) {
-        if (!huge) round_logits();
-        huge = true;
+      const bool now = !huge && fabsf(m) > kHuge && m != kNoRef;
+      if (__any(now)) {
+        round_logits(now);
+        huge = huge || now;
       }
       probabilities();
     }
