@@ -12,12 +12,19 @@ values.  Outputs are bf16: queries and keys normed and rotated, values rounded.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import Fp8Error, _check, _dtype_code, _empty, _need, _need_kind, _need_place, _stream, lib
+from . import Fp8Error, _check, _dtype_code, _empty, _need, _need_place, _stream, lib
 from .attention import HEAD_DIMS, _head_rows
 
 
 def _opt(t):
     return 0 if t is None else t.data_ptr()
+
+
+def _here(t, name, dtype, shape, dev):
+    """_need, its checks in line."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda or \
+            t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, dev, shape=shape)
 
 
 def _args(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs):
@@ -38,20 +45,19 @@ def _args(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs):
         raise ValueError("norm weights for both queries and keys, or for neither")
     if wq is not None:
         wt = _dtype_code(wq)
-        _need(wq, "wq", wq.dtype, dev, shape=(D,))
-        _need(wk, "wk", wq.dtype, dev, shape=(D,))
+        _here(wq, "wq", wq.dtype, (D,), dev)
+        _here(wk, "wk", wq.dtype, (D,), dev)
     if positions is not None:
-        _need(positions, "positions", torch.int32, dev, shape=(T,))
+        _here(positions, "positions", torch.int32, (T,), dev)
     cos = sin = None
     rows = 0
     if rope is not None:
         cos, sin = rope
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            _need_kind(t, name, torch.float32)
-            if t.dim() != 2 or t.shape[1] != D // 2 or t.shape != cos.shape:
-                raise ValueError(f"{name} must be [positions, {D // 2}], got {tuple(t.shape)}")
-            _need_place(t, name, dev)
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError(f"cos must be a [positions, {D // 2}] tensor")
         rows = cos.shape[0]
+        _here(cos, "cos", torch.float32, (rows, D // 2), dev)
+        _here(sin, "sin", torch.float32, (rows, D // 2), dev)
         if rows < (1 if positions is not None else T):
             raise ValueError(f"cos holds {rows} positions for {T} tokens")
     return T, D, (qkv.data_ptr(), dt, stride, T, Hq, H, D, _opt(wq), _opt(wk), wt, float(eps), _opt(positions), _opt(cos),

@@ -71,11 +71,17 @@ class Sequences:
         return t - self.cu_tokens[i]
 
 
-def _rows(t, name, seqs, heads, d, dev):
-    stride = _head_rows(t, name, seqs.tokens, heads, d, dev, torch.bfloat16)
-    if stride > MAX_STRIDE:
-        raise ValueError(f"{name}: rows {stride} elements apart, {MAX_STRIDE} at most")
-    return stride
+def _rows(t, name, T, heads, d, dev):
+    """Row stride in elements of [T, heads, d] bf16 rows with packed heads.  (The
+    checks in line: a call for each of a step's tensors is a third of its host time.)"""
+    if t.shape == (T, heads, d) and t.dtype is torch.bfloat16 and t.device == dev and t.is_cuda and T > 1:
+        row, head, one = t.stride()
+        if one == 1 and (head == d or heads == 1) and row <= MAX_STRIDE:
+            return row
+    row = _head_rows(t, name, T, heads, d, dev, torch.bfloat16)
+    if row > MAX_STRIDE:
+        raise ValueError(f"{name}: rows {row} elements apart, {MAX_STRIDE} at most")
+    return row
 
 
 def _args(q, k, v, seqs, scale, causal, window):
@@ -85,15 +91,16 @@ def _args(q, k, v, seqs, scale, causal, window):
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
-    Hq, D, H = q.shape[1], q.shape[2], k.shape[1]
+    _, Hq, D = q.shape
+    H = k.shape[1]
     if D not in HEAD_DIMS:
         raise ValueError(f"head dimensions are {HEAD_DIMS}, got {D}")
     if H < 1 or Hq < 1 or Hq % H:
         raise ValueError(f"{Hq} query heads over {H} key heads: a positive multiple is wanted")
     if window < 0 or (window and not causal):
         raise ValueError("a window is positive and needs causal")
-    dev = seqs.device
-    strides = (_rows(q, "q", seqs, Hq, D, dev), _rows(k, "k", seqs, H, D, dev), _rows(v, "v", seqs, H, D, dev))
+    T, dev = seqs.tokens, seqs.device
+    strides = (_rows(q, "q", T, Hq, D, dev), _rows(k, "k", T, H, D, dev), _rows(v, "v", T, H, D, dev))
     # a window past every position is none: what the library's 32 bits hold
     return Hq, H, D, strides, float(D ** -0.5 if scale is None else scale), int(bool(causal)), min(int(window), 0x7FFFFFFF)
 
@@ -136,22 +143,27 @@ def attention_bwd(dout, q, k, v, out, lse, seqs, scale=None, causal=True, window
     attention_bwd_workspace_bytes(...) bytes, otherwise from torch's allocator."""
     Hq, H, D, (qs, ks, vs), scale, causal, window = _args(q, k, v, seqs, scale, causal, window)
     T, dev = seqs.tokens, seqs.device
-    gs = _rows(dout, "dout", seqs, Hq, D, dev)
+    if not isinstance(dout, torch.Tensor):
+        raise ValueError(f"dout must be a tensor, got {type(dout).__name__}")
+    gs = _rows(dout, "dout", T, Hq, D, dev)
     _need(out, "out", torch.bfloat16, dev, shape=(T, Hq, D))
     _need(lse, "lse", torch.float32, dev, shape=(T, Hq))
-    if dq is None and dk is None and dv is None and (Hq + 2 * H) * D <= MAX_STRIDE:   # one tensor's heads
+    row = (Hq + 2 * H) * D
+    if dq is None and dk is None and dv is None and row <= MAX_STRIDE:   # one tensor's heads
         dq, dk, dv = _empty((T, Hq + 2 * H, D), torch.bfloat16, dev, stream).split_with_sizes((Hq, H, H), 1)
-    grads, strides = [], []
-    for t, name, heads in ((dq, "dq", Hq), (dk, "dk", H), (dv, "dv", H)):
-        t = _empty((T, heads, D), torch.bfloat16, dev, stream) if t is None else t
-        grads.append(t)
-        strides.append(_rows(t, name, seqs, heads, D, dev))
+        strides = (row, row, row)
+    else:
+        grads = [_empty((T, n, D), torch.bfloat16, dev, stream) if t is None else t
+                 for t, n in ((dq, Hq), (dk, H), (dv, H))]
+        if not all(isinstance(t, torch.Tensor) for t in grads):
+            raise ValueError("dq, dk and dv must be tensors")
+        strides = [_rows(t, name, T, n, D, dev) for t, name, n in zip(grads, ("dq", "dk", "dv"), (Hq, H, H))]
+        dq, dk, dv = grads
     need = attention_bwd_workspace_bytes(seqs, Hq, H, D)
     if workspace is not None:
         _need_place(workspace, "workspace", dev)
     else:
         workspace = _empty(need, torch.uint8, dev, stream)
-    dq, dk, dv = grads
     _check("fp8_attention_bwd",
            lib.fp8_attention_bwd(dout.data_ptr(), gs, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, out.data_ptr(),
                                  lse.data_ptr(), seqs._ref, Hq, H, D, scale, causal, window, dq.data_ptr(), strides[0],
