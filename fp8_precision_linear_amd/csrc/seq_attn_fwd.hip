@@ -270,10 +270,14 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
 hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) {
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
   const int64_t groups = (int64_t)a.tiles * a.batch * a.q_heads;
-  // Two sets where a workgroup has a CU to itself (256 CUs) and more than one
-  // tile: two sequences of 1024, 12 heads of 64.
+  // Two sets where a workgroup has a CU to itself (256 CUs), and where the last
+  // rows of a long causal sequence would go on alone: one of 3000 tokens, 12 heads
+  // of 64, 47 us with one set and 37 with two, of 2048 tokens, 32 heads of 128, 61
+  // and 54.  Elsewhere the sets' joining costs more: two sequences of 1000 tokens,
+  // 32 heads of 64, 22 and 24, of 1500 and 300, 40 heads of 128, 48 and 61.
   const int64_t busy = std::min(groups, ((int64_t)a.tokens / kSeqRows + a.batch) * a.q_heads);
-  const bool two = busy <= 256 && a.max_len > 64 && head_dim != 256;
+  const bool uneven = a.causal && a.window == 0 && a.max_len >= 2048 && busy <= 600;
+  const bool two = (busy <= 256 || uneven) && a.max_len > 64 && head_dim != 256;
   auto launch = [&](auto kernel, int threads) {
     in_stretches(groups, threads, [&](uint32_t first, uint32_t count) {
       a.first = first;
