@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "norm_kernel.h"
+#include "quotient.h"
 
 namespace fp8lin {
 namespace {
@@ -54,7 +55,7 @@ struct LookupArgs {
 template <int TT, int OT, bool WHOLE, int U>
 __global__ __launch_bounds__(256) void embedding_fwd_kernel(LookupArgs a) {
   const int64_t base = (int64_t)(a.first + blockIdx.x) * (256 * U);
-  const int64_t row0 = base / a.units;
+  const int64_t row0 = quotient(base, a.units);
   const int rem = (int)(base - row0 * a.units) + threadIdx.x;
   Raw<TT> raw[U];
   Unit at[U];
@@ -336,7 +337,7 @@ template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t chunk = g / a.cols, p0 = chunk * kChunk;
+  const int64_t chunk = quotient(g, a.cols), p0 = chunk * kChunk;
   if (chunk >= a.chunks) return;
   const int col = ((int)(g - chunk * a.cols) * 64 + lane) * 4, left = (int)a.d - col;
   const int n = (int)min((int64_t)kChunk, a.tokens - p0);
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
 template <bool WHOLE>
 __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs a) {
   const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t chunk = g / a.cols, p0 = chunk * kChunk, p1 = p0 + kChunk;
+  const int64_t chunk = quotient(g, a.cols), p0 = chunk * kChunk, p1 = p0 + kChunk;
   if (chunk + 1 >= a.chunks) return;  // nothing goes on from the last one
   const int col = ((int)(g - chunk * a.cols) * 64 + (int)(threadIdx.x & 63)) * 4, left = (int)a.d - col;
   const uint32_t id = a.key[p1 - 1];

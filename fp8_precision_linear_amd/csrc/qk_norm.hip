@@ -12,6 +12,7 @@
 // a head, and with it its weights and angles, are the same in all of them.
 #include <algorithm>
 
+#include "quotient.h"
 #include "rope.h"
 
 namespace fp8lin {
@@ -73,7 +74,7 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const QkArgs& a, int64_t i) {
   Item r;
-  r.token = i / a.items;
+  r.token = quotient(i, a.items);
   r.step0 = (int)(i - r.token * a.items) * a.per;
   r.steps = min(a.per, a.steps - r.step0);
   return r;

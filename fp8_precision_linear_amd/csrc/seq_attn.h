@@ -20,6 +20,7 @@
 
 #include "attn_common.h"
 #include "lds_dma.h"
+#include "quotient.h"
 
 namespace fp8lin {
 

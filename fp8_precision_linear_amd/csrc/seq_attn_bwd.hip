@@ -108,7 +108,7 @@ __device__ void write_line(const SeqAttnArgs& a) {
 }
 
 // Share j of a line: from here to share j + 1's start.
-__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int64_t j) { return total * j / shares; }
+__device__ __forceinline__ int64_t share_start(int64_t total, int shares, int64_t j) { return quotient(total * j, shares); }
 
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int64_t scalar(int64_t v) {
@@ -164,11 +164,12 @@ __global__ __launch_bounds__(256) void seq_attn_stats_kernel(SeqAttnArgs a) {
   constexpr int kLanes = D / 8;
   uint32_t x = a.first + blockIdx.x;
   if (a.shares > 0 && x-- == 0) return write_line<D>(a);
-  const int64_t i = (int64_t)x * (256 / kLanes) + threadIdx.x / kLanes, token = i / a.q_heads;
+  const uint32_t i = x * (256 / kLanes) + threadIdx.x / kLanes;  // of tokens * q_heads, fewer than 2^31
+  const int64_t token = i / (uint32_t)a.q_heads;
   if (token >= a.tokens) return;
   const int head = (int)(i - token * a.q_heads), d = 8 * (threadIdx.x % kLanes);
   const v8b g = *reinterpret_cast<const v8b*>(a.dout + token * a.dout_stride + head * D + d);
-  const v8b o = *reinterpret_cast<const v8b*>(a.out + i * D + d);
+  const v8b o = *reinterpret_cast<const v8b*>(a.out + (int64_t)i * D + d);
   float delta = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) delta = fmaf((float)g[e], (float)o[e], delta);
@@ -498,7 +499,7 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
         }
     };
 
-    int group = (int)(piece.begin / walk.tiles), t = (int)(piece.begin % walk.tiles), buf = 0;
+    int group = (int)quotient(piece.begin, walk.tiles), t = (int)(piece.begin - (int64_t)group * walk.tiles), buf = 0;
     issue(group, t, 0);
     for (int64_t it = 0; it < its; ++it, buf ^= 1) {
       const int T = walk.lo + t * kQueries;
@@ -597,7 +598,7 @@ __device__ __forceinline__ void join_group(const SeqAttnArgs& a, uint32_t x) {
   const int64_t length = ROWS ? keys_of<D>(a, s.n, tile.k0).tiles : (int64_t)walk_of<D>(a, s.n, tile.k0).tiles * a.group;
   // the shares that hold the walk's first and last tile
   const int64_t walk = start + kEntry<D>;
-  const int64_t j0 = ((walk + 1) * shares - 1) / total, j1 = ((walk + length) * shares - 1) / total;
+  const int64_t j0 = quotient((walk + 1) * shares - 1, total), j1 = quotient((walk + length) * shares - 1, total);
   if (j0 == j1 || row >= s.n - tile.k0) return;
   // slots: the first share's second one, the others' first
   const int64_t step = (int64_t)heads * 2 * kSeqRows * D;
@@ -605,12 +606,13 @@ __device__ __forceinline__ void join_group(const SeqAttnArgs& a, uint32_t x) {
   const float* const part = ROWS ? a.part_q : a.part_k;
   v4f sum = *reinterpret_cast<const v4f*>(part + from + kSeqRows * D), v = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (!ROWS) v = *reinterpret_cast<const v4f*>(a.part_v + from + kSeqRows * D);
-  // (where the line is shorter than its shares are many, some are empty)
+  const bool some_empty = total < shares;
   for (int64_t j = j0 + 1; j <= j1; j += 4) {
     v4f pk[4], pv[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const bool there = j + c <= j1 && share_start(total, shares, j + c) < share_start(total, shares, j + c + 1);
+      const bool there = j + c <= j1 && !(some_empty && share_start(total, shares, j + c) ==
+                                                            share_start(total, shares, j + c + 1));
       pk[c] = pv[c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       if (there) {
         pk[c] = *reinterpret_cast<const v4f*>(part + from + (j + c - j0) * step);
