@@ -25,11 +25,12 @@
 namespace fp8lin {
 
 // A tile of kSeqRows keys, or rows: where its walk over the queries starts on the
-// head's line of key tiles and its walk over the keys on that of row tiles, its
-// sequence and first position.
+// head's line of key tiles and its walk over the keys on that of row tiles; its
+// sequence's first row and length, and its own first position.
 struct SeqLine {
   int64_t start, start_q;
-  int seq, k0;
+  int first, n, k0;
+  int count;  // of the line's end: the tiles' number
 };
 
 struct SeqAttnArgs {
@@ -52,7 +53,7 @@ struct SeqAttnArgs {
   float *lse2, *delta;  // [q_heads][tokens], lse * log2(e) and rowsum(dout * out)
   // sums of walks that are cut: [workgroups of that kind][2][kSeqRows][D]
   float *part_k, *part_v, *part_q;
-  SeqLine *line, *line_end;  // tiles of a head; the lines' lengths, and the tiles' number in `seq`
+  SeqLine *line, *line_end;  // tiles of a head; the lines' lengths, and the tiles' number
   int most_tiles;  // of `line`
   int shares, row_shares;  // of a head's line of key tiles, of row tiles; 0: a workgroup takes a tile
   uint32_t dkv_groups;  // workgroups of dk and dv, each

@@ -66,9 +66,9 @@ __device__ void write_line(const SeqAttnArgs& a) {
   int64_t tiles0 = 0, its0 = 0, keys0 = 0;
   for (int i0 = 0; i0 < a.batch; i0 += 256) {
     const int i = i0 + threadIdx.x;
-    int n = 0;
+    int first = 0, n = 0;
     if (i < a.batch) {
-      const int first = max(0, min(a.cu[i], a.tokens));
+      first = max(0, min(a.cu[i], a.tokens));
       n = min(max(first, min(a.cu[i + 1], a.tokens)) - first, a.max_len);
     }
     int64_t its = 0, keys = 0;
@@ -99,12 +99,12 @@ __device__ void write_line(const SeqAttnArgs& a) {
     }
     for (int k0 = 0; k0 < n; k0 += kSeqRows, ++at) {
       if (at >= a.most_tiles) break;  // (overlapping sequences: past what there is room for)
-      a.line[at] = {start, start_q, i, k0};
+      a.line[at] = {start, start_q, first, n, k0, 0};
       start += (int64_t)walk_of<D>(a, n, k0).tiles * a.group + kEntry<D>;
       start_q += keys_of<D>(a, n, k0).tiles + kEntry<D>;
     }
   }
-  if (threadIdx.x == 0) *a.line_end = {its0, keys0, (int)min(tiles0, (int64_t)a.most_tiles), 0};
+  if (threadIdx.x == 0) *a.line_end = {its0, keys0, 0, 0, 0, (int)min(tiles0, (int64_t)a.most_tiles)};
 }
 
 // Share j of a line: from here to share j + 1's start.
@@ -127,7 +127,7 @@ __device__ __forceinline__ Share share_of(const SeqAttnArgs& a, int shares, int 
   const int64_t total = scalar(ROWS ? a.line_end->start_q : a.line_end->start);
   r.pos = share_start(total, shares, j);
   r.end = share_start(total, shares, j + 1);
-  r.tiles = __builtin_amdgcn_readfirstlane(a.line_end->seq);
+  r.tiles = __builtin_amdgcn_readfirstlane(a.line_end->count);
   int at = -1;  // the tile that the share begins in: the last that starts at or before it
   for (int i0 = 0; i0 < r.tiles; i0 += 256) {
     const int i = i0 + (int)threadIdx.x;
@@ -219,9 +219,14 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
   const uint32_t by_row = row_place<D>(lane), by_column = column_place<D>(lane);
 
   for (; share.pos < share.end && share.at < share.tiles; ++share.at) {
-    SeqLine tile = {0, 0, place % a.batch, (a.tiles - 1 - place / a.batch) * kSeqRows};  // late rows see most: first
-    if constexpr (CUT) tile = a.line[share.at];
-    const Seq s = seq_of(a, __builtin_amdgcn_readfirstlane(tile.seq));
+    SeqLine tile = {};
+    if constexpr (CUT) {
+      tile = a.line[share.at];
+    } else {
+      const Seq q = seq_of(a, place % a.batch);
+      tile.first = q.first, tile.n = q.n, tile.k0 = (a.tiles - 1 - place / a.batch) * kSeqRows;  // late rows see most
+    }
+    const Seq s = {__builtin_amdgcn_readfirstlane(tile.first), __builtin_amdgcn_readfirstlane(tile.n)};
     const int row0 = __builtin_amdgcn_readfirstlane(tile.k0);
     if (row0 >= s.n) return;  // (not one of a line)
     const Walk walk = keys_of<D>(a, s.n, row0);
@@ -389,9 +394,14 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
   const uint32_t by_row = row_place<D>(lane), by_column = column_place<D>(lane);
 
   for (; share.pos < share.end && share.at < share.tiles; ++share.at) {
-    SeqLine tile = {0, 0, place % a.batch, place / a.batch * kSeqRows};  // early keys are seen most: first
-    if constexpr (CUT) tile = a.line[share.at];
-    const Seq s = seq_of(a, __builtin_amdgcn_readfirstlane(tile.seq));
+    SeqLine tile = {};
+    if constexpr (CUT) {
+      tile = a.line[share.at];
+    } else {
+      const Seq q = seq_of(a, place % a.batch);
+      tile.first = q.first, tile.n = q.n, tile.k0 = place / a.batch * kSeqRows;  // early keys are seen most
+    }
+    const Seq s = {__builtin_amdgcn_readfirstlane(tile.first), __builtin_amdgcn_readfirstlane(tile.n)};
     const int k0 = __builtin_amdgcn_readfirstlane(tile.k0);
     if (k0 >= s.n) return;  // (not one of a line)
     const Walk walk = walk_of<D>(a, s.n, k0);
@@ -591,9 +601,9 @@ __device__ __forceinline__ void join_group(const SeqAttnArgs& a, uint32_t x) {
   const int nth = x % heads, head = ROWS ? (nth % a.heads) * a.group + nth / a.heads : nth;
   x /= heads;
   const int at = x / kParts, row = (int)(x % kParts) * kRows + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
-  if (at >= a.line_end->seq) return;
+  if (at >= a.line_end->count) return;
   const SeqLine tile = a.line[at];
-  const Seq s = seq_of(a, tile.seq);
+  const Seq s = {tile.first, tile.n};
   const int64_t total = ROWS ? a.line_end->start_q : a.line_end->start, start = ROWS ? tile.start_q : tile.start;
   const int64_t length = ROWS ? keys_of<D>(a, s.n, tile.k0).tiles : (int64_t)walk_of<D>(a, s.n, tile.k0).tiles * a.group;
   // the shares that hold the walk's first and last tile
