@@ -152,3 +152,62 @@ def test_another_stream(em):
     got = em.embedding_bwd(dout, ids, 1000, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_graph(em):
+    """Lookup and gradient captured, for the sort of one workgroup and that of
+    tiles; replays on new ids, with eager calls between them, give their bits."""
+    for n, vocab, d in ((700, 1000, 64), (20000, 500, 20)):
+        ids = make_ids("text", n, vocab, torch.int64)
+        table, dout = torch.randn(vocab, d, device="cuda"), torch.randn(n, d, device="cuda")
+        em.embedding_bwd(dout, ids, vocab)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = (em.embedding_fwd(ids, table, dtype=torch.float32), em.embedding_bwd(dout, ids, vocab))
+        for r, kind in enumerate(("few", "one", "random")):
+            ids.copy_(make_ids(kind, n, vocab, torch.int64, seed=r))
+            want = (em.embedding_fwd(ids, table, dtype=torch.float32), em.embedding_bwd(dout, ids, vocab))
+            torch.cuda.synchronize()
+            for t in outs:
+                t.fill_(3)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs, want)), kind
+
+
+def test_two_calls_at_once(em):
+    ids = [make_ids("text", 20000, 700, torch.int64, seed=s) for s in range(2)]
+    dout = torch.randn(20000, 96, device="cuda")
+    want = [em.embedding_bwd(dout, i, 700) for i in ids]
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [em.embedding_bwd(dout, i, 700, stream=s) for _ in range(2) for i, s in zip(ids, sides)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want * 2))
+
+
+def test_offsets_past_32_bits(em):
+    """A table, and rows of tokens, of more than 2^31 elements."""
+    d, vocab = 8192, (1 << 18) + 100
+    say("table of", vocab, "rows of", d)
+    table = torch.empty(vocab, d, dtype=torch.bfloat16, device="cuda")
+    table[-3:] = torch.randn(3, d, device="cuda").to(torch.bfloat16)
+    ids = torch.tensor([vocab - 3, vocab - 1, vocab, vocab - 2, vocab - 1], device="cuda")
+    got = em.embedding_fwd(ids, table)
+    assert torch.equal(got[[0, 1, 3, 4]], table[[vocab - 3, vocab - 1, vocab - 2, vocab - 1]]) and not got[2].any()
+    del table
+    dout = torch.randn(5, d, device="cuda")
+    grad = em.embedding_bwd(dout, ids, vocab)
+    assert torch.equal(grad[vocab - 3:], torch.stack((dout[0], dout[3], dout[1] + dout[4])))
+    assert not grad[:vocab - 3].any()
+    del grad
+    many = torch.full((vocab,), -1, dtype=torch.int64, device="cuda")   # tokens: all but some are none
+    many[-2:] = torch.tensor([5, 9], device="cuda")
+    small = torch.randn(10, d, device="cuda").to(torch.bfloat16)
+    out = em.embedding_fwd(many, small)
+    assert torch.equal(out[-2:], small[[5, 9]]) and not out[:-2].any()
+    out[-2:] = 1.0
+    grad = em.embedding_bwd(out, many, 10)
+    assert bool((grad[[5, 9]] == 1.0).all()) and not grad[:5].any()

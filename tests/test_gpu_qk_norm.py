@@ -171,3 +171,55 @@ def test_autograd(qn):
         down = loss(*[t - step * way if j == i else t for j, t in enumerate(at)])
         got = (leaf.grad.double() * way).sum().item()
         assert abs(got - (up - down) / (2 * step)) <= 1e-5 * (leaf.grad.double() * way).abs().sum().item() + 1e-6
+
+
+def test_graph_and_streams(qn):
+    """Both directions captured and replayed, and on two other streams at once:
+    the eager calls' bits."""
+    T, Hq, H, D = 333, 6, 2, 128
+    x, (wq, wk), dy, pos = make(T, Hq, H, D, torch.bfloat16, True)
+    more = dict(wq=wq, wk=wk, rope=tables(50, D), positions=pos)
+
+    def both(stream=None):
+        y = qn.qk_norm_rope_fwd(x, Hq, H, **more, stream=stream)
+        return (*y, *qn.qk_norm_rope_bwd(*dy, x, **more, stream=stream))
+    want = both()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [both(s) for _ in range(2) for s in sides]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = both()
+    for r in range(3):
+        new, _, more_dy, _ = make(T, Hq, H, D, torch.bfloat16, True, seed=1 + r)
+        for a, b in zip((x, *dy), (new, *more_dy)):
+            a.copy_(b)
+        pos.add_(1)
+        want = both()
+        torch.cuda.synchronize()
+        for t in outs:
+            t.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), r
+
+
+def test_offsets_past_32_bits(qn):
+    """Rows 2^23 elements apart."""
+    T, Hq, H, D, row = 300, 2, 1, 64, 1 << 23
+    say("rows", row, "apart")
+    x, (wq, wk), dy, pos = make(T, Hq, H, D, torch.bfloat16, True)
+    more = dict(wq=wq, wk=wk, rope=tables(50, D), positions=pos)
+    want = (*qn.qk_norm_rope_fwd(x, Hq, H, **more), *qn.qk_norm_rope_bwd(*dy, x, **more))
+    wide = torch.empty(T * row, dtype=torch.bfloat16, device="cuda").view(T, row)
+    far, at = [], 0
+    for t in (x, *dy):
+        n = t.shape[1]
+        far.append(wide[:, at:at + n * D].unflatten(1, (n, D)))
+        far[-1].copy_(t)
+        at += n * D
+    got = (*qn.qk_norm_rope_fwd(far[0], Hq, H, **more), *qn.qk_norm_rope_bwd(*far[1:], far[0], **more))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
