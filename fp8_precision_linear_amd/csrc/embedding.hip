@@ -313,6 +313,7 @@ struct SumArgs {
   float* dtable;
   float* part;     // [chunks][2][d]: sums that reach past the chunk's first, its last position
   int64_t chunks;
+  float* span;     // [chunks / kSpan][d]: sums of spans of chunks, or null
   int cols;        // waves across a row, 256 columns each
   uint32_t first;
 };
@@ -380,41 +381,91 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
   }
 }
 
-// Ids whose rows begin in one chunk and end in another: the chunks' sums in order,
-// a wave for 256 columns.
+// Rows of partial sums on their way at once.
+constexpr int kAhead = 16;
+// Of many tokens an id may have very many (padding that is a token): the chunks of
+// a span that it fills are added before the join, all spans at the same time
+// (65536 rows of 1024, all of one id: 1323 -> 126 us; 16384 of 768: 144 -> 63, and
+// 59 -> 61 where no id fills a span, which is the launch: none for fewer tokens).
+constexpr int kSpan = 64, kManyChunks = 512;
+
+// Whether span s lies in a run of `id` that its first chunk is a part of.
+__device__ __forceinline__ bool fills_span(const SumArgs& a, int64_t s, uint32_t id) {
+  return (s + 1) * kSpan <= a.chunks && a.key[min((s + 1) * kSpan * kChunk, a.tokens) - 1] == id;
+}
+
+template <bool WHOLE>
+__global__ __launch_bounds__(256) void embedding_span_kernel(SumArgs a) {
+  const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t s = quotient(g, a.cols), p0 = s * kSpan * kChunk;
+  if ((s + 1) * kSpan > a.chunks || s == 0) return;
+  const int col = ((int)(g - s * a.cols) * 64 + (int)(threadIdx.x & 63)) * 4, left = (int)a.d - col;
+  const uint32_t id = a.key[p0];
+  if (left <= 0 || id >= (uint32_t)a.vocab || a.key[p0 - 1] != id || !fills_span(a, s, id)) return;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int c0 = 0; c0 < kSpan; c0 += kAhead) {
+    Raw<FP8_IN_FP32> raw[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      raw[i] = load_raw<FP8_IN_FP32, WHOLE, false>(a.part, 2 * (s * kSpan + c0 + i) * a.d + col, left);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      float v[4];
+      unpack<FP8_IN_FP32>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    }
+  }
+  store_as<FP8_IN_FP32, WHOLE>(a.span, s * a.d + col, left, sum);
+}
+
+// Ids whose rows begin in one chunk and end in another: the chunks' sums, or those
+// of whole spans, in order, a wave for 256 columns.
 template <bool WHOLE>
 __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs a) {
   const int64_t g = (int64_t)(a.first + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int64_t chunk = quotient(g, a.cols), p0 = chunk * kChunk, p1 = p0 + kChunk;
   if (chunk + 1 >= a.chunks) return;  // nothing goes on from the last one
-  const int col = ((int)(g - chunk * a.cols) * 64 + (int)(threadIdx.x & 63)) * 4, left = (int)a.d - col;
+  const int lane = threadIdx.x & 63, col = ((int)(g - chunk * a.cols) * 64 + lane) * 4, left = (int)a.d - col;
   const uint32_t id = a.key[p1 - 1];
-  if (left <= 0 || id >= (uint32_t)a.vocab || a.key[p1] != id) return;
+  if (id >= (uint32_t)a.vocab || a.key[p1] != id) return;
   if (p0 > 0 && a.key[p0 - 1] == id && a.key[p0] == id) return;  // begun in an earlier one
-  float sum[4];
-  unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, (2 * chunk + 1) * a.d + col, left), sum);
-  constexpr int kAhead = 4;
-  for (int64_t c0 = chunk + 1; c0 < a.chunks && a.key[c0 * kChunk] == id; c0 += kAhead) {
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (left > 0) unpack<FP8_IN_FP32>(load_raw<FP8_IN_FP32, WHOLE, false>(a.part, (2 * chunk + 1) * a.d + col, left), sum);
+  for (int64_t c0 = chunk + 1; c0 < a.chunks && a.key[c0 * kChunk] == id;) {
+    const bool spans = a.span && c0 % kSpan == 0 && fills_span(a, c0 / kSpan, id);
+    const int64_t unit = spans ? kSpan : 1, step = spans ? a.d : 2 * a.d;
+    const float* from = spans ? a.span + c0 / kSpan * a.d : a.part + 2 * c0 * a.d;
+    // how many there are, a lane each (sorted: they come first); chunks up to
+    // where the next span begins
+    const int64_t c = c0 + lane * unit;
+    const int most = (int)min((int64_t)kAhead, spans || !a.span ? kAhead : kSpan - c0 % kSpan);
+    const bool there = lane < most && c < a.chunks && (spans ? fills_span(a, c / kSpan, id) : a.key[c * kChunk] == id);
+    const int taken = __popcll(__ballot(there));
     Raw<FP8_IN_FP32> raw[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       raw[i] = Raw<FP8_IN_FP32>{};
-      if (c0 + i < a.chunks && a.key[(c0 + i) * kChunk] == id)
-        raw[i] = load_raw<FP8_IN_FP32, WHOLE, false>(a.part, 2 * (c0 + i) * a.d + col, left);
+      if (i < taken && left > 0) raw[i] = load_raw<FP8_IN_FP32, WHOLE, false>(from, i * step + col, left);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < kAhead; ++i) {
+      float v[4];
+      unpack<FP8_IN_FP32>(raw[i], v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += raw[i][e];
+      for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    }
+    c0 += taken * unit;
   }
-  store_sum<WHOLE>(a, id, col, left, sum);
+  if (left > 0) store_sum<WHOLE>(a, id, col, left, sum);
 }
 
 int64_t aligned(int64_t bytes) { return (bytes + 255) & ~(int64_t)255; }
 struct GradPlan {
   int64_t tiles, chunks;
   int passes, bits;
-  int64_t key, order, key2, order2, hist, part, bytes;  // offsets
+  int64_t spans;                                              // 0: the join takes chunks alone
+  int64_t key, order, key2, order2, hist, part, span, bytes;  // offsets
 };
 GradPlan plan_of(int64_t tokens, int64_t vocab, int64_t d) {
   GradPlan p{};
@@ -437,7 +488,10 @@ GradPlan plan_of(int64_t tokens, int64_t vocab, int64_t d) {
     p.order2 = take(4 * tokens);
     p.hist = take(4 * ((int64_t)1 << p.bits) * p.tiles);
   }
-  p.part = take(8 * p.chunks * ((d + 3) & ~(int64_t)3));
+  const int64_t row = 4 * ((d + 3) & ~(int64_t)3);
+  p.part = take(2 * p.chunks * row);
+  p.spans = p.chunks > kManyChunks ? p.chunks / kSpan : 0;
+  p.span = take(p.spans * row);
   p.bytes = at;
   return p;
 }
@@ -514,6 +568,7 @@ hipError_t launch_embedding_bwd(const EmbeddingGrad& g, void* ws, hipStream_t st
   a.scale = g.scale, a.accumulate = g.accumulate, a.dtable = g.dtable;
   a.part = reinterpret_cast<float*>(w + p.part);
   a.chunks = p.chunks;
+  a.span = p.spans > 0 ? reinterpret_cast<float*>(w + p.span) : nullptr;
   a.cols = (int)((g.d + 255) / 256);
   auto launch = [&](auto kernel, int64_t waves) {
     in_stretches((waves + 3) / 4, 256, [&](uint32_t first, uint32_t count) {
@@ -528,6 +583,7 @@ hipError_t launch_embedding_bwd(const EmbeddingGrad& g, void* ws, hipStream_t st
   else
     launch(whole ? embedding_sum_kernel<FP8_IN_FP32, true> : embedding_sum_kernel<FP8_IN_FP32, false>,
            p.chunks * a.cols);
+  if (p.spans > 0) launch(whole ? embedding_span_kernel<true> : embedding_span_kernel<false>, p.spans * a.cols);
   launch(whole ? embedding_join_kernel<true> : embedding_join_kernel<false>, (p.chunks - 1) * a.cols);
   return hipGetLastError();
 }

@@ -108,6 +108,25 @@ def test_gradient_of_many_tokens(em, n, vocab):
         assert bool(((got - want).abs() <= bound).all()), kind
 
 
+@pytest.mark.parametrize("n", [8192, 8193, 9215, 9216, 20003])
+def test_long_runs(em, n):
+    """Runs that fill spans of chunks, begin and end inside them, next to short
+    ones; rows of an odd length."""
+    say("long runs", n)
+    d, vocab = 7, 6
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dout = torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+    for cuts in ([n], [1, n], [1023, n - 17], [15, 1024, 2 * 1024 + 1, n - 1024], [n // 3, n // 3 + 1, n // 2]):
+        ids = torch.zeros(n, dtype=torch.int32)
+        for c in cuts:
+            ids[c:] += 1
+        ids = ids[torch.randperm(n, generator=torch.Generator().manual_seed(1))].cuda()
+        want, total, count = reference(dout, ids, vocab, 1.0)
+        got = em.embedding_bwd(dout, ids, vocab).double()
+        bound = 2.0 ** -24 * ((count - 1).clamp(min=0) * total * (1 + 2.0 ** -10) + want.abs()) + TINY
+        assert bool(((got - want).abs() <= bound).all()), cuts
+
+
 def test_no_tokens(em):
     out = torch.full((5, 8), 3.0, device="cuda")
     em.embedding_bwd(torch.empty(0, 8, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), 5, out=out)
