@@ -156,6 +156,22 @@ __device__ __forceinline__ int64_t slot_of(uint32_t group, const Piece& p, int r
   return ((2 * (int64_t)group + (p.begin == 0)) * kSeqRows + row) * D;
 }
 
+// The tile of a workgroup that takes a whole one, the last first or the first; of
+// ragged batches (ragged_places) from the line.
+template <bool LAST_FIRST>
+__device__ __forceinline__ SeqLine whole_tile(const SeqAttnArgs& a, int place) {
+  SeqLine tile = {};
+  if (a.rest > 0) {
+    const int at = LAST_FIRST ? a.most_tiles - 1 - place : place;
+    if (at < a.line_end->count) tile = a.line[at];
+  } else {
+    const Seq s = seq_of(a, place % a.batch);
+    const int nth = place / a.batch;
+    tile.first = s.first, tile.n = s.n, tile.k0 = (LAST_FIRST ? a.tiles - 1 - nth : nth) * kSeqRows;
+  }
+  return tile;
+}
+
 // What a row's gradients are formed from: -lse log2(e), or NaN where the forward's
 // results are not finite, which makes everything that the row sees NaN, and
 // -delta.  D / 8 lanes a row; one more workgroup writes the line of key tiles.
@@ -163,7 +179,7 @@ template <int D>
 __global__ __launch_bounds__(256) void seq_attn_stats_kernel(SeqAttnArgs a) {
   constexpr int kLanes = D / 8;
   uint32_t x = a.first + blockIdx.x;
-  if (a.shares > 0 && x-- == 0) return write_line<D>(a);
+  if ((a.shares > 0 || a.rest > 0) && x-- == 0) return write_line<D>(a);
   const uint32_t i = x * (256 / kLanes) + threadIdx.x / kLanes;  // of tokens * q_heads, fewer than 2^31
   const int64_t token = i / (uint32_t)a.q_heads;
   if (token >= a.tokens) return;
@@ -223,8 +239,7 @@ __device__ __forceinline__ void dq_group(const SeqAttnArgs& a, GradShared<D>& ld
     if constexpr (CUT) {
       tile = a.line[share.at];
     } else {
-      const Seq q = seq_of(a, place % a.batch);
-      tile.first = q.first, tile.n = q.n, tile.k0 = (a.tiles - 1 - place / a.batch) * kSeqRows;  // late rows see most
+      tile = whole_tile<true>(a, place);  // late rows see most
     }
     const Seq s = {__builtin_amdgcn_readfirstlane(tile.first), __builtin_amdgcn_readfirstlane(tile.n)};
     const int row0 = __builtin_amdgcn_readfirstlane(tile.k0);
@@ -398,8 +413,7 @@ __device__ __forceinline__ void dkv_group(const SeqAttnArgs& a, GradShared<D>& l
     if constexpr (CUT) {
       tile = a.line[share.at];
     } else {
-      const Seq q = seq_of(a, place % a.batch);
-      tile.first = q.first, tile.n = q.n, tile.k0 = place / a.batch * kSeqRows;  // early keys are seen most
+      tile = whole_tile<false>(a, place);  // early keys are seen most
     }
     const Seq s = {__builtin_amdgcn_readfirstlane(tile.first), __builtin_amdgcn_readfirstlane(tile.n)};
     const int k0 = __builtin_amdgcn_readfirstlane(tile.k0);
@@ -700,8 +714,8 @@ void run_bwd(SeqAttnArgs& a, int64_t share_tiles, hipStream_t stream) {
       hipLaunchKernelGGL(kernel, dim3(count), dim3(256), 0, stream, a);
     });
   };
-  launch(seq_attn_stats_kernel<D>, ((int64_t)a.tokens * a.q_heads * (D / 8) + 255) / 256 + (a.shares > 0));
-  const int64_t tiles = (int64_t)a.tiles * a.batch;
+  launch(seq_attn_stats_kernel<D>, ((int64_t)a.tokens * a.q_heads * (D / 8) + 255) / 256 + (a.shares > 0 || a.rest > 0));
+  const int64_t tiles = a.rest > 0 ? a.most_tiles : (int64_t)a.tiles * a.batch;
   const int64_t dkv = a.shares > 0 ? (int64_t)a.heads * a.shares : tiles * a.heads;
   const int64_t dq = (a.row_shares > 0 ? a.row_shares : tiles) * a.q_heads;
   a.dkv_groups = (uint32_t)dkv;
@@ -726,6 +740,7 @@ hipError_t launch_seq_attn_bwd(SeqAttnArgs a, int head_dim, void* ws, hipStream_
   a.row_shares = p.row_shares;
   a.most_tiles = (int)p.most_tiles;
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
+  a.rest = ragged_places(a.tokens, a.batch, a.tiles);
   uint8_t* at = static_cast<uint8_t*>(ws);
   auto take = [&](int64_t bytes) {
     uint8_t* r = at;

@@ -42,8 +42,15 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
   x /= a.heads;
   const int head = kv_head * a.group + x % a.group;
   x /= a.group;
-  const Seq s = seq_of(a, x % a.batch);
-  const int row0 = (a.tiles - 1 - (int)(x / a.batch)) * kSeqRows;  // late rows see most: first
+  // late rows see most: first
+  NthTile tile = {(int)(x % a.batch), a.tiles - 1 - (int)(x / a.batch)};
+  if (a.rest > 0) {
+    tile = {(int)x - a.rest, 0};
+    if ((int)x < a.rest) tile = nth_tile(a, a.rest - 1 - (int)x);
+    if (tile.seq < 0) return;
+  }
+  const Seq s = seq_of(a, tile.seq);
+  const int row0 = tile.tile * kSeqRows;
   if (row0 >= s.n) return;
   const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
   const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
@@ -269,7 +276,8 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
 
 hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) {
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
-  const int64_t groups = (int64_t)a.tiles * a.batch * a.q_heads;
+  a.rest = ragged_places(a.tokens, a.batch, a.tiles);
+  const int64_t groups = (a.rest > 0 ? (int64_t)a.rest + a.batch : (int64_t)a.tiles * a.batch) * a.q_heads;
   // Two sets where a workgroup has a CU to itself (256 CUs), and where the last
   // rows of a long causal sequence would go on alone: one of 3000 tokens, 12 heads
   // of 64, 47 us with one set and 37 with two, of 2048 tokens, 32 heads of 128, 61

@@ -6,7 +6,7 @@ import torch
 
 from gpu_util import need_gpu, say
 from test_gpu_self_attention import check, inputs
-from test_gpu_self_attention_edges import both, same
+from test_gpu_self_attention_edges import both, inside, same
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,29 @@ def sa():
 @pytest.mark.parametrize("mask", [{}, {"window": 50}, {"causal": False}])
 def test_plans(sa, shape, mask):
     check(sa, *shape, **mask, seed=1)
+
+
+# long sequences among many short ones, whose tiles are counted through
+RAGGED = [([20] * 30 + [2100] + [0, 33] * 15, 32, 32, 64), ([1300] + [3] * 600 + [257, 1] * 2, 2, 2, 64),
+          ([5] * 20 + [129, 1800, 130] + [1] * 30, 20, 20, 128), ([2, 2000] + [9] * 30, 12, 12, 256)]
+
+
+@pytest.mark.parametrize("shape", RAGGED)
+@pytest.mark.parametrize("mask", [{}, {"window": 140}, {"causal": False}])
+def test_ragged(sa, shape, mask):
+    check(sa, *shape, **mask, seed=11)
+
+
+def test_loose_bounds(sa):
+    """No host knowledge of the lengths but their sum: the bound is all rows."""
+    lens, Hq, H, D = [60] * 30 + [500] + [0] * 300, 32, 32, 64
+    T = sum(lens) + 40
+    q, k, v, dout = inputs([T], Hq, H, D, 12)
+    cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+    seqs = sa.Sequences(cu, max_len=1 << 30, tokens=T)
+    got = both(sa, q, k, v, dout, seqs)
+    say("loose bounds")
+    inside(lens, Hq, D, q, k, v, dout, *[t[:T - 40] for t in got])
 
 
 @pytest.mark.parametrize("mask", [{}, {"causal": False}])
