@@ -165,15 +165,15 @@ __device__ __forceinline__ v8b column_step(uint32_t place, int d) {
   return __builtin_bit_cast(v8b, v8s{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
 
-// DMA of ROWS rows of D bf16 by four waves; rows past the last are the last one
+// DMA of ROWS rows of D bf16 by WAVES waves; rows past the last are the last one
 // again (whoever reads them masks them).
-template <int D, int ROWS>
+template <int D, int ROWS, int WAVES = 4>
 struct TileLoad {
   static constexpr int kBytes = ROWS * D * 2;
-  static constexpr int kLoads = kBytes / 4096;  // of each wave
-  static constexpr int kStep = 2048 / D;        // rows between a wave's loads
-  // loads of odd and even number, where their rows are swizzled differently
-  static constexpr int kKinds = D == 256 ? 2 : 1;
+  static constexpr int kLoads = kBytes / (1024 * WAVES);  // of each wave
+  static constexpr int kStep = 512 * WAVES / D;           // rows between a wave's loads
+  // loads whose rows are swizzled differently (alike: sixteen rows apart)
+  static constexpr int kKinds = kStep % 16 == 0 ? 1 : 16 / kStep;
   uint32_t offset[kKinds];
   static __device__ __forceinline__ uint32_t row_of(int lane, int wave) { return wave * (512 / D) + lane / (D / 8); }
   static __device__ __forceinline__ uint32_t chunk_of(int lane, uint32_t row) {
@@ -191,14 +191,14 @@ struct TileLoad {
     if (left >= ROWS) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        dma16(p + (int64_t)(i * kStep) * stride_bytes, offset[i % kKinds], lds + (wave + 4 * i) * 1024);
+        dma16(p + (int64_t)(i * kStep) * stride_bytes, offset[i % kKinds], lds + (wave + WAVES * i) * 1024);
     } else {
       const int lane = threadIdx.x & 63;
       const uint32_t row = row_of(lane, wave);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t r = min((int)row + i * kStep, left - 1);
-        dma16(p, r * (uint32_t)stride_bytes + chunk_of(lane, row + (i % kKinds) * kStep), lds + (wave + 4 * i) * 1024);
+        dma16(p, r * (uint32_t)stride_bytes + chunk_of(lane, row + (i % kKinds) * kStep), lds + (wave + WAVES * i) * 1024);
       }
     }
   }
@@ -227,16 +227,16 @@ __device__ __forceinline__ v4i32 bad_of(v8b f) {
 
 // A tile that some column does not see whole is multiplied with zeros where it
 // is not seen, and 0 * NaN must not reach a result.  So such tiles are searched
-// for NaN and infinities (has_bad: whether any wave found one; the tile's four
+// for NaN and infinities (has_bad: whether any wave found one; the workgroup's
 // waves call it together), and what is found is cleared in LDS (clear_bad) once
 // those that do see it have it on record.
-// GROUPS sets of four waves have a tile each, the last ones perhaps none (`there`).
-template <int BYTES, int GROUPS = 1>
+// GROUPS sets of WAVES waves have a tile each, the last ones perhaps none (`there`).
+template <int BYTES, int GROUPS = 1, int WAVES = 4>
 __device__ __forceinline__ bool has_bad(uint32_t tile, int* found, bool there = true) {
   uint32_t bad = 0;
-  const uint32_t mine = tile + (threadIdx.x & 255) * 16;
+  const uint32_t mine = tile + (threadIdx.x % (64 * WAVES)) * 16;
 #pragma unroll
-  for (int i = 0; i < BYTES; i += 4096) {
+  for (int i = 0; i < BYTES; i += 1024 * WAVES) {
     const v4i32 w = bad_of(lds_row(mine + i));
     bad |= (uint32_t)(w[0] | w[1] | w[2] | w[3]);
   }
@@ -245,14 +245,14 @@ __device__ __forceinline__ bool has_bad(uint32_t tile, int* found, bool there = 
   __syncthreads();
   int all = 0;
 #pragma unroll
-  for (int w = 0; w < 4 * GROUPS; ++w) all |= found[w];
+  for (int w = 0; w < WAVES * GROUPS; ++w) all |= found[w];
   return all != 0;
 }
 // rows: where given, set to 1 for each row of `row_bytes` that held one.
-template <int BYTES>
+template <int BYTES, int WAVES = 4>
 __device__ __forceinline__ void clear_bad(uint32_t tile, int row_bytes, int* rows) {
   __syncthreads();  // every wave is done with the tile as it was
-  for (int i = (threadIdx.x & 255) * 16; i < BYTES; i += 4096) {
+  for (int i = (threadIdx.x % (64 * WAVES)) * 16; i < BYTES; i += 1024 * WAVES) {
     v4i32 w = __builtin_bit_cast(v4i32, lds_row(tile + i));
     const v4i32 bad = bad_of(__builtin_bit_cast(v8b, w));
     w &= ~bad;

@@ -1,14 +1,20 @@
 // Attention over packed sequences, forward: seq_attn.h has the mathematics.
 //
-// A workgroup of four waves takes 128 query rows of one head; a wave owns 32 of
-// them, its queries, logits and output in registers.  Tiles of 64 keys and
-// values go through LDS by DMA, the next one on its way while one is consumed.
-// Logits against a reference that follows the row maximum lazily: it moves when
-// a tile's probabilities outgrow it, so most tiles rescale nothing.
+// A workgroup takes 128 query rows of one head, a wave 32 of them, its queries,
+// logits and output in registers.  Tiles of 64 keys and values (32 with heads of
+// 256) go through LDS by DMA, the next one on its way while one is consumed.  Logits
+// against a reference that follows the row maximum lazily: it moves when a tile's
+// probabilities outgrow it, so most tiles rescale nothing.
 //
-// Where the workgroups would leave CUs without work, eight waves take the 128
-// rows: two sets of four, each with every other tile of the keys, joined in LDS
-// at the end.
+// Where the workgroups would leave CUs without work they have more waves than rows
+// need: two sets of four with every other tile of the keys, or four sets of two
+// waves with 64 rows (two with heads of 256); the sets are joined in LDS at the end.
+//
+// Large calls run at the card's power limit: two sequences of 4096, 32 heads of 128,
+// everything seen, MFMA busy 44% of the cycles at 1.6-1.7 GHz, no bank conflicts;
+// four causal ones 600 us, 920 TFLOP/s.  Heads of 256 hold one wave a SIMD (its
+// output alone takes 128 registers): three causal sequences of 2000, 16 heads on 4,
+// 265 us, 370 TFLOP/s.  Small calls are latency: 2 x 1024, 12 heads of 64, 15 us.
 #include <algorithm>
 
 #include "seq_attn.h"
@@ -16,9 +22,9 @@
 namespace fp8lin {
 namespace {
 
-// Keys of a tile.
-template <int D>
-constexpr int kKeysOf = D == 256 ? 32 : 64;
+// Keys of a tile: the sets' buffers, two of keys and values each, fit the LDS.
+template <int D, int SETS>
+constexpr int kKeysOf = D * SETS >= 256 && !(D == 128 && SETS == 2) ? 32 : 64;
 // A lane's 32 probabilities of a tile may add up to this before its row's
 // reference moves.
 constexpr float kMostPart = 0x1p16f;
@@ -26,16 +32,16 @@ constexpr float kMostPart = 0x1p16f;
 // (attn_common.h).
 constexpr float kHuge = 0x1p22f;
 
-// SETS of four waves.
-template <int D, int SETS>
-__global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(SeqAttnArgs a) {
-  constexpr int J = D / 16, DT = D / 32, kKeys = kKeysOf<D>, SUB = kKeys / 32;
-  using Load = TileLoad<D, kKeys>;
+// SETS of WAVES waves, each with 32 rows.
+template <int D, int WAVES, int SETS>
+__global__ __launch_bounds__(64 * WAVES * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_kernel(SeqAttnArgs a) {
+  constexpr int J = D / 16, DT = D / 32, kKeys = kKeysOf<D, SETS>, SUB = kKeys / 32, kRows = 32 * WAVES;
+  using Load = TileLoad<D, kKeys, WAVES>;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[SETS][2][2][Load::kBytes];  // [set][buffer][keys, values]
-  __shared__ int found[4 * SETS];
+  __shared__ int found[WAVES * SETS];
 
   const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wave = all_waves & 3, set = SETS == 1 ? 0 : all_waves >> 2;
+  const int wave = all_waves % WAVES, set = all_waves / WAVES;
   const int r32 = lane & 31, h = lane >> 5;
   uint32_t x = a.first + blockIdx.x;
   const int kv_head = x % a.heads;
@@ -50,9 +56,9 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
     if (tile.seq < 0) return;
   }
   const Seq s = seq_of(a, tile.seq);
-  const int row0 = tile.tile * kSeqRows;
+  const int row0 = tile.tile * kRows;
   if (row0 >= s.n) return;
-  const int khi = a.causal ? min(s.n, row0 + kSeqRows) : s.n;
+  const int khi = a.causal ? min(s.n, row0 + kRows) : s.n;
   const int klo = a.window ? max(0, row0 - a.window + 1) & ~(kKeys - 1) : 0;
 
   const uint32_t ring0 = lds_addr(ring[set]);
@@ -84,7 +90,7 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
   const int wlo = a.window ? wrow - a.window + 1 : 0;
   // the keys that every row of the workgroup sees
   const int all_hi = a.causal ? min(s.n, row0 + 1) : s.n;
-  const int all_lo = a.window ? min(row0 + kSeqRows, s.n) - a.window : 0;
+  const int all_lo = a.window ? min(row0 + kRows, s.n) - a.window : 0;
 
   v16f o[DT];
 #pragma unroll
@@ -219,9 +225,9 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
     const uint32_t tile = ring0 + buf * 2 * Load::kBytes;
     if (all + SETS * kKeys > all_hi || all < all_lo) {
       const uint32_t values = tile + Load::kBytes;
-      if (has_bad<Load::kBytes, SETS>(values, found, T < khi)) {
+      if (has_bad<Load::kBytes, SETS, WAVES>(values, found, T < khi)) {
         if (T < khi) record(T, values);
-        clear_bad<Load::kBytes>(values, 2 * D, nullptr);
+        clear_bad<Load::kBytes, WAVES>(values, 2 * D, nullptr);
       }
     }
     if (T >= min(whi, khi) || T + kKeys <= wlo) continue;
@@ -231,11 +237,12 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
   }
 
   if constexpr (SETS > 1) {
-    // the second set's rows to LDS, lane by lane; the first set's waves add them
-    static_assert(SETS == 2 && sizeof(ring) >= 4 * 64 * (16 * DT + 2) * 4, "a set's state fits the ring");
-    float* const state = reinterpret_cast<float*>(&ring[0][0][0][0]) + wave * 64 * (16 * DT + 2) + lane;
+    // the other sets' rows to LDS, lane by lane; the first set's waves add them
+    constexpr int kState = 64 * (16 * DT + 2);
+    static_assert(sizeof(ring) >= (SETS - 1) * WAVES * kState * 4, "the sets' state fits the ring");
+    float* state = reinterpret_cast<float*>(&ring[0][0][0][0]) + (all_waves - WAVES) * kState + lane;
     __syncthreads();
-    if (set == 1) {
+    if (set > 0) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -244,15 +251,19 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
       state[64 * (16 * DT + 1)] = l;
     }
     __syncthreads();
-    if (set == 1) return;
-    const float m1 = state[64 * 16 * DT], to = m1 > m ? m1 : m;
-    const float f0 = __builtin_amdgcn_exp2f(m - to), f1 = __builtin_amdgcn_exp2f(m1 - to);
-    m = to;
-    l = l * f0 + state[64 * (16 * DT + 1)] * f1;
+    if (set > 0) return;
+#pragma unroll 1
+    for (int other = 1; other < SETS; ++other) {
+      state += WAVES * kState;
+      const float m1 = state[64 * 16 * DT], to = m1 > m ? m1 : m;
+      const float f0 = __builtin_amdgcn_exp2f(m - to), f1 = __builtin_amdgcn_exp2f(m1 - to);
+      m = to;
+      l = l * f0 + state[64 * (16 * DT + 1)] * f1;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f0 + state[64 * (16 * d + e)] * f1;
+        for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f0 + state[64 * (16 * d + e)] * f1;
+    }
   }
 
   l = swap32_sum(l);
@@ -277,24 +288,45 @@ __global__ __launch_bounds__(256 * SETS, D == 256 ? 1 : 2) void seq_attn_fwd_ker
 hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) {
   a.tiles = (a.max_len + kSeqRows - 1) / kSeqRows;
   a.rest = ragged_places(a.tokens, a.batch, a.tiles);
-  const int64_t groups = (a.rest > 0 ? (int64_t)a.rest + a.batch : (int64_t)a.tiles * a.batch) * a.q_heads;
-  // Two sets where a workgroup has a CU to itself (256 CUs), and where the last
-  // rows of a long causal sequence would go on alone: one of 3000 tokens, 12 heads
-  // of 64, 47 us with one set and 37 with two, of 2048 tokens, 32 heads of 128, 61
-  // and 54.  Elsewhere the sets' joining costs more: two sequences of 1000 tokens,
-  // 32 heads of 64, 22 and 24, of 1500 and 300, 40 heads of 128, 48 and 61.
+  int64_t groups = (a.rest > 0 ? (int64_t)a.rest + a.batch : (int64_t)a.tiles * a.batch) * a.q_heads;
+  // tiles of 128 rows that there may be, of all heads; and whether the last rows of
+  // a sequence walk on when the others are done
   const int64_t busy = std::min(groups, ((int64_t)a.tokens / kSeqRows + a.batch) * a.q_heads);
-  const bool uneven = a.causal && a.window == 0 && a.max_len >= 2048 && busy <= 600;
-  const bool two = (busy <= 256 || uneven) && a.max_len > 64 && head_dim != 256;
+  const bool uneven = a.causal && a.window == 0, long_rows = a.max_len >= 2048;
+  // 64 rows a workgroup where each has a CU to itself (256 CUs); of uneven walks
+  // also where two share one, with heads of 128 only the long ones' (the sets' tiles
+  // are half as large there, and half as many fit a CU).  us with 128 and with 64
+  // rows: causal, 2 x 1024 tokens of 12 heads of 64 17.7 and 15.4, 4000 of 2 of 128
+  // 69 and 47, 4000 of 2 of 256 267 and 157, 2048 of 16 on 4 of 256 145 and 102, 8192
+  // of 4 of 128 139 and 110; but 1024 of 32 of 128 26.8 and 28.6, 8192 of 8 of 64 98
+  // and 100; everything seen, 2048 of 16 on 4 of 256 147 and 172.
+  const int64_t most = !uneven ? 128 : head_dim == 64 ? (long_rows ? 400 : 256) : head_dim == 256 || long_rows ? 256 : 128;
+  const bool half = busy <= most && a.max_len > 64 && a.rest == 0;
+  // 128 rows, two sets: where a workgroup has a CU to itself, and where the last rows
+  // of a long causal sequence would go on alone: one of 8192 tokens, 8 heads of 64,
+  // 98 us with two sets, 2048 of 32 heads of 128 61 us with one set and 54 with two.
+  // Elsewhere the sets' joining costs more: two sequences of 1000 tokens, 32 heads of
+  // 64, 22 and 24, of 1500 and 300, 40 heads of 128, 48 and 61.
+  const bool two = (busy <= 256 || (uneven && long_rows && busy <= 600)) && a.max_len > 64;
+  if (half) {
+    a.tiles = (a.max_len + 63) / 64;
+    groups = (int64_t)a.tiles * a.batch * a.q_heads;
+  }
   auto launch = [&](auto kernel, int threads) {
     in_stretches(groups, threads, [&](uint32_t first, uint32_t count) {
       a.first = first;
       hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, stream, a);
     });
   };
-  if (head_dim == 64) two ? launch(seq_attn_fwd_kernel<64, 2>, 512) : launch(seq_attn_fwd_kernel<64, 1>, 256);
-  else if (head_dim == 128) two ? launch(seq_attn_fwd_kernel<128, 2>, 512) : launch(seq_attn_fwd_kernel<128, 1>, 256);
-  else launch(seq_attn_fwd_kernel<256, 1>, 256);
+  if (head_dim == 64) {
+    if (half) launch(seq_attn_fwd_kernel<64, 2, 4>, 512);
+    else two ? launch(seq_attn_fwd_kernel<64, 4, 2>, 512) : launch(seq_attn_fwd_kernel<64, 4, 1>, 256);
+  } else if (head_dim == 128) {
+    if (half) launch(seq_attn_fwd_kernel<128, 2, 4>, 512);
+    else two ? launch(seq_attn_fwd_kernel<128, 4, 2>, 512) : launch(seq_attn_fwd_kernel<128, 4, 1>, 256);
+  } else {
+    half ? launch(seq_attn_fwd_kernel<256, 2, 2>, 256) : launch(seq_attn_fwd_kernel<256, 4, 1>, 256);
+  }
   return hipGetLastError();
 }
 

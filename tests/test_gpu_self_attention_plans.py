@@ -4,6 +4,7 @@ both, are cut into shares (seq_ref.py has the bounds)."""
 import pytest
 import torch
 
+import seq_ref
 from gpu_util import need_gpu, say
 from test_gpu_self_attention import check, inputs
 from test_gpu_self_attention_edges import both, inside, same
@@ -62,6 +63,23 @@ def test_one_head_of_long_rows(sa, mask):
 def test_long_causal_rows(sa, D):
     """More workgroups than CUs, and the last of them by far the longest."""
     check(sa, [2100, 300], 16, 4, D, seed=3)
+
+
+# workgroups of 64 rows, of 128 with two sets of waves, and with one: by the number
+# of tiles, the mask and the length
+FORWARD = [([300, 65, 1], 4, 2, 64), ([700], 6, 2, 128), ([500, 64], 4, 4, 256), ([1000], 28, 4, 64), ([900], 30, 30, 128),
+           ([700, 600], 20, 5, 256), ([2100], 20, 4, 64), ([2100], 14, 2, 128), ([64, 50], 2, 2, 128)]
+
+
+@pytest.mark.parametrize("shape", FORWARD)
+@pytest.mark.parametrize("mask", [{}, {"window": 33}, {"causal": False}])
+def test_forward(sa, shape, mask):
+    lens, Hq, H, D = shape
+    what = f"{lens} {Hq}/{H} of {D} {mask}"
+    say(what)
+    q, k, v, _ = inputs(lens, Hq, H, D, 13)
+    out, lse = sa.attention_fwd(q, k, v, sa.Sequences.from_lists(lens), **mask)
+    seq_ref.inside({"out": out, "lse": lse}, seq_ref.forward(q, k, v, lens, D ** -0.5, **mask), what)
 
 
 @pytest.mark.parametrize("shape", [WHOLE[0], KEYS_CUT[1], WHOLE[2]])
