@@ -124,12 +124,15 @@ struct Share {
 template <bool ROWS>
 __device__ __forceinline__ Share share_of(const SeqAttnArgs& a, int shares, int j) {
   Share r;
+  // (read before the number of tiles is known: the line has room for all)
+  const SeqLine mine = a.line[min((int)threadIdx.x, a.most_tiles - 1)];
   const int64_t total = scalar(ROWS ? a.line_end->start_q : a.line_end->start);
   r.pos = share_start(total, shares, j);
   r.end = share_start(total, shares, j + 1);
   r.tiles = __builtin_amdgcn_readfirstlane(a.line_end->count);
-  int at = -1;  // the tile that the share begins in: the last that starts at or before it
-  for (int i0 = 0; i0 < r.tiles; i0 += 256) {
+  // the tile that the share begins in: the last that starts at or before it
+  int at = __syncthreads_count((int)threadIdx.x < r.tiles && (ROWS ? mine.start_q : mine.start) <= r.pos) - 1;
+  for (int i0 = 256; i0 < r.tiles; i0 += 256) {
     const int i = i0 + (int)threadIdx.x;
     const SeqLine& l = a.line[min(i, r.tiles - 1)];
     at += __syncthreads_count(i < r.tiles && (ROWS ? l.start_q : l.start) <= r.pos);
@@ -615,10 +618,10 @@ __device__ __forceinline__ void join_group(const SeqAttnArgs& a, uint32_t x) {
   const int nth = x % heads, head = ROWS ? (nth % a.heads) * a.group + nth / a.heads : nth;
   x /= heads;
   const int at = x / kParts, row = (int)(x % kParts) * kRows + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
-  if (at >= a.line_end->count) return;
-  const SeqLine tile = a.line[at];
+  const SeqLine end = *a.line_end, tile = a.line[at];  // (one of `most_tiles`)
+  if (at >= end.count) return;
   const Seq s = {tile.first, tile.n};
-  const int64_t total = ROWS ? a.line_end->start_q : a.line_end->start, start = ROWS ? tile.start_q : tile.start;
+  const int64_t total = ROWS ? end.start_q : end.start, start = ROWS ? tile.start_q : tile.start;
   const int64_t length = ROWS ? keys_of<D>(a, s.n, tile.k0).tiles : (int64_t)walk_of<D>(a, s.n, tile.k0).tiles * a.group;
   // the shares that hold the walk's first and last tile
   const int64_t walk = start + kEntry<D>;
