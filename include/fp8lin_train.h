@@ -7,7 +7,7 @@
  *     their gradients (single tokens in front of the FP8 cache likewise);
  *   - attention over packed sequences, and its gradients.
  * Dtypes, status codes and the conventions for every entry point are
- * fp8lin.h's.
+ * fp8lin.h's.  No output may overlap an input, another output or a workspace.
  */
 #ifndef FP8LIN_TRAIN_H
 #define FP8LIN_TRAIN_H
@@ -37,8 +37,8 @@ extern "C" {
  *              bytes.  The call overwrites it and keeps no pointer; calls in
  *              flight at the same time need separate ones.
  * Tokens are sorted by id, stably, and an id's rows are added in their order
- * in fp32, in runs of at most 16 whose sums are added in their order: same
- * inputs, same bits.  vocab < 2^31, tokens < 2^31 - 2^16.
+ * in fp32, in runs of at most 16 whose sums (of long runs also sums of 64 of
+ * these) are added in their order: same inputs, same bits.  vocab < 2^31, tokens < 2^31 - 2^16.
  */
 int fp8_embedding_fwd(const void* ids, int32_t id_bits, int64_t tokens, const void* table, fp8_dtype_t table_dtype,
                       int64_t vocab, int64_t d, float scale, void* out, fp8_dtype_t out_dtype, void* stream);
@@ -99,8 +99,8 @@ int fp8_qk_norm_rope_bwd(const uint16_t* dq, int64_t dq_stride, const uint16_t* 
  * Sequences packed one behind the other: sequence i is rows cu_tokens[i] ..
  * cu_tokens[i + 1] - 1 of the token tensors.
  *   cu_tokens  device, batch + 1 int32, ascending, at most `tokens`
- *   max_len    at least every sequence's length (a looser bound costs launches
- *              of empty workgroups)
+ *   max_len    at least every sequence's length (a looser bound may cost empty
+ *              workgroups and a worse division of the work)
  * The device array is read by the kernels only.  They stay within the buffers
  * whatever it holds: tokens past max_len or `tokens` do not exist, and rows of
  * outputs that belong to no token of a sequence stay as they are.

@@ -32,7 +32,7 @@ def test_plans(sa, shape, mask):
 # long sequences among many short ones, whose tiles are counted through
 RAGGED = [([20] * 30 + [2100] + [0, 33] * 15, 32, 32, 64), ([1300] + [3] * 600 + [257, 1] * 2, 2, 2, 64),
           ([5] * 20 + [129, 1800, 130] + [1] * 30, 20, 20, 128), ([2, 2000] + [9] * 30, 12, 12, 256),
-          ([3] * 100 + [1500], 4, 2, 128)]
+          ([3] * 100 + [1500], 4, 2, 128), ([1300] + [3] * 600, 2, 1, 64), ([2] * 300 + [900] + [5] * 300, 1, 1, 64)]
 
 
 @pytest.mark.parametrize("shape", RAGGED)
