@@ -36,7 +36,8 @@ from .self_attention import Sequences, attention
 
 class FP8Block(torch.nn.Module):
     """One layer.  qk_norm: norms of queries and keys, with a weight [head_dim]
-    each."""
+    each.  window > 0: a token sees the last `window` positions of its sequence,
+    its own among them."""
 
     def __init__(self, d, f, q_heads, kv_heads, head_dim, eps=1e-5, qk_norm=True, window=0, device=None):
         super().__init__()
@@ -62,14 +63,15 @@ class FP8Block(torch.nn.Module):
 
 
 class FP8Model(torch.nn.Module):
-    """Embedding, layers, and the product that gives logits behind the last norm."""
+    """Embedding, layers (their qk_norm and window: FP8Block), and the product that
+    gives logits behind the last norm."""
 
     def __init__(self, vocab, layers, d, f, q_heads, kv_heads, head_dim, positions, eps=1e-5, qk_norm=True, embed_scale=1.0,
-                 device=None):
+                 device=None, window=0):
         super().__init__()
         from .decoder import rope_tables
         self.embedding = Embedding(vocab, d, scale=embed_scale, device=device)
-        self.layers = torch.nn.ModuleList(FP8Block(d, f, q_heads, kv_heads, head_dim, eps, qk_norm, device=device)
+        self.layers = torch.nn.ModuleList(FP8Block(d, f, q_heads, kv_heads, head_dim, eps, qk_norm, window, device)
                                           for _ in range(layers))
         self.head = FP8NormLinear(d, vocab, eps=eps, device=device)
         self.rope = rope_tables(positions, head_dim, device=device)

@@ -40,17 +40,18 @@ def rope_tables(positions, head_dim, base=10000.0, device="cuda"):
 class FP8DecoderLayer:
     """Weights: wqkv [(q_heads + 2 kv_heads) head_dim, d], wo [d, q_heads
     head_dim], w_gate_up [2f, d], w_down [d, f]; norm weights [d].  q_norm, k_norm
-    [head_dim], both or neither: the norms of queries and keys."""
+    [head_dim], both or neither: the norms of queries and keys.  window > 0: a
+    token sees the last `window` positions, its own among them."""
 
     def __init__(self, norm_attn, wqkv, wo, norm_mlp, w_gate_up, w_down, q_heads, kv_heads, head_dim, eps=1e-5,
-                 q_norm=None, k_norm=None):
+                 q_norm=None, k_norm=None, window=0):
         d = norm_attn.shape[0]
         if wqkv.shape != ((q_heads + 2 * kv_heads) * head_dim, d) or wo.shape != (d, q_heads * head_dim):
             raise ValueError(f"wqkv {tuple(wqkv.shape)} and wo {tuple(wo.shape)} do not fit {q_heads} + 2 * {kv_heads} "
                              f"heads of {head_dim} and d = {d}")
         if w_gate_up.dim() != 2 or w_gate_up.shape[1] != d or w_down.shape != (d, w_gate_up.shape[0] // 2):
             raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not chain")
-        self.q_heads, self.kv_heads, self.head_dim, self.eps = q_heads, kv_heads, head_dim, eps
+        self.q_heads, self.kv_heads, self.head_dim, self.eps, self.window = q_heads, kv_heads, head_dim, eps, window
         self.norm_attn, self.norm_mlp = norm_attn, norm_mlp
         if (q_norm is None) != (k_norm is None):
             raise ValueError("norm weights for both queries and keys, or for neither")
@@ -75,14 +76,15 @@ class FP8DecoderLayer:
         w = lambda t: None if t is None else t.detach()  # noqa: E731
         return cls(w(block.attn_in.norm_weight), w(block.attn_in.weight), w(block.attn_out.weight), w(block.norm_mlp),
                    w(block.mlp.w1), w(block.mlp.w2), block.q_heads, block.kv_heads, block.head_dim, block.eps,
-                   w(block.q_norm), w(block.k_norm))
+                   w(block.q_norm), w(block.k_norm), block.window)
 
     @torch.no_grad()
-    def forward(self, x, residual, cache, batch, rope, window=0, positions=None):
+    def forward(self, x, residual, cache, batch, rope, window=None, positions=None):
         """(x, h) for the next layer; x [tokens, d] float32 or bf16, residual
         [tokens, d] bf16 or None (the first layer: x is the residual stream).
-        positions: batch.positions(), made here if None; a layer with norms of
-        queries and keys asks for it."""
+        window: in place of the layer's own (0: none).  positions:
+        batch.positions(), made here if None; a layer with norms of queries and
+        keys asks for it."""
         T, Hq, H, D = batch.tokens, self.q_heads, self.kv_heads, self.head_dim
         n8, bn, _, h, _ = rmsnorm_quantize(x, self.norm_attn, E4M3, residual=residual, eps=self.eps)
         qkv = scaled_gemm_auto(OP_FWD, n8, E4M3, bn, self.wqkv[0], E4M3, self.wqkv[1]).view(T, Hq + 2 * H, D)
@@ -92,7 +94,7 @@ class FP8DecoderLayer:
             positions = batch.positions() if positions is None else positions
             q, k, v = qk_norm_rope_fwd(qkv, Hq, H, self.q_norm, self.k_norm, self.eps, rope, positions)
             kv_append(cache, batch, k, v)
-        o = kv_attention(cache, batch, q, window=window).view(T, Hq * D)
+        o = kv_attention(cache, batch, q, window=self.window if window is None else window).view(T, Hq * D)
         o8, bo, _ = quantize(o, E4M3)
         a = scaled_gemm_auto(OP_FWD, o8, E4M3, bo, self.wo[0], E4M3, self.wo[1])
         n8, bn, _, h, _ = rmsnorm_quantize(a, self.norm_mlp, E4M3, residual=h, eps=self.eps)
