@@ -26,6 +26,7 @@ and prints the time of a step.
 """
 import torch
 
+from .decoder import need_positions, rope_tables
 from .embedding import Embedding
 from .linear import FP8Linear
 from .mlp import FP8SwiGLUMLP
@@ -54,6 +55,7 @@ class FP8Block(torch.nn.Module):
         (the first layer: x is the residual stream).  rope: (cos, sin) of
         decoder.rope_tables; positions: seqs.positions(), made here if None."""
         T, Hq, H, D = seqs.tokens, self.q_heads, self.kv_heads, self.head_dim
+        need_positions(rope, min(seqs.max_len, T))   # (the bound may be a loose one)
         positions = seqs.positions() if positions is None else positions
         qkv, h = (self.attn_in(x), x) if residual is None else self.attn_in(x, residual)
         q, k, v = qk_norm_rope(qkv.view(T, Hq + 2 * H, D), Hq, H, self.q_norm, self.k_norm, self.eps, rope, positions)
@@ -69,7 +71,6 @@ class FP8Model(torch.nn.Module):
     def __init__(self, vocab, layers, d, f, q_heads, kv_heads, head_dim, positions, eps=1e-5, qk_norm=True, embed_scale=1.0,
                  device=None, window=0):
         super().__init__()
-        from .decoder import rope_tables
         self.embedding = Embedding(vocab, d, scale=embed_scale, device=device)
         self.layers = torch.nn.ModuleList(FP8Block(d, f, q_heads, kv_heads, head_dim, eps, qk_norm, window, device)
                                           for _ in range(layers))

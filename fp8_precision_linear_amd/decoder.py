@@ -37,6 +37,13 @@ def rope_tables(positions, head_dim, base=10000.0, device="cuda"):
     return angle.cos().float(), angle.sin().float()
 
 
+def need_positions(rope, most):
+    """Refuses tables with fewer than `most` positions (the rotation alone would
+    turn every later token as the last)."""
+    if rope is not None and rope[0].shape[0] < most:
+        raise ValueError(f"the rotation's tables hold {rope[0].shape[0]} positions, the sequences up to {most}")
+
+
 class FP8DecoderLayer:
     """Weights: wqkv [(q_heads + 2 kv_heads) head_dim, d], wo [d, q_heads
     head_dim], w_gate_up [2f, d], w_down [d, f]; norm weights [d].  q_norm, k_norm
@@ -86,6 +93,7 @@ class FP8DecoderLayer:
         batch.positions(), made here if None; a layer with norms of queries and
         keys asks for it."""
         T, Hq, H, D = batch.tokens, self.q_heads, self.kv_heads, self.head_dim
+        need_positions(rope, batch.max_len)
         n8, bn, _, h, _ = rmsnorm_quantize(x, self.norm_attn, E4M3, residual=residual, eps=self.eps)
         qkv = scaled_gemm_auto(OP_FWD, n8, E4M3, bn, self.wqkv[0], E4M3, self.wqkv[1]).view(T, Hq + 2 * H, D)
         if self.q_norm is None:
