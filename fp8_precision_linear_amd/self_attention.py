@@ -32,7 +32,9 @@ class Sequences:
     device, sequence i in rows cu_tokens[i] .. cu_tokens[i + 1] - 1.  max_len
     bounds their lengths, `tokens` is the packed tensors' row count (the host's
     numbers: the device array is not read here).  whole: every row belongs to a
-    sequence; otherwise the autograd function clears the rows that may not."""
+    sequence; otherwise the autograd function clears the rows that may not.
+    cu_tokens may be rewritten for other sequences, but not between a pass through
+    the autograd function and its backward pass, which reads it again."""
 
     def __init__(self, cu_tokens, max_len, tokens, whole=False):
         _need_kind(cu_tokens, "cu_tokens", torch.int32)
@@ -183,14 +185,17 @@ class AttentionFunction(torch.autograd.Function):
             out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
             lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
         out, lse = attention_fwd(q, k, v, seqs, scale, causal, window, out, lse)
-        ctx.save_for_backward(q, k, v, out, lse)
+        # held with the rest: rewritten before the backward pass, it is refused
+        # there (what was made in inference mode has no versions to tell by)
+        cu = None if seqs.cu_tokens.is_inference() else seqs.cu_tokens
+        ctx.save_for_backward(q, k, v, out, lse, cu)
         ctx.call = (seqs, scale, causal, window)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, out, lse = ctx.saved_tensors
+        q, k, v, out, lse, _ = ctx.saved_tensors
         new = torch.empty if ctx.call[0].whole else torch.zeros
         grads = [new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
         return (*attention_bwd(_packed(dout), q, k, v, out, lse, *ctx.call, *grads), None, None, None, None)
