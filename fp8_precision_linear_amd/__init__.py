@@ -201,6 +201,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _aligned(t):
+    """t, or a copy that is contiguous and on a 16-byte boundary, as the library
+    takes tensors.  (contiguous() alone leaves a contiguous slice where it is: of a
+    gradient that torch.cat cuts up, of a buffer of all parameters.)"""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _scalar(t, name, dtype, device):
     _need(t, name, dtype, device, numel=1)
 

@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import (E4M3, E5M2, Fp8Error, _check, _dtype_code, _empty, _need_kind, _need_place, _places, _stream, lib)
+from . import (E4M3, E5M2, Fp8Error, _aligned, _check, _dtype_code, _empty, _need_kind, _need_place, _places, _stream, lib)
 
 BLOCK_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128, 256)
@@ -155,6 +155,17 @@ def _head_rows(t, name, tokens, heads, d, device, dtype=None):
     if tokens and (one != 1 or (heads > 1 and head != d)):
         raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
     return row if tokens > 1 else heads * d
+
+
+def _packed(t, most=(1 << 63) - 1):
+    """t, or a copy whose rows the kernels can read: heads side by side, rows that
+    do not overlap and are at most `most` elements apart, on 16-byte boundaries."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        row, head, one = t.stride()
+        n, d = t.shape[1:]
+        if one != 1 or head != d or not n * d <= row <= most or row * t.element_size() % 16 or t.data_ptr() % 16:
+            return _aligned(t)
+    return t
 
 
 def kv_append(cache, batch, k, v, q=None, rope=None, rope_pairs=False, q_out=None, stream=None):

@@ -11,7 +11,7 @@ no token: a row of zeros, and no gradient.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import Fp8Error, _check, _dtype_code, _empty, _need, _need_kind, _need_place, _stream, lib
+from . import Fp8Error, _aligned, _check, _dtype_code, _empty, _need, _need_place, _stream, lib
 
 
 def _ids(ids):
@@ -90,13 +90,13 @@ class EmbeddingFunction(torch.autograd.Function):
         ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.vocab, ctx.scale, ctx.dtype = table.shape[0], scale, table.dtype
-        return embedding_fwd(ids, table.contiguous(), scale, dtype)
+        return embedding_fwd(ids, _aligned(table), scale, dtype)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         ids, = ctx.saved_tensors
-        return None, embedding_bwd(dout.contiguous(), ids, ctx.vocab, ctx.scale).to(ctx.dtype), None, None
+        return None, embedding_bwd(_aligned(dout), ids, ctx.vocab, ctx.scale).to(ctx.dtype), None, None
 
 
 class Embedding(torch.nn.Module):

@@ -12,8 +12,8 @@ values.  Outputs are bf16: queries and keys normed and rotated, values rounded.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import Fp8Error, _check, _dtype_code, _empty, _need, _need_place, _stream, lib
-from .attention import HEAD_DIMS, _head_rows
+from . import Fp8Error, _aligned, _check, _dtype_code, _empty, _need, _need_place, _stream, lib
+from .attention import HEAD_DIMS, _head_rows, _packed
 
 
 def _opt(t):
@@ -133,24 +133,13 @@ def qk_norm_rope_bwd(dq, dk, dv, qkv, wq=None, wk=None, eps=1e-5, rope=None, pos
     return out, dwq, dwk
 
 
-def _packed(t):
-    """t, or a copy whose rows the kernels can read: heads side by side, rows
-    that do not overlap, on 16-byte boundaries."""
-    if isinstance(t, torch.Tensor) and t.dim() == 3:
-        row, head, one = t.stride()
-        n, d = t.shape[1:]
-        if one != 1 or head != d or row < n * d or row * t.element_size() % 16 or t.data_ptr() % 16:
-            return t.contiguous()
-    return t
-
-
 class QKNormRopeFunction(torch.autograd.Function):
     """(q, k, v) of qk_norm_rope_fwd; gradients for qkv and the weights."""
 
     @staticmethod
     def forward(ctx, qkv, wq, wk, q_heads, kv_heads, eps, rope, positions, rope_pairs):
         cos, sin = (None, None) if rope is None else rope
-        qkv, wq, wk = _packed(qkv), *(None if w is None else w.contiguous() for w in (wq, wk))
+        qkv, wq, wk = _packed(qkv), *(None if w is None else _aligned(w) for w in (wq, wk))
         ctx.save_for_backward(qkv, wq, wk, cos, sin, positions)
         ctx.heads, ctx.eps, ctx.rope_pairs = (q_heads, kv_heads), eps, rope_pairs
         return qk_norm_rope_fwd(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs)

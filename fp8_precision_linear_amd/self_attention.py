@@ -16,7 +16,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import Fp8Error, _check, _empty, _need, _need_kind, _need_place, _stream, lib
-from .attention import HEAD_DIMS, _head_rows
+from .attention import HEAD_DIMS, _head_rows, _packed
 
 MAX_STRIDE = 1 << 24   # elements between two rows
 
@@ -179,7 +179,7 @@ class AttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, seqs, scale, causal, window):
-        q, k, v = (_packed(t) for t in (q, k, v))
+        q, k, v = (_packed(t, MAX_STRIDE) for t in (q, k, v))
         out = lse = None
         if not seqs.whole and isinstance(q, torch.Tensor):   # rows of no sequence: zeros
             out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
@@ -198,18 +198,7 @@ class AttentionFunction(torch.autograd.Function):
         q, k, v, out, lse, _ = ctx.saved_tensors
         new = torch.empty if ctx.call[0].whole else torch.zeros
         grads = [new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
-        return (*attention_bwd(_packed(dout), q, k, v, out, lse, *ctx.call, *grads), None, None, None, None)
-
-
-def _packed(t):
-    """t, or a copy whose rows the kernels can read: heads side by side, rows
-    that do not overlap, on 16-byte boundaries."""
-    if isinstance(t, torch.Tensor) and t.dim() == 3:
-        row, head, one = t.stride()
-        n, d = t.shape[1:]
-        if one != 1 or head != d or row % 8 or not n * d <= row <= MAX_STRIDE or t.data_ptr() % 16:
-            return t.contiguous()
-    return t
+        return (*attention_bwd(_packed(dout, MAX_STRIDE), q, k, v, out, lse, *ctx.call, *grads), None, None, None, None)
 
 
 def attention(q, k, v, seqs, scale=None, causal=True, window=0):
