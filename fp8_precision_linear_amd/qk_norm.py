@@ -142,7 +142,9 @@ class QKNormRopeFunction(torch.autograd.Function):
         qkv, wq, wk = _packed(qkv), *(None if w is None else _aligned(w) for w in (wq, wk))
         ctx.save_for_backward(qkv, wq, wk, cos, sin, positions)
         ctx.heads, ctx.eps, ctx.rope_pairs = (q_heads, kv_heads), eps, rope_pairs
-        return qk_norm_rope_fwd(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs)
+        # three tensors to autograd, though they share their rows: outputs that are
+        # views of one may not be changed in place
+        return tuple(t.data for t in qk_norm_rope_fwd(qkv, q_heads, kv_heads, wq, wk, eps, rope, positions, rope_pairs))
 
     @staticmethod
     @once_differentiable
