@@ -77,6 +77,17 @@ class FP8Model(torch.nn.Module):
         self.head = FP8NormLinear(d, vocab, eps=eps, device=device)
         self.rope = rope_tables(positions, head_dim, device=device)
 
+    def _apply(self, fn, *args, **kwargs):
+        super()._apply(fn, *args, **kwargs)
+        # the rotation's tables go where the weights go, and stay float32
+        positions, half = self.rope[0].shape
+        dev = self.embedding.weight.device
+        if self.rope[0].is_meta:   # nothing to move
+            self.rope = rope_tables(positions, 2 * half, device=dev)
+        else:
+            self.rope = tuple(t.to(dev) for t in self.rope)
+        return self
+
     def forward(self, ids, seqs):
         """Logits float32 [tokens, vocab] of the packed sequences' tokens, whose
         ids are [tokens]."""
