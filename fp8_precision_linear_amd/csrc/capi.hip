@@ -166,6 +166,9 @@ int seqs_checks(const fp8_seqs_t* s, int32_t q_heads, int32_t kv_heads, int32_t 
   if (misaligned_word(s->cu_tokens)) return FP8_ERR_ALIGN;
   return FP8_OK;
 }
+// The kernels take it times log2(e), which has to be finite too.
+constexpr float kLog2e = 1.44269504088896340736f;
+bool bad_scale(float scale) { return !std::isfinite(scale * kLog2e); }
 bool seqs_empty(const fp8_seqs_t& s) { return s.batch == 0 || s.tokens == 0 || s.max_len == 0; }
 fp8lin::SeqAttnArgs seq_args(const fp8_seqs_t& s, int32_t q_heads, int32_t kv_heads, float scale, int32_t causal,
                              int32_t window) {
@@ -178,7 +181,7 @@ fp8lin::SeqAttnArgs seq_args(const fp8_seqs_t& s, int32_t q_heads, int32_t kv_he
   a.heads = kv_heads;
   a.group = q_heads / kv_heads;
   a.scale = scale;
-  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.scale_log2 = scale * kLog2e;
   a.causal = causal != 0;
   a.window = window;
   return a;
@@ -745,7 +748,7 @@ int fp8_attention_fwd(const uint16_t* q, int64_t q_stride, const uint16_t* k, in
                       float scale, int32_t causal, int32_t window, uint16_t* out, float* lse, void* stream) {
   int st = seqs_checks(seqs, q_heads, kv_heads, head_dim);
   if (st != FP8_OK) return st;
-  if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
+  if (window < 0 || (window > 0 && !causal) || bad_scale(scale)) return FP8_ERR_SIZE;
   if (seqs_empty(*seqs)) return FP8_OK;
   if ((st = seq_rows_checks(q, q_stride, q_heads, head_dim)) != FP8_OK) return st;
   if ((st = seq_rows_checks(k, k_stride, kv_heads, head_dim)) != FP8_OK) return st;
@@ -777,7 +780,7 @@ int fp8_attention_bwd(const uint16_t* dout, int64_t dout_stride, const uint16_t*
                       int64_t dk_stride, uint16_t* dv, int64_t dv_stride, void* ws, int64_t ws_bytes, void* stream) {
   const int64_t need = fp8_attention_bwd_workspace_bytes(seqs, q_heads, kv_heads, head_dim);
   if (need < 0) return (int)need;
-  if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale)) return FP8_ERR_SIZE;
+  if (window < 0 || (window > 0 && !causal) || bad_scale(scale)) return FP8_ERR_SIZE;
   if (seqs_empty(*seqs)) return FP8_OK;
   int st = FP8_OK;
   const struct { const void* p; int64_t stride; int32_t heads; } rows[] = {

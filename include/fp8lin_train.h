@@ -134,7 +134,8 @@ typedef struct {
  * fp32 until the last rounding, lse's last step 64 bits.  Values whose weighted
  * sums pass fp32's range (from some 2^110 on) are out of range.
  * Row pointers and strides (in bytes) must be multiples of 16.  q_heads: a
- * positive multiple of kv_heads (FP8_ERR_SIZE otherwise).
+ * positive multiple of kv_heads (FP8_ERR_SIZE otherwise), scale: finite, and
+ * times log2(e) too (likewise).
  *
  * fp8_attention_bwd: with p = exp(s - lse), dp_j = sum_d dout_d v_jd and
  * delta = sum_d dout_d out_d,
