@@ -80,8 +80,15 @@ __global__ __launch_bounds__(64 * WAVES * SETS, D == 256 ? 1 : 2) void seq_attn_
   if (row < s.n) {
     const uint16_t* p = a.q + (int64_t)(s.first + row) * a.q_stride + head * D + 8 * h;
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      q[j] = __builtin_bit_cast(v8b, sign_queries(*reinterpret_cast<const uint4*>(p + 16 * j), a.scale));
+    for (int j = 0; j < J; ++j) q[j] = *reinterpret_cast<const v8b*>(p + 16 * j);
+    if (__builtin_expect(a.scale == 0.0f, 0)) {
+      asm volatile("");  // a branch
+#pragma unroll
+      for (int j = 0; j < J; ++j) q[j] = __builtin_bit_cast(v8b, bad_of(q[j]) & 0x7FC07FC0);  // 0 * NaN, 0 * inf
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) q[j] = __builtin_bit_cast(v8b, sign_queries(__builtin_bit_cast(uint4, q[j]), a.scale));
+    }
   }
   const float c_log2 = a.scale == 0.0f ? 1.0f : fabsf(a.scale_log2);
   // the keys of the lane's row, and of any of the wave's
