@@ -129,8 +129,8 @@ typedef struct {
  *            elements apart (slices of one tensor's rows; at most 2^24)
  *   out      device, tokens x q_heads x head_dim bf16 words, written
  *   lse      device, tokens x q_heads floats, written
- * Probabilities are bf16 relative to a running maximum (2^-9 of each, as the
- * values they are multiplied with); logits, sums, maxima and the output are
+ * Probabilities are bf16 relative to a running maximum (at most 2^-8 off
+ * each, as the values they are multiplied with); logits, sums, maxima and the output are
  * fp32 until the last rounding, lse's last step 64 bits.  Values whose weighted
  * sums pass fp32's range (from some 2^110 on) are out of range.
  * Row pointers and strides (in bytes) must be multiples of 16.  q_heads: a
@@ -151,10 +151,11 @@ typedef struct {
  *       time need separate ones.
  * p and ds are rounded to bf16 as operands of the products; everything else is
  * fp32, rounded once at the end, and nothing is added by atomics (same inputs,
- * same bits).  p is as exact as lse lets it be: its relative error is that of
- * exp over lse's rounding, 2^-24 |lse|.  A query whose out, lse or dout is not
- * finite makes dq of its row, and dk and dv of the keys that it sees, NaN;
- * what is not seen has no influence here either.
+ * same bits).  p is as exact as its argument: beside the logits' own sums, s, lse
+ * and their factor log2(e) are rounded to fp32, in all 2^-22 |lse| of p where it
+ * counts; a p below 2^-126 is 0.  A query whose out, lse or dout is not finite
+ * makes dq of its row, and dk and dv of the keys that it sees, NaN; what is not
+ * seen has no influence here either.
  */
 int fp8_attention_fwd(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                       int64_t v_stride, const fp8_seqs_t* seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
