@@ -12,7 +12,9 @@
 // chunk writes the ids that lie whole in it, and leaves the sums of those that
 // reach past its ends in the workspace, which a last kernel adds in order.
 // HBM-bound by the gradient's writing: vocab x d floats, and dout read once (4095
-// tokens, 32000 x 5120: 144 us, of which 113 clear; 2048 tokens, 50257 x 768: 36).
+// tokens, 32000 x 5120: 144 us, of which 111 clear; 2048 tokens, 50257 x 768: 36).
+// Tiles add the later digits' launches, beside which nothing is cleared, and places
+// that few workgroups find (32768 tokens, 32000 x 4096: 270 us, 152 at 5.2 TB/s).
 #include <algorithm>
 
 #include "norm_kernel.h"

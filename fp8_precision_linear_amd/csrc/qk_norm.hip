@@ -5,13 +5,13 @@
 //   dn = R(-pos) dy,  g = dn w,  xhat = x rstd
 //   dx_j = rstd (g_j - xhat_j mean(g xhat)),  dw_j = sum dn_j xhat_j
 //
-// HBM-bound: every element is read once and written once (8192 tokens of 80 heads
-// of 128: 92 us, 5.5 TB/s; gradients of 4095 of 120: 121 us, 5.2 TB/s, and 12 for
-// the weights').  A lane holds a unit of eight dimensions of a head -- four and the
-// four that they rotate with -- so D / 8 lanes hold a head, its sums take
-// log2(D / 8) shuffles, and the rotation none.  A wave takes several steps of 64
-// units of one token: the lane's unit of a head, and with it its weights and angles,
-// are the same in all of them.
+// HBM-bound: every element is read once and written once, x of the values by the
+// forward alone (8192 tokens of 80 heads of 128: 93 us, 5.4 TB/s; gradients of 4095
+// of 120: 122 us, 4.5 TB/s, and 12 for the weights').  A lane holds a unit of eight
+// dimensions of a head -- four and the four that they rotate with -- so D / 8 lanes
+// hold a head, its sums take log2(D / 8) shuffles, and the rotation none.  A wave
+// takes several steps of 64 units of one token: the lane's unit of a head, and with
+// it its weights and angles, are the same in all of them.
 #include <algorithm>
 
 #include "quotient.h"

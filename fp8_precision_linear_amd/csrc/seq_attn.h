@@ -84,7 +84,7 @@ __device__ __forceinline__ Seq seq_of(const SeqAttnArgs& a, int i) {
 // tokens / 128 tiles beside the sequences' first ones, so where that leaves an
 // eighth of the places a sequence's first tile has the place of its number, and the
 // others are counted through in order.  4096 tokens and 1000 sequences of 64, 32
-// heads of 128: forward 1357 -> 854 us, backward 3918 -> 2121; where it leaves a
+// heads of 128: forward 1222 -> 728 us, backward 4083 -> 2116; where it leaves a
 // quarter (1024 tokens and 16 sequences of 100), 36 -> 38 and 93 -> 104.
 inline int ragged_places(int tokens, int batch, int tiles) {
   const int64_t rest = tokens / kSeqRows;

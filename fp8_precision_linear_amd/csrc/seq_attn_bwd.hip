@@ -20,12 +20,13 @@
 // Both kinds run in one launch, behind a small one that leaves -lse log2(e) and
 // -delta of every row and head.
 //
-// Large calls run at the card's power limit: two causal sequences of 3500-4096, 64
-// heads on 8 of 128, 1790-1870 us, 950 TFLOP/s of the seven products (51 us are the
-// first kernel's, at HBM's rate, 29 the join's); two of 4096, 32 heads of 128,
-// everything seen, MFMA busy 48% of the cycles at 1.6 GHz, no bank conflicts.  Heads
-// of 256 hold one wave a SIMD: three of 2000, 16 on 4, 800 us.  Small calls are the
-// launches' latency and the partial sums: 2 x 1024, 12 heads of 64, 45 us.
+// Large calls: two causal sequences of 3500-4096, 64 heads on 8 of 128, 1820-1870 us,
+// 930 TFLOP/s of the seven products (50 us are the first kernel's, at HBM's rate, 29
+// the join's); two of 4096, 32 heads of 128, everything seen, MFMA busy 48% of the
+// SIMDs' cycles and the other vector instructions 30%, with little overlap, at 1.6 GHz
+// (the power limit), no bank conflicts.  Heads of 256 hold one wave a SIMD: three of
+// 2000, 16 on 4, 800 us.  Small calls are the launches' latency and the partial sums:
+// 2 x 1024, 12 heads of 64, 45 us.
 #include <algorithm>
 
 #include "seq_attn.h"

@@ -10,11 +10,12 @@
 // need: two sets of four with every other tile of the keys, or four sets of two
 // waves with 64 rows (two with heads of 256); the sets are joined in LDS at the end.
 //
-// Large calls run at the card's power limit: two sequences of 4096, 32 heads of 128,
-// everything seen, MFMA busy 44% of the cycles at 1.6-1.7 GHz, no bank conflicts;
-// four causal ones 600 us, 920 TFLOP/s.  Heads of 256 hold one wave a SIMD (its
-// output alone takes 128 registers): three causal sequences of 2000, 16 heads on 4,
-// 265 us, 370 TFLOP/s.  Small calls are latency: 2 x 1024, 12 heads of 64, 15 us.
+// Large calls: two sequences of 4096, 32 heads of 128, everything seen, MFMA busy 46%
+// of the SIMDs' cycles and the other vector instructions 39%, with little overlap, at
+// 1.6-1.7 GHz (the power limit), no bank conflicts; four causal ones 610-640 us, 860-900
+// TFLOP/s.  Heads of 256 hold one wave a SIMD (its output alone takes 128 registers):
+// three causal sequences of 2000, 16 heads on 4, 263 us, 370 TFLOP/s.  Small calls
+// are latency: 2 x 1024, 12 heads of 64, 14-16 us.
 #include <algorithm>
 
 #include "seq_attn.h"
@@ -81,6 +82,8 @@ __global__ __launch_bounds__(64 * WAVES * SETS, D == 256 ? 1 : 2) void seq_attn_
     const uint16_t* p = a.q + (int64_t)(s.first + row) * a.q_stride + head * D + 8 * h;
 #pragma unroll
     for (int j = 0; j < J; ++j) q[j] = *reinterpret_cast<const v8b*>(p + 16 * j);
+    // (all on their way before the first is used: 1000 sequences of 64 tokens, 32 heads
+    // of 128, one after the other 616 us, so 464)
     if (__builtin_expect(a.scale == 0.0f, 0)) {
       asm volatile("");  // a branch
 #pragma unroll
@@ -303,17 +306,17 @@ hipError_t launch_seq_attn_fwd(SeqAttnArgs a, int head_dim, hipStream_t stream) 
   // 64 rows a workgroup where each has a CU to itself (256 CUs); of uneven walks
   // also where two share one, with heads of 128 only the long ones' (the sets' tiles
   // are half as large there, and half as many fit a CU).  us with 128 and with 64
-  // rows: causal, 2 x 1024 tokens of 12 heads of 64 17.7 and 15.4, 4000 of 2 of 128
-  // 69 and 47, 4000 of 2 of 256 267 and 157, 2048 of 16 on 4 of 256 145 and 102, 8192
-  // of 4 of 128 139 and 110; but 1024 of 32 of 128 26.8 and 28.6, 8192 of 8 of 64 98
-  // and 100; everything seen, 2048 of 16 on 4 of 256 147 and 172.
+  // rows: causal, 2 x 1024 tokens of 12 heads of 64 17.1 and 13.9, 4000 of 2 of 128
+  // 69 and 48, 4000 of 2 of 256 267 and 161, 2048 of 16 on 4 of 256 146 and 104, 8192
+  // of 4 of 128 139 and 110; but 1024 of 32 of 128 26.6 and 28.1, 8192 of 8 of 64 98
+  // and 100; everything seen, 2048 of 16 on 4 of 256 147 and 176.
   const int64_t most = !uneven ? 128 : head_dim == 64 ? (long_rows ? 400 : 256) : head_dim == 256 || long_rows ? 256 : 128;
   const bool half = busy <= most && a.max_len > 64 && a.rest == 0;
   // 128 rows, two sets: where a workgroup has a CU to itself, and where the last rows
-  // of a long causal sequence would go on alone: one of 8192 tokens, 8 heads of 64,
-  // 98 us with two sets, 2048 of 32 heads of 128 61 us with one set and 54 with two.
+  // of a long causal sequence would go on alone: us with one set and with two, one of
+  // 8192 tokens, 8 heads of 64, 123 and 98, 2048 of 32 heads of 128 59 and 54.
   // Elsewhere the sets' joining costs more: two sequences of 1000 tokens, 32 heads of
-  // 64, 22 and 24, of 1500 and 300, 40 heads of 128, 48 and 61.
+  // 64, 21.5 and 23.1, of 1500 and 300, 40 heads of 128, 47 and 60.
   const bool two = (busy <= 256 || (uneven && long_rows && busy <= 600)) && a.max_len > 64;
   if (half) {
     a.tiles = (a.max_len + 63) / 64;
