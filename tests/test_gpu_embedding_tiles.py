@@ -13,7 +13,7 @@ import pytest
 import torch
 
 from gpu_util import need_gpu, say
-from test_gpu_embedding import TINY, TYPES, make_ids, reference
+from test_gpu_embedding import TINY, TYPES, make_ids
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +23,20 @@ def em():
     need_gpu()
     from fp8_precision_linear_amd import embedding
     return embedding
+
+
+def reference(dout, ids, vocab, scale):
+    """(sum, sum of magnitudes, rows) of each id, float64, added on the host: the
+    device's additions to a few ids wait for one another."""
+    ids, rows = ids.cpu().long(), dout.cpu().double()
+    there = (ids >= 0) & (ids < vocab)
+    at, rows = ids[there], rows[there]
+    out = torch.zeros(vocab, dout.shape[1], dtype=torch.float64)
+    total, count = torch.zeros_like(out), torch.zeros(vocab, dtype=torch.float64)
+    out.index_add_(0, at, rows)
+    total.index_add_(0, at, rows.abs())
+    count.index_add_(0, at, torch.ones(at.shape[0], dtype=torch.float64))
+    return (out * scale).cuda(), (total * abs(scale)).cuda(), count[:, None].cuda()
 
 
 @pytest.mark.parametrize("kind", ["random", "few", "text", "one", "none"])
