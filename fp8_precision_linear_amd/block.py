@@ -81,7 +81,7 @@ class FP8Model(torch.nn.Module):
         super()._apply(fn, *args, **kwargs)
         # the rotation's tables go where the weights go, and stay float32
         positions, half = self.rope[0].shape
-        dev = self.embedding.weight.device
+        dev = fn(self.rope[0]).device
         if self.rope[0].is_meta:   # nothing to move
             self.rope = rope_tables(positions, 2 * half, device=dev)
         else:

@@ -100,6 +100,7 @@ class FP8DecoderLayer:
             q = kv_append(cache, batch, qkv[:, Hq:Hq + H], qkv[:, Hq + H:], q=qkv[:, :Hq], rope=rope)
         else:
             positions = batch.positions() if positions is None else positions
+            # (keys and values reach the cache in bf16: 2^-8 beside the 2^-4 of their codes)
             q, k, v = qk_norm_rope_fwd(qkv, Hq, H, self.q_norm, self.k_norm, self.eps, rope, positions)
             kv_append(cache, batch, k, v)
         o = kv_attention(cache, batch, q, window=self.window if window is None else window).view(T, Hq * D)
