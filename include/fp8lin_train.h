@@ -129,8 +129,8 @@ typedef struct {
  *            elements apart (slices of one tensor's rows; at most 2^24)
  *   out      device, tokens x q_heads x head_dim bf16 words, written
  *   lse      device, tokens x q_heads floats, written
- * Probabilities are bf16 relative to a running maximum (at most 2^-8 off
- * each, as the values they are multiplied with); logits, sums, maxima and the output are
+ * Probabilities are bf16 relative to a running maximum (at most 2^-8 off each, as
+ * the values they are multiplied with); logits, sums, maxima and the output are
  * fp32 until the last rounding, lse's last step 64 bits.  Values whose weighted
  * sums pass fp32's range (from some 2^110 on) are out of range.
  * Row pointers and strides (in bytes) must be multiples of 16.  q_heads: a
